@@ -3,7 +3,7 @@
 Argument marshalling only.  Every function takes torch tensors that live on
 the current CUDA device, derives the extents from them, passes their data
 pointers and sizes to the C-ABI entry point of the same name (see
-include/gbfuse.h) on the current torch stream, and raises GbfError on a
+include/gbfuse.h and include/gbfuse_decode.h) on the current torch stream, and raises GbfError on a
 non-zero status.  A raw pointer carries no size, so before the call each
 wrapper checks what the C library cannot: every operand holds exactly the
 elements the call will read or write (ValueError otherwise), is a contiguous
@@ -53,12 +53,22 @@ _SIGNATURES = {
     "gbf_last_error": [],
     "gbf_version": [],
 }
-for _name, _args in _SIGNATURES.items():
+# the decode-step operators: include/gbfuse_decode.h
+_SIGNATURES_DECODE = {
+    "gbfd_paged_slots": [_p, _p, _i64, _p, _i64, _i64, _i32, _p, _p, _i64, _p, _p, _p, _p, _i64, _p, _p],
+    "gbfd_paged_attention": [_p, _p, _p, _i64, _p, _i64, _i64, _i32, _p, _i64, _i32, _i32, _i32, _f, _i64, _p, _f, _p,
+                             _p, _i64, _p],
+    "gbfd_paged_attention_workspace": [_i32, _i32, _i32],
+    "gbfd_sample_tokens": [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p],
+}
+_RESTYPES = {"gbf_last_error": ctypes.c_char_p, "gbfd_paged_attention_workspace": _i64}
+for _name, _args in {**_SIGNATURES, **_SIGNATURES_DECODE}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
-    _fn.restype = ctypes.c_char_p if _name == "gbf_last_error" else ctypes.c_int
+    _fn.restype = _RESTYPES.get(_name, ctypes.c_int)
 
 EXPORTED = tuple(_SIGNATURES)
+EXPORTED_DECODE = tuple(_SIGNATURES_DECODE)
 
 
 class GbfError(RuntimeError):
@@ -263,6 +273,131 @@ def bn_fold(w, b, gamma, beta, mean, var, eps, w_out, b_out, stream=None):
                                    _ptr(beta, _F32, "beta"), _ptr(mean, _F32, "mean"), _ptr(var, _F32, "var"), eps,
                                    out_ch, inner, _ptr(w_out, _BF16, "w_out"), _ptr(b_out, _BF16, "b_out"),
                                    _stream(stream)))
+
+
+def _table(t, batch, name="block_table"):
+    """(entries per row, row stride) of a block table [batch, max_blocks] whose
+    rows may be apart (a column range of a wider table)."""
+    _numel(t, name)
+    if t.dim() != 2 or t.shape[0] != batch:
+        raise ValueError(f"{name}: expected [{batch}, max_blocks], got {list(t.shape)}")
+    width = t.shape[1]
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the entries of a row must be contiguous")
+    return width, (t.stride(0) if batch > 1 else width)
+
+
+def _place(t, dtype, name, device, dense=True):
+    """Data pointer of a decode operand after _ptr's checks, with the current
+    device looked up once per call (these calls are short); None passes through.
+    dense=False: the caller has checked the strides itself."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    where = t.get_device()
+    if where != device:
+        raise ValueError(f"{name}: must be on a CUDA device" if where < 0 else
+                         f"{name}: is on cuda:{where}, the current device is cuda:{device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _device():
+    """The current CUDA device, -2 without one (no tensor is on it)."""
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+
+def paged_slots(ctx_lens, new_lens, block_table, free_ring, ring, block_size, seq_lens, ring_out, slots, pos,
+                start=None, stream=None):
+    """gbfd_paged_slots: block tables, slot maps and positions of one step from
+    the requests' lengths.  ctx_lens, new_lens, seq_lens [batch]; block_table
+    [batch, max_blocks] (rows may be apart); free_ring [num_blocks]; ring,
+    ring_out [2]; slots, pos [tokens]; start [batch + 1] or None; all int32."""
+    batch = _numel(ctx_lens, "ctx_lens")
+    _extent(new_lens, batch, "new_lens")
+    _extent(seq_lens, batch, "seq_lens")
+    _extent(ring, 2, "ring")
+    _extent(ring_out, 2, "ring_out")
+    tokens = _numel(slots, "slots")
+    _extent(pos, tokens, "pos")
+    _extent(start, batch + 1, "start")
+    width, apart = _table(block_table, batch)
+    blocks = _numel(free_ring, "free_ring")
+    d = _device()
+    return _check(_lib.gbfd_paged_slots(
+        _place(ctx_lens, _I32, "ctx_lens", d), _place(new_lens, _I32, "new_lens", d), batch,
+        _place(block_table, _I32, "block_table", d, False), apart, width, block_size,
+        _place(free_ring, _I32, "free_ring", d), _place(ring, _I32, "ring", d), blocks,
+        _place(seq_lens, _I32, "seq_lens", d), _place(ring_out, _I32, "ring_out", d), _place(slots, _I32, "slots", d),
+        _place(pos, _I32, "pos", d), tokens, _place(start, _I32, "start", d), _stream(stream)))
+
+
+def paged_attention_workspace(n_q_heads, n_kv_heads, head_dim):
+    """Bytes of workspace paged_attention needs with these heads, for any batch."""
+    n = _lib.gbfd_paged_attention_workspace(n_q_heads, n_kv_heads, head_dim)
+    if n <= 0:
+        raise ValueError(f"heads not supported: {n_q_heads} query, {n_kv_heads} KV, head_dim {head_dim}")
+    return n
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, block_size, out, workspace, scale=None, window=0,
+                    lse=None, out_scale=None, stream=None):
+    """gbfd_paged_attention: out[b] = attention of q[b] over the seq_lens[b]
+    cached positions of request b.  q [batch, n_q_heads, head_dim]; k_cache,
+    v_cache [cache_rows, n_kv_heads, head_dim]; block_table [batch, max_blocks]
+    (rows may be apart); out as q in bf16, or uint8 E4M3 codes with out_scale;
+    workspace: any dense tensor of at least paged_attention_workspace() bytes;
+    scale defaults to head_dim ** -0.5."""
+    _numel(q, "q")
+    _numel(k_cache, "k_cache")
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [batch, n_q_heads, head_dim], got {list(q.shape)}")
+    batch, hq, dim = q.shape
+    if k_cache.dim() != 3 or k_cache.shape[2] != dim:
+        raise ValueError(f"k_cache: expected [cache_rows, n_kv_heads, {dim}], got {list(k_cache.shape)}")
+    rows, hkv = k_cache.shape[0], k_cache.shape[1]
+    _extent(v_cache, rows * hkv * dim, "v_cache")
+    _extent(seq_lens, batch, "seq_lens")
+    _extent(out, batch * hq * dim, "out")
+    _extent(lse, batch * hq, "lse")
+    width, apart = _table(block_table, batch)
+    room = _numel(workspace, "workspace") * workspace.element_size()
+    if out_scale is not None and not out_scale > 0.0:
+        raise ValueError(f"out_scale: must be > 0, got {out_scale}")
+    d = _device()
+    return _check(_lib.gbfd_paged_attention(
+        _place(q, _BF16, "q", d), _place(k_cache, _BF16, "k_cache", d), _place(v_cache, _BF16, "v_cache", d), rows,
+        _place(block_table, _I32, "block_table", d, False), apart, width, block_size,
+        _place(seq_lens, _I32, "seq_lens", d), batch, hq, hkv, dim, dim ** -0.5 if scale is None else scale, window,
+        _place(out, _BF16 if out_scale is None else _U8, "out", d), 0.0 if out_scale is None else out_scale,
+        _place(lse, _F32, "lse", d), _place(workspace, workspace.dtype, "workspace", d), room, _stream(stream)))
+
+
+def sample_tokens(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                  stream=None):
+    """gbfd_sample_tokens: tokens[b] drawn from logits[b] (bf16 or float32
+    [batch, vocab], rows may be apart) with the given uniform[b] and, where the
+    tensors are given, temperature, top_k (int32), top_p and min_p of each row."""
+    _numel(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits: expected [batch, vocab] with contiguous rows, got {list(logits.shape)}")
+    batch, vocab = logits.shape
+    for t, name in ((uniform, "uniform"), (tokens, "tokens"), (temperature, "temperature"), (top_k, "top_k"),
+                    (top_p, "top_p"), (min_p, "min_p"), (logprob, "logprob")):
+        _extent(t, batch, name)
+    if logits.dtype not in (_BF16, _F32):
+        raise TypeError(f"logits: expected torch.bfloat16 or torch.float32, got {logits.dtype}")
+    d = _device()
+    return _check(_lib.gbfd_sample_tokens(
+        _place(logits, logits.dtype, "logits", d, False), 1 if logits.dtype == _F32 else 0, batch, vocab,
+        logits.stride(0) if batch > 1 else vocab, _place(uniform, _F32, "uniform", d),
+        _place(temperature, _F32, "temperature", d), _place(top_k, _I32, "top_k", d), _place(top_p, _F32, "top_p", d),
+        _place(min_p, _F32, "min_p", d), _place(tokens, _I32, "tokens", d), _place(logprob, _F32, "logprob", d),
+        _stream(stream)))
 
 
 def copy(src, dst, nbytes=None, stream=None):

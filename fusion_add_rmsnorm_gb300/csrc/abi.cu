@@ -13,7 +13,9 @@
 #include <mutex>
 
 #include "gbfuse.h"
+#include "gbfuse_decode.h"
 #include "common.cuh"
+#include "decode.h"
 #include "kernels.h"
 
 namespace {
@@ -402,6 +404,181 @@ GBF_API int gbf_bn_fold(const void* W, const void* b, const float* gamma, const 
   return launch_status(gbf::launch_bn_fold(a, static_cast<cudaStream_t>(stream)), fn);
 }
 
+// ------------------------------------------------------------ decode step
+
+GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch, int32_t* block_table,
+                             int64_t table_stride, int64_t max_blocks, int block_size, int32_t* free_ring,
+                             const int32_t* ring, int64_t num_blocks, int32_t* seq_lens, int32_t* ring_out,
+                             int32_t* slots, int32_t* pos, int64_t tokens, int32_t* start, void* stream) {
+  const char* fn = "gbfd_paged_slots";
+  const int64_t lim = 1LL << 31;
+  if (batch < 0 || tokens < 0 || block_size <= 0 || max_blocks < 0 || num_blocks <= 0)
+    return fail(GBF_EINVAL, "%s: batch, tokens, max_blocks >= 0 and block_size, num_blocks > 0 are required", fn);
+  if (table_stride < max_blocks) return fail(GBF_EINVAL, "%s: table_stride must be >= max_blocks", fn);
+  if (batch > gbf::kSlotsMaxBatch)
+    return fail(GBF_EUNSUPPORTED, "%s: batch (%lld) > %d", fn, (long long)batch, gbf::kSlotsMaxBatch);
+  if (num_blocks >= lim || num_blocks * block_size >= lim || tokens >= lim || max_blocks >= lim)
+    return fail(GBF_EUNSUPPORTED, "%s: num_blocks * block_size, tokens and max_blocks must be below 2^31", fn);
+  if (batch == 0) return ok();
+  if (!ctx_lens || !new_lens || !free_ring || !ring || !seq_lens || !ring_out || (max_blocks && !block_table) ||
+      (tokens && (!slots || !pos)))
+    return fail(GBF_EINVAL, "%s: every tensor but start is required", fn);
+  const int64_t table_b = max_blocks ? ((batch - 1) * table_stride + max_blocks) * 4 : 0;
+  const void* outs[] = {block_table, free_ring, seq_lens, ring_out, slots, pos, start};
+  const int64_t out_len[] = {table_b, num_blocks * 4, batch * 4, 8, tokens * 4, tokens * 4, start ? (batch + 1) * 4 : 0};
+  const void* ins[] = {ctx_lens, new_lens, ring};
+  const int64_t in_len[] = {batch * 4, batch * 4, 8};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      if (outs[i] == ins[j] && ((i == 2 && j == 0) || (i == 3 && j == 2))) continue;   // exact in-place update
+      if (overlap(outs[i], out_len[i], ins[j], in_len[j])) return fail(GBF_EINVAL, "%s: an output overlaps an input", fn);
+    }
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(outs[i], out_len[i], outs[j], out_len[j])) return fail(GBF_EINVAL, "%s: outputs overlap", fn);
+  }
+  gbf::PagedSlotsArgs a = {};
+  a.ctx = ctx_lens;
+  a.add = new_lens;
+  a.table = block_table;
+  a.free_ring = free_ring;
+  a.ring = ring;
+  a.seq = seq_lens;
+  a.ring_out = ring_out;
+  a.slots = slots;
+  a.pos = pos;
+  a.start = start;
+  a.err = error_word();
+  a.table_stride = table_stride;
+  a.num_blocks = static_cast<int32_t>(num_blocks);
+  a.tokens = static_cast<int32_t>(tokens);
+  a.batch = static_cast<int>(batch);
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.block_size = block_size;
+  return launch_status(gbf::launch_paged_slots(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+namespace {
+
+bool attention_heads_ok(int n_q_heads, int n_kv_heads, int head_dim) {
+  return n_q_heads > 0 && n_kv_heads > 0 && n_q_heads % n_kv_heads == 0 && n_q_heads <= 4096 && head_dim > 0 &&
+         head_dim % 16 == 0 && head_dim <= 256;
+}
+
+}  // namespace
+
+GBF_API int64_t gbfd_paged_attention_workspace(int n_q_heads, int n_kv_heads, int head_dim) {
+  if (!attention_heads_ok(n_q_heads, n_kv_heads, head_dim)) return 0;
+  return gbf::paged_attention_workspace(n_q_heads, n_kv_heads, head_dim);
+}
+
+GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void* v_cache, int64_t cache_rows,
+                                 const int32_t* block_table, int64_t table_stride, int64_t max_blocks,
+                                 int block_size, const int32_t* seq_lens, int64_t batch, int n_q_heads,
+                                 int n_kv_heads, int head_dim, float scale, int64_t window, void* out,
+                                 float out_scale, float* lse, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+  const char* fn = "gbfd_paged_attention";
+  const int64_t lim = 1LL << 31;
+  if (batch < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks < 0 ||
+      cache_rows < 0 || window < 0)
+    return fail(GBF_EINVAL, "%s: batch, max_blocks, cache_rows, window >= 0 and positive heads, head_dim, block_size "
+                "are required", fn);
+  if (n_q_heads % n_kv_heads != 0)
+    return fail(GBF_EINVAL, "%s: n_q_heads (%d) must be a multiple of n_kv_heads (%d)", fn, n_q_heads, n_kv_heads);
+  if (table_stride < max_blocks) return fail(GBF_EINVAL, "%s: table_stride must be >= max_blocks", fn);
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(GBF_EINVAL, "%s: scale must be finite and > 0", fn);
+  if (!(out_scale >= 0.0f) || !std::isfinite(out_scale))
+    return fail(GBF_EINVAL, "%s: out_scale must be finite and >= 0", fn);
+  if (out_scale > 0.0f && !std::isfinite(1.0f / out_scale))
+    return fail(GBF_EINVAL, "%s: out_scale is too small to divide by", fn);
+  if (head_dim % 16 != 0 || head_dim > 256)
+    return fail(GBF_EUNSUPPORTED, "%s: head_dim (%d) must be a multiple of 16 and <= 256", fn, head_dim);
+  if (n_q_heads > 4096) return fail(GBF_EUNSUPPORTED, "%s: too many heads", fn);
+  if (cache_rows >= lim || max_blocks >= lim || batch * n_q_heads >= lim || batch >= lim)
+    return fail(GBF_EUNSUPPORTED, "%s: cache_rows, max_blocks and batch * n_q_heads must be below 2^31", fn);
+  if (batch == 0) return ok();
+  if (!q || !seq_lens || !out || !workspace || (max_blocks && !block_table) || (cache_rows && (!k_cache || !v_cache)))
+    return fail(GBF_EINVAL, "%s: q, k_cache, v_cache, block_table, seq_lens, out and workspace are required", fn);
+  const void* al[] = {q, k_cache, v_cache, out, workspace};
+  for (const void* p : al)
+    if (!aligned16(p)) return fail(GBF_EALIGN, "%s: q, caches, out and workspace must be 16-byte aligned", fn);
+  const int64_t need = gbf::paged_attention_workspace(n_q_heads, n_kv_heads, head_dim);
+  if (workspace_bytes < need)
+    return fail(GBF_EINVAL, "%s: workspace holds %lld bytes, the call needs %lld", fn, (long long)workspace_bytes,
+                (long long)need);
+  const int64_t elems = batch * n_q_heads * head_dim, cache_b = cache_rows * n_kv_heads * head_dim * 2;
+  const void* outs[] = {out, lse, workspace};
+  const int64_t out_len[] = {elems * (out_scale > 0.0f ? 1 : 2), lse ? batch * n_q_heads * 4 : 0, need};
+  const void* ins[] = {q, k_cache, v_cache, block_table, seq_lens};
+  const int64_t in_len[] = {elems * 2, cache_b, cache_b,
+                            max_blocks ? ((batch - 1) * table_stride + max_blocks) * 4 : 0, batch * 4};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i], out_len[i], ins[j], in_len[j])) return fail(GBF_EINVAL, "%s: an output overlaps an input", fn);
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], out_len[i], outs[j], out_len[j])) return fail(GBF_EINVAL, "%s: outputs overlap", fn);
+  }
+  gbf::PagedAttnArgs a = {};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<float*>(workspace);
+  a.err = error_word();
+  a.table_stride = table_stride;
+  a.num_blocks = cache_rows / block_size;
+  a.batch = static_cast<int>(batch);
+  a.hq = n_q_heads;
+  a.hkv = n_kv_heads;
+  a.d = head_dim;
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.block_size = block_size;
+  a.window = static_cast<int>(window < lim ? window : 0);     // longer than any length: the whole length
+  a.out_fp8 = out_scale > 0.0f ? 1 : 0;
+  a.inv_out_scale = out_scale > 0.0f ? 1.0f / out_scale : 0.0f;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  return launch_status(gbf::launch_paged_attention(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+GBF_API int gbfd_sample_tokens(const void* logits, int f32, int64_t batch, int64_t vocab, int64_t logits_stride,
+                               const float* uniform, const float* temperature, const int32_t* top_k,
+                               const float* top_p, const float* min_p, int32_t* tokens, float* logprob,
+                               void* stream) {
+  const char* fn = "gbfd_sample_tokens";
+  if (batch < 0 || vocab <= 0) return fail(GBF_EINVAL, "%s: batch >= 0 and vocab > 0 are required", fn);
+  if (f32 != 0 && f32 != 1) return fail(GBF_EINVAL, "%s: f32 must be 0 or 1", fn);
+  if (logits_stride < vocab) return fail(GBF_EINVAL, "%s: logits_stride must be >= vocab", fn);
+  if (vocab > (1LL << 20)) return fail(GBF_EUNSUPPORTED, "%s: vocab (%lld) > 2^20", fn, (long long)vocab);
+  if (batch >= (1LL << 24)) return fail(GBF_EUNSUPPORTED, "%s: batch must be below 2^24", fn);
+  if (batch == 0) return ok();
+  if (!logits || !uniform || !tokens) return fail(GBF_EINVAL, "%s: logits, uniform and tokens are required", fn);
+  if (!aligned16(logits)) return fail(GBF_EALIGN, "%s: logits must be 16-byte aligned", fn);
+  const int64_t lb = ((batch - 1) * logits_stride + vocab) * (f32 ? 4 : 2), rb = batch * 4;
+  const void* ins[] = {logits, uniform, temperature, top_k, top_p, min_p};
+  for (int j = 0; j < 6; ++j)
+    if (overlap(tokens, rb, ins[j], j ? rb : lb) || overlap(logprob, rb, ins[j], j ? rb : lb))
+      return fail(GBF_EINVAL, "%s: an output overlaps an input", fn);
+  if (overlap(tokens, rb, logprob, rb)) return fail(GBF_EINVAL, "%s: outputs overlap", fn);
+  gbf::SampleArgs a = {};
+  a.logits = logits;
+  a.uniform = uniform;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.tokens = tokens;
+  a.logprob = logprob;
+  a.err = error_word();
+  a.stride = logits_stride;
+  a.batch = batch;
+  a.vocab = static_cast<int>(vocab);
+  a.f32 = f32;
+  return launch_status(gbf::launch_sample_tokens(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
 // ------------------------------------------------------------- copy probe
 
 GBF_API int gbf_copy(const void* src, void* dst, int64_t bytes, void* stream) {
@@ -438,7 +615,9 @@ GBF_API int gbf_device_status(void* stream) {
   if (word & gbf::DEV_ERR_MBAR_TIMEOUT)
     return fail(GBF_ETIMEOUT, "gbf_device_status: a bounded wait inside a kernel gave up (word 0x%x)", word);
   if (word) return fail(GBF_EDEVICE, "gbf_device_status: device fault word 0x%x (bit 0: cache slot out of range; "
-                         "bit 2: a GEMM CTA pair got different TMEM bases)", word);
+                         "bit 2: a GEMM CTA pair got different TMEM bases; bit 3: block id or length out of range; "
+                         "bit 4: block pool exhausted or inconsistent; bit 5: sampling parameter out of range or no "
+                         "candidate)", word);
   return ok();
 }
 

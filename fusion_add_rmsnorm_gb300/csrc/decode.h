@@ -1,0 +1,104 @@
+// Internal interface of the decode-step operators (paged slots, paged
+// attention, sampling) between the C-ABI layer and their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+namespace gbf {
+
+// Lets `Kernel` use `bytes` of dynamic shared memory on the current device;
+// asked once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Further bits of the device error word (bits 0..2 are common.cuh's).
+enum : unsigned int {
+  DEV_ERR_BLOCK_RANGE = 1u << 3,   // a block id outside the cache, or a length outside its block-table row
+  DEV_ERR_BLOCK_POOL = 1u << 4,    // the ring of free blocks ran out, or its state is inconsistent
+  DEV_ERR_SAMPLING = 1u << 5,      // a sampling parameter outside its range, or a row without a candidate
+};
+
+// ---------------------------------------------------------- paged attention
+struct PagedAttnArgs {
+  const void* q;            // bf16 [batch, hq, d]
+  const void* k;            // bf16 [cache_rows, hkv, d]
+  const void* v;
+  const int32_t* table;     // [batch, max_blocks], rows table_stride apart
+  const int32_t* lens;      // [batch]
+  void* out;                // bf16 [batch, hq, d], or E4M3 codes when out_fp8
+  float* lse;               // [batch, hq], nullable
+  float* ws;                // partial results
+  unsigned int* err;
+  int64_t table_stride;
+  int64_t num_blocks;
+  int batch, hq, hkv, d;
+  int max_blocks, block_size;
+  int window;               // 0: the whole length
+  int out_fp8;
+  float scale_log2;         // softmax scale * log2(e)
+  float inv_out_scale;
+  // set by the launcher
+  int block_shift;          // log2(block_size), or -1
+  int group, chunks;        // query heads per KV head; row tiles they are cut into
+  int min_units;            // least token tiles per CTA
+  int ctas;
+};
+
+int64_t paged_attention_workspace(int hq, int hkv, int d);
+cudaError_t launch_paged_attention(PagedAttnArgs a, cudaStream_t stream);
+
+// --------------------------------------------------------------- paged slots
+constexpr int kSlotsMaxBatch = 8192;
+
+struct PagedSlotsArgs {
+  const int32_t* ctx;       // [batch]
+  const int32_t* add;       // [batch]
+  int32_t* table;           // [batch, max_blocks], rows table_stride apart
+  int32_t* free_ring;       // [num_blocks]
+  const int32_t* ring;      // [2] head, count
+  int32_t* seq;             // [batch] (may equal ctx)
+  int32_t* ring_out;        // [2] (may equal ring)
+  int32_t* slots;           // [tokens]
+  int32_t* pos;             // [tokens]
+  int32_t* start;           // [batch + 1], nullable
+  unsigned int* err;
+  int64_t table_stride;
+  int32_t num_blocks, tokens;
+  int batch, max_blocks, block_size;
+};
+
+cudaError_t launch_paged_slots(const PagedSlotsArgs& a, cudaStream_t stream);
+
+// ----------------------------------------------------------------- sampling
+struct SampleArgs {
+  const void* logits;       // [batch, vocab], rows `stride` elements apart
+  const float* uniform;     // [batch]
+  const float* temperature; // [batch], nullable: 1
+  const int32_t* top_k;     // [batch], nullable: off
+  const float* top_p;       // [batch], nullable: off
+  const float* min_p;       // [batch], nullable: off
+  int32_t* tokens;          // [batch]
+  float* logprob;           // [batch], nullable
+  unsigned int* err;
+  int64_t stride;
+  int64_t batch;
+  int vocab;
+  int f32;                  // logits are float32 (else bf16)
+};
+
+cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t stream);
+
+}  // namespace gbf

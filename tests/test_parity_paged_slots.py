@@ -1,0 +1,177 @@
+"""gbfd_paged_slots against the oracle's request-by-request allocation: every
+output equal, entries it has no business with unchanged."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decode
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gbf():
+    import fusion_add_rmsnorm_gb300 as g
+    assert g.device_status()[0] == g.OK
+    return g
+
+
+def case(rng, batch, block, longest, prompts=0, ended=0, spare=5, head=None, extra_width=2):
+    """A pool in use: scattered blocks in the table, the rest free in a ring that has gone round."""
+    ctx = rng.integers(0, longest + 1, batch)
+    new = np.where(rng.random(batch) < 0.1, 0, 1)
+    who = rng.permutation(batch)
+    new[who[:prompts]] = rng.integers(1, 3 * longest + 2, min(prompts, batch))
+    new[who[prompts:prompts + ended]] = -1 - rng.integers(0, 3, len(who[prompts:prompts + ended]))
+    have = -(-ctx // block)
+    need = -(-(ctx + np.maximum(new, 0)) // block) - have
+    blocks = max(1, int(have.sum() + need.sum()) + spare)
+    order = rng.permutation(blocks)
+    width = int((-(-(ctx + np.maximum(new, 0)) // block)).max()) + extra_width
+    table = np.full((batch, width), -3, np.int32)
+    at = 0
+    for b in range(batch):
+        table[b, :have[b]] = order[at:at + have[b]]
+        at += have[b]
+    head = int(rng.integers(0, blocks)) if head is None else head
+    free = np.full(blocks, -4, np.int32)
+    free[(head + np.arange(blocks - at)) % blocks] = order[at:]
+    return dict(ctx=ctx.astype(np.int32), new=new.astype(np.int32), table=table, free=free,
+                ring=np.array([head, blocks - at], np.int32), block=block,
+                tokens=int(np.maximum(new, 0).sum()))
+
+
+def run(gbf, c, pad=3, in_place=False, start=True, apart=0, tokens=None):
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()      # noqa: E731
+    n, batch = (c["tokens"] if tokens is None else tokens) + pad, c["ctx"].size
+    wide = torch.full((batch, c["table"].shape[1] + apart), -8, dtype=torch.int32, device="cuda")
+    table = wide[:, apart // 2:apart // 2 + c["table"].shape[1]]
+    table.copy_(d(c["table"]))
+    ctx, new, free, ring = d(c["ctx"]), d(c["new"]), d(c["free"]), d(c["ring"])
+    full = lambda m: torch.full((m,), -9, dtype=torch.int32, device="cuda")           # noqa: E731
+    seq, ring_out = (ctx, ring) if in_place else (full(batch), full(2))
+    slots, pos, st = full(n), full(n), full(batch + 1) if start else None
+    gbf.paged_slots(ctx, new, table, free, ring, c["block"], seq, ring_out, slots, pos, st)
+    torch.cuda.synchronize()
+    out = dict(table=table, free=free, ring=ring_out, seq=seq, slots=slots, pos=pos, start=st, wide=wide)
+    return {k: None if v is None else v.cpu().numpy() for k, v in out.items()}
+
+
+def check(c, got, pad=3, apart=0):
+    p, seq, slots, pos, start, refused = decode.paged_slots(c["ctx"], c["new"], c["table"], c["free"], c["ring"],
+                                                            c["block"])
+    assert np.array_equal(got["table"], p.table)
+    assert np.array_equal(got["free"], p.free_ring) and got["ring"].tolist() == [p.head, p.count]
+    assert np.array_equal(got["seq"], seq)
+    n = got["slots"].size - pad
+    assert np.array_equal(got["slots"][:n], slots[:n]) and np.array_equal(got["pos"][:n], pos[:n])
+    assert (got["slots"][n:] == -9).all() and (got["pos"][n:] == -9).all()
+    if got["start"] is not None:
+        assert np.array_equal(got["start"], start)
+    if apart:
+        assert (got["wide"][:, :apart // 2] == -8).all() and (got["wide"][:, apart // 2 + c["table"].shape[1]:] == -8).all()
+    return refused
+
+
+@pytest.mark.parametrize("block", [1, 7, 16, 64])
+@pytest.mark.parametrize("batch,longest,prompts,ended", [(1, 0, 1, 0), (1, 100, 0, 1), (5, 40, 2, 1), (33, 300, 5, 4),
+                                                         (257, 90, 40, 30), (1500, 60, 20, 100), (8192, 20, 10, 50)])
+def test_steps(gbf, block, batch, longest, prompts, ended):
+    c = case(np.random.default_rng(batch + block), batch, block, longest, prompts, ended)
+    check(c, run(gbf, c))
+    assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("tokens_each", [3, 3000])
+def test_in_place_and_tables_apart(gbf, tokens_each):
+    """seq_lens on ctx_lens and ring_out on ring, small (one CTA) and large (a cluster)."""
+    rng = np.random.default_rng(tokens_each)
+    c = case(rng, 40, 16, tokens_each, prompts=20, ended=5)
+    check(c, run(gbf, c, in_place=True, apart=10), apart=10)
+    check(c, run(gbf, c, start=False))
+
+
+def test_a_repeated_call_writes_the_same(gbf):
+    c = case(np.random.default_rng(1), 50, 16, 200, prompts=5, ended=5)
+    first = run(gbf, c)
+    again = run(gbf, {**c, "table": first["table"], "free": first["free"]})
+    for k in ("table", "free", "ring", "seq", "slots", "pos", "start"):
+        assert np.array_equal(first[k], again[k]), k
+
+
+@pytest.mark.parametrize("prompts", [0, 12])
+def test_pool_runs_out(gbf, prompts):
+    """The requests behind the last free block are refused, the others served."""
+    rng = np.random.default_rng(2 + prompts)
+    c = case(rng, 60, 4, 50, prompts=prompts, ended=6, spare=0)
+    short = max(1, int(c["ring"][1]) // 2)
+    keep = int(c["ring"][1]) - short
+    gone = (c["ring"][0] + np.arange(keep, c["ring"][1])) % c["free"].size
+    c["free"][gone] = -4
+    c["ring"][1] = keep
+    got = run(gbf, c)
+    refused = check(c, got)
+    assert refused.any() and not refused.all()
+    s, msg = gbf.device_status()
+    assert s == gbf.EDEVICE and "pool" in msg
+    # no block is in two places
+    served = got["seq"]
+    used = np.concatenate([got["table"][b, :-(-served[b] // 4)] for b in range(60)])
+    assert np.unique(used).size == used.size
+
+
+def test_rows_too_short_and_bad_lengths(gbf):
+    c = case(np.random.default_rng(3), 20, 16, 200, prompts=3, extra_width=0)
+    c["new"][4] = 10 ** 6
+    c["tokens"] = int(np.maximum(c["new"], 0).sum())
+    got = run(gbf, c)
+    assert check(c, got)[4]
+    assert gbf.device_status()[0] == gbf.EDEVICE
+    c = case(np.random.default_rng(4), 20, 16, 200)
+    c["ctx"][7] = -1
+    assert check(c, run(gbf, c))[7]
+    assert gbf.device_status()[0] == gbf.EDEVICE
+
+
+def test_more_tokens_than_rows(gbf):
+    c = case(np.random.default_rng(5), 20, 16, 100, prompts=4)
+    got = run(gbf, c, pad=0, tokens=c["tokens"] - 7)
+    check(c, got, pad=0)
+    assert gbf.device_status()[0] == gbf.EDEVICE
+
+
+def test_bad_ids_and_ring_states(gbf):
+    c = case(np.random.default_rng(6), 8, 16, 200, head=3)
+    c["ctx"][:], c["new"][:] = 20, 1
+    c = {**c, "ctx": np.full(8, 20, np.int32), "new": np.ones(8, np.int32), "tokens": 8}
+    c["table"][:, 1] = np.arange(8)
+    c["table"][2, 1] = 1 << 20
+    got = run(gbf, c)
+    assert got["slots"][2] == -1 and (got["slots"][[0, 1, 3, 4, 5, 6, 7]] >= 0).all()
+    assert gbf.device_status()[0] == gbf.EDEVICE
+    for ring in ([-1, 2], [c["free"].size, 2], [0, -2], [0, c["free"].size + 1]):
+        run(gbf, {**c, "ring": np.array(ring, np.int32)})
+        s, msg = gbf.device_status()
+        assert s == gbf.EDEVICE and "pool" in msg
+
+
+def test_graph_follows_the_lengths(gbf):
+    """A captured step, replayed three times in place, walks the requests on."""
+    rng = np.random.default_rng(8)
+    c = case(rng, 10, 4, 30, spare=200, extra_width=20)
+    c["new"][:] = 1
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()      # noqa: E731
+    ctx, new, table, free, ring = (d(c[k]) for k in ("ctx", "new", "table", "free", "ring"))
+    slots, pos = (torch.zeros(10, dtype=torch.int32, device="cuda") for _ in range(2))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gbf.paged_slots(ctx, new, table, free, ring, 4, ctx, ring, slots, pos)
+    want = dict(c)
+    for _ in range(6):
+        g.replay()
+        torch.cuda.synchronize()
+        p, seq, s, q, _, _ = decode.paged_slots(want["ctx"], want["new"], want["table"], want["free"], want["ring"], 4)
+        assert np.array_equal(slots.cpu().numpy(), s) and np.array_equal(pos.cpu().numpy(), q)
+        want = {**want, "ctx": seq, "table": p.table, "free": p.free_ring, "ring": [p.head, p.count]}
+    assert np.array_equal(ctx.cpu().numpy(), want["ctx"]) and ring.cpu().numpy().tolist() == want["ring"]
+    assert gbf.device_status()[0] == gbf.OK

@@ -1,0 +1,233 @@
+"""gbfd_sample_tokens against the float64 oracle: the same token, always, and
+its log-probability.
+
+The kernel's weights are within 2^-37 of their value or half a unit of 2^-43 of
+the largest, and its sums are exact, so a running mass is within
+d = 2^-37 + vocab 2^-44 / total of itself (total: the kept mass, the largest weight
+as 1): a row whose smallest margin (distance of a running mass from a bound it is
+compared with) is below 4 d may fall either way and is left out.  A bound that
+is uniform over the mass comes that near one of vocab sums with a chance of
+8 d vocab at most, below 1 in 100 for 151936 and total >= 4; one row in eight may be.
+logprob = (l - top) / T - ln(mass): two float32 terms, each off by at most a few
+half steps 2^-24 of its size."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decode, formats
+from parity import from_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gbf():
+    import fusion_add_rmsnorm_gb300 as g
+    assert g.device_status()[0] == g.OK
+    return g
+
+
+def logits(rng, batch, vocab, f32, std=2.5):
+    l = (rng.standard_normal((batch, vocab)) * std).astype(np.float32)
+    strong = rng.integers(0, vocab, (batch, 8))
+    np.put_along_axis(l, strong, (rng.random((batch, 8)) * 8 + 2).astype(np.float32), 1)
+    if f32:
+        return l
+    return torch.from_numpy(l).to(torch.bfloat16).float().numpy()
+
+
+def run(gbf, l, u, f32, temperature=None, top_k=None, top_p=None, min_p=None, stride=None, logprob=True):
+    batch, vocab = l.shape
+    t = torch.from_numpy(np.ascontiguousarray(l, np.float32)).cuda()
+    t = t if f32 else t.to(torch.bfloat16)
+    if stride:
+        wide = torch.full((batch, stride), float("inf"), dtype=t.dtype, device="cuda")    # beside the rows: never read as theirs
+        wide[:, :vocab] = t
+        t = wide[:, :vocab]
+    f = lambda a, ty: None if a is None else torch.from_numpy(np.asarray(a, ty)).cuda()            # noqa: E731
+    tokens = torch.full((batch,), -7, dtype=torch.int32, device="cuda")
+    lp = torch.full((batch,), 9.0, device="cuda") if logprob else None
+    gbf.sample_tokens(t, f(u, np.float32), tokens, temperature=f(temperature, np.float32), top_k=f(top_k, np.int32),
+                      top_p=f(top_p, np.float32), min_p=f(min_p, np.float32), logprob=lp)
+    torch.cuda.synchronize()
+    return tokens.cpu().numpy(), None if lp is None else lp.cpu().numpy()
+
+
+def check(l, u, got, temperature=None, top_k=None, top_p=None, min_p=None, skip=0):
+    tokens, lps = got
+    batch, vocab = l.shape
+    at = lambda a, b, other, ty: other if a is None else ty(np.asarray(a, ty)[b])                 # noqa: E731
+    skipped = 0
+    for b in range(batch):
+        t = at(temperature, b, 1.0, np.float32)
+        token, lp, margin, total = decode.sample_row(l[b], np.float32(u[b]), float(t), int(at(top_k, b, 0, np.int32)),
+                                                     float(at(top_p, b, 1.0, np.float32)),
+                                                     float(at(min_p, b, 0.0, np.float32)))
+        near = 4 * (2.0 ** -37 + vocab * 2.0 ** -44 / max(total, 1.0))
+        if margin < near:
+            skipped += 1
+            continue
+        assert tokens[b] == token, f"row {b}: {tokens[b]}, the oracle says {token} (margin {margin:.1e})"
+        if lps is not None:
+            if np.isnan(lp):
+                assert np.isnan(lps[b])
+            else:
+                assert abs(lps[b] - lp) <= 8 * 2.0 ** -24 * (abs(lp) + 1e-3) + near, (b, lps[b], lp)
+    assert skipped <= max(skip, batch // 8), f"{skipped} rows with margins too small to compare"
+
+
+def params(rng, batch):
+    kind = np.arange(batch) % 8
+    return dict(temperature=np.where(kind == 1, 0, 0.4 + rng.random(batch)).astype(np.float32),
+                top_k=np.where((kind >= 2) & (kind <= 4), rng.integers(1, 100, batch), 0).astype(np.int32),
+                top_p=np.where((kind == 3) | (kind == 5) | (kind == 7), 0.3 + 0.69 * rng.random(batch), 1).astype(np.float32),
+                min_p=np.where((kind == 4) | (kind == 6) | (kind == 7), 0.3 * rng.random(batch), 0).astype(np.float32))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("batch,vocab", [(1, 1), (3, 2), (9, 7), (16, 8), (16, 63), (24, 1000), (40, 4099), (16, 32000),
+                                         (16, 50257), (16, 151936)])
+def test_mixed_parameters(gbf, batch, vocab, f32):
+    rng = np.random.default_rng(batch * vocab + f32)
+    l, u, p = logits(rng, batch, vocab, f32), rng.random(batch).astype(np.float32), params(rng, batch)
+    check(l, u, run(gbf, l, u, f32, **p), **p)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_defaults_and_no_logprob(gbf, f32):
+    rng = np.random.default_rng(5)
+    l, u = logits(rng, 12, 5001, f32), rng.random(12).astype(np.float32)
+    check(l, u, run(gbf, l, u, f32))
+    check(l, u, run(gbf, l, u, f32, logprob=False))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("vocab,stride", [(1000, 1001), (1001, 1003), (1001, 4096), (17, 18)])
+def test_row_strides(gbf, vocab, stride, f32):
+    """Rows that begin at any element offset; what lies between them is +inf."""
+    rng = np.random.default_rng(stride)
+    l, u, p = logits(rng, 19, vocab, f32), rng.random(19).astype(np.float32), params(rng, 19)
+    check(l, u, run(gbf, l, u, f32, stride=stride, **p), **p)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("kind", ["equal", "two", "few", "ramp"])
+def test_ties(gbf, kind, f32):
+    """Logits with very few values: the borders of top-k and top-p fall inside runs
+    of thousands of equals and are drawn by index."""
+    rng = np.random.default_rng(11)
+    batch, vocab = 16, 20011
+    l = {"equal": np.full((batch, vocab), 1.5), "two": rng.integers(0, 2, (batch, vocab)) * 3.0,
+         "few": rng.integers(0, 5, (batch, vocab)) * 0.5, "ramp": np.tile(np.arange(vocab) // 64 / 64.0, (batch, 1))}[kind]
+    l = l.astype(np.float32)
+    if not f32:
+        l = torch.from_numpy(l).to(torch.bfloat16).float().numpy()
+    u = rng.random(batch).astype(np.float32)
+    k = rng.integers(1, vocab, batch).astype(np.int32)
+    p = (0.05 + 0.9 * rng.random(batch)).astype(np.float32)
+    for q in (dict(top_k=k), dict(top_p=p), dict(top_k=k, top_p=p), dict(top_k=np.ones(batch)),
+              dict(top_k=np.full(batch, vocab)), dict(top_k=np.full(batch, vocab - 1)), dict(min_p=np.ones(batch))):
+        check(l, u, run(gbf, l, u, f32, **q), **q)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_masked_infinite_and_nan_logits(gbf, f32):
+    rng = np.random.default_rng(12)
+    l = logits(rng, 10, 3001, f32)
+    l[0, 100:] = -np.inf
+    l[1] = -np.inf
+    l[1, 1234] = -50.0
+    l[2] = -np.inf                         # nothing to draw
+    l[3, ::3] = np.nan
+    l[4] = np.nan
+    l[5, [7, 2000, 2999]] = np.inf         # the only weights
+    l[6] = np.finfo(np.float32).min if f32 else -3.3895313892515355e38
+    l[7] = -np.inf
+    l[7, -1] = 3.0
+    l[8] = 0.0
+    l[8, ::2] = -0.0                       # equal to +0
+    u = rng.random(10).astype(np.float32)
+    for q in (dict(), dict(top_k=np.full(10, 2)), dict(top_p=np.full(10, 0.7)), dict(min_p=np.full(10, 0.5)),
+              dict(temperature=np.zeros(10)), dict(top_k=np.full(10, 500), top_p=np.full(10, 0.5))):
+        got = run(gbf, l, u, f32, **q)
+        check(l, u, got, **q)
+        assert got[0][2] == -1 and got[0][4] == -1 and np.isnan(got[1][[2, 4]]).all()
+        s, msg = gbf.device_status()
+        assert s == gbf.EDEVICE and "candidate" in msg
+    assert gbf.device_status()[0] == gbf.OK
+
+
+def test_extreme_parameters(gbf):
+    rng = np.random.default_rng(13)
+    l, u = logits(rng, 8, 2000, True), np.array([0, 2.0 ** -30, 0.5, 1 - 2.0 ** -24, 0, 1 - 2.0 ** -24, 0.3, 0.6], np.float32)
+    for q in (dict(temperature=np.full(8, 1e-30)), dict(temperature=np.full(8, 1e-45)), dict(temperature=np.full(8, 1e30)),
+              dict(top_p=np.zeros(8)), dict(top_p=np.full(8, -1.0)), dict(top_p=np.full(8, 1e-30)),
+              dict(top_p=np.full(8, 1 - 2.0 ** -24)), dict(top_k=np.full(8, -5)), dict(top_k=np.full(8, 2 ** 31 - 1)),
+              dict(min_p=np.full(8, 1e-30)), dict(min_p=np.full(8, -1.0)), dict(top_p=np.full(8, np.inf))):
+        check(l, u, run(gbf, l, u, True, **q), **q, skip=8 if "temperature" in q and q["temperature"][0] > 1 else 4)
+    assert gbf.device_status()[0] == gbf.OK
+
+
+def test_parameters_out_of_range_are_reported(gbf):
+    rng = np.random.default_rng(14)
+    l, u = logits(rng, 4, 500, False), np.full(4, 0.5, np.float32)
+    nan, inf = np.nan, np.inf
+    for q in (dict(temperature=[-1.0, 1, 1, 1]), dict(temperature=[nan, 1, 1, 1]), dict(temperature=[inf, 1, 1, 1]),
+              dict(top_p=[nan, 1, 1, 1]), dict(min_p=[nan, 0, 0, 0]), dict(min_p=[1.5, 0, 0, 0])):
+        got = run(gbf, l, u, False, **q)
+        assert got[0][0] == -1 and np.isnan(got[1][0])
+        check(l, u, got, **q)
+        assert gbf.device_status()[0] == gbf.EDEVICE
+    for x in (1.0, -0.1, nan):
+        u[1] = x
+        got = run(gbf, l, u, False)
+        assert got[0][1] == -1 and (got[0][[0, 2, 3]] >= 0).all()
+        assert gbf.device_status()[0] == gbf.EDEVICE
+
+
+def test_frequencies(gbf):
+    """An even grid of uniforms draws each kept token in proportion to its weight."""
+    rng = np.random.default_rng(15)
+    n = 4096
+    row = rng.standard_normal(300).astype(np.float32) * 2
+    l = np.tile(row, (n, 1))
+    u = ((np.arange(n) + 0.5) / n).astype(np.float32)
+    tokens, _ = run(gbf, l, u, True, temperature=np.full(n, 0.8), top_k=np.full(n, 40))
+    w = np.exp(row.astype(np.float64) / np.float32(0.8))
+    w[np.argsort(-row, kind="stable")[40:]] = 0
+    got = np.bincount(tokens, minlength=300)
+    assert np.abs(got - n * w / w.sum()).max() <= 1.0 + 1e-3      # an interval of length x holds x n or one more or less
+
+
+@pytest.mark.parametrize("f32,vocab", [(True, 262144), (False, 262147), (True, 1 << 20), (False, 1 << 20)])
+def test_large_vocabularies(gbf, f32, vocab):
+    """Up to the largest vocabulary: slices that do not fit in shared memory."""
+    rng = np.random.default_rng(vocab)
+    l, u, p = logits(rng, 8, vocab, f32), rng.random(8).astype(np.float32), params(rng, 8)
+    check(l, u, run(gbf, l, u, f32, **p), **p)
+
+
+def test_repeats_graph_and_streams(gbf):
+    rng = np.random.default_rng(16)
+    l = torch.from_numpy(logits(rng, 64, 30011, False)).cuda().bfloat16()
+    u = torch.from_numpy(rng.random(64).astype(np.float32)).cuda()
+    p = torch.full((64,), 0.9, device="cuda")
+    outs = [torch.full((64,), -9, dtype=torch.int32, device="cuda") for _ in range(4)]
+    gbf.sample_tokens(l, u, outs[0], top_p=p)
+    torch.cuda.synchronize()
+    for i in (1, 2):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(4):
+                gbf.sample_tokens(l, u, outs[i], top_p=p)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gbf.sample_tokens(l, u, outs[3], top_p=p)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    u.copy_(torch.rand(64, device="cuda"))                    # new numbers: the graph reads them
+    g.replay()
+    gbf.sample_tokens(l, u, outs[0], top_p=p)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[3], outs[0])
