@@ -9,8 +9,9 @@
 
 namespace gbf {
 
-// Lets `Kernel` use `bytes` of dynamic shared memory on the current device;
-// asked once per device.
+// Lets `Kernel` use `bytes` of dynamic shared memory on the current device, and
+// asks for the largest shared-memory share of the L1 (the default one holds a
+// single CTA of these kernels); done once per device.
 template <auto Kernel>
 cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> done{0};
@@ -20,6 +21,8 @@ cudaError_t allow_smem(int bytes) {
   const uint64_t bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

@@ -11,20 +11,42 @@
 // Exactness.  The answer is an integer that jumps where a running sum passes a
 // bound, and with 10^5 candidates of 10^-5 each a float32 sum would put one
 // row in a hundred on the wrong side.  Weights are therefore 43-bit fixed-point
-// integers (2^43 for the largest), computed to 2^-37 or better in pairs of
+// integers (2^43 for the largest), computed to 2^-36 or better in pairs of
 // float32, and every sum is a 64-bit integer sum: exact, so equal in any order
 // and on any number of CTAs.  Float64 would do the same at about a fiftieth of
 // the rate on this part.
 //
 // Work split: a row is one cluster of 1, 2, 4 or 8 CTAs, each with a
-// contiguous slice.  The logits are read from HBM once; a slice that fits is
-// kept in shared memory for the later passes, a larger one is read again from
-// L2.  Top-k and top-p look for the border element of the sorted order without
-// sorting: a histogram over 2048 bins of (max - l) / T (counts and masses)
-// gives the bin it lies in, the bin's few elements are gathered and ranked by
-// comparison, and a bin with too many of them (equal or almost equal logits)
-// is cut further by (logit, index) until they are few.  Rows that ask for
-// neither skip this.
+// contiguous slice, and within it each warp with a contiguous run.  The logits
+// are read from HBM once; a slice that fits is kept in shared memory for the
+// later passes, a larger one is read again from L2.
+//
+// The border of top-k and top-p in the sorted order is found without sorting:
+//   1. a histogram of counts over 4096 bins of (max - l) / T, 1/128 octave of
+//      weight each (one shared atomic per element);
+//   2. top-k: the bin the k-th element lies in.  Top-p: the histogram also sums
+//      the elements' places in their bins, which gives each bin's mass to 50
+//      ppm and so the few bins the border can lie in; one pass over the weights
+//      then gives the total, the mass above those bins, and the masses within
+//      them;
+//   3. the border bin's few elements are gathered on one CTA and ranked by
+//      comparison; a bin with too many of them (equal or almost equal logits)
+//      is first cut by (logit, index).
+// The pass of step 2 also sums each warp's run of the kept elements above the
+// border's bins, so the draw only adds the few within them.  A row that asks for
+// neither top-k nor top-p takes that pass alone.
+//
+// The exact weight is the dear part (some 45 integer instructions, which run at
+// half rate), so a long slice is first done in float32 with an error bound: the
+// weight to 2^-23 in float32 arithmetic alone, compensated sums, and every
+// decision checked against twice that bound.  A row in which all decisions
+// clear it is done; the others (a few in a hundred with nuclei of 10^4 tokens)
+// are done again exactly.
+//
+// Ranks hand each other totals by remote stores into boxes (read locally behind
+// the next barrier).
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -35,15 +57,25 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+typedef unsigned long long u64;
+
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr float kBinsPerOctave = 64.0f;     // 32 octaves; what is smaller shares the last bin
+constexpr int kBins = 4096;
+constexpr float kBinsPerOctave = 128.0f;    // 32 octaves; what is smaller shares the last bin
+constexpr int kCells = kBins / 2;           // mass histogram in the same memory: low words, then high words
+// With top-p alone an element adds 2^20 and its place in the bin, so that a bin's mass is known to 2^(1/16384) + 4e-6
+// (46 ppm), as long as no more than 4095 elements of a CTA fall in it (otherwise the border turns out to lie outside the
+// bins searched, and all are).  Those of the last bin (weights below 2^-31.9) add vocab 2^-31.9 of the total at most.
+constexpr float kBinError = 60e-6f, kLastBinError = 2.6e-10f;
 constexpr int kList = 512;                  // candidates ranked by comparison
+constexpr int kGroup = 64;                  // bins per group (and groups): the two steps of a search over the bins
+constexpr int kNear = 1024;                 // this rank's elements in the bins that may hold top-p's border
+constexpr int kFilterVectors = 512;         // slices of more 16-byte vectors are first done in float32
+constexpr int kSpans = 32;                  // parts the bins that may hold top-p's border are cut into
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
-constexpr int kStageBytes = 72 * 1024;      // largest slice kept in shared memory
-
-typedef unsigned long long u64;
+constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
+constexpr float kLeastTemperature = 1e-30f;
 
 // 2^43 * 2^(j / 64)
 __device__ const u64 kPow[64] = {
@@ -60,25 +92,44 @@ __device__ const u64 kPow[64] = {
     0xf5257d15248ull, 0xf7d0df730adull, 0xfa83b2db723ull, 0xfd3e0c0cf48ull,
 };
 
-// What a row's threads share.  One per CTA; ranks read and write each other's.
-struct Shared {
-  u64 pow[64];
-  unsigned cnt[kBins], lo[kBins], hi[kBins];   // a histogram: counts, masses as low and high words
-  unsigned list_key[kList], list_idx[kList];
-  u64 list_w[kList];
-  u64 warp_mass[kWarps], warp_rank[kWarps];
-  unsigned warp_cnt[kWarps];
-  u64 best;                                    // this rank's largest (key, ~index)
-  u64 range_lo, range_hi;                      // of the searched bin's elements, this rank's
-  u64 tot_mass;                                // of this rank's bins, or of its slice
-  unsigned tot_cnt;
-  unsigned list_n;                             // rank 0's: candidates gathered
-  // found by one rank, written to all
-  unsigned found_bin, found_cnt, before_cnt;
-  u64 before_mass;
-  u64 border;                                  // (key, ~index) of the last element kept
-  u64 kept_mass;                               // of the elements up to the border
+struct Candidate {
+  unsigned key, idx;           // key, ~index: a rank
+  u64 w;
 };
+
+// What a row's threads share.  One per CTA; ranks read and write each other's.
+struct __align__(16) Shared {
+  unsigned hist[kBins];
+  u64 pow[64];
+  union {
+    struct {
+      float group[8][kGroup];  // every rank's sums of the groups of bins,
+      float bin[2][8][kGroup]; // and of the bins of a group, for two targets
+    } search;
+    struct {
+      Candidate list[kList];   // rank 0's: candidates gathered
+      Candidate near[kNear];   // this rank's elements in the bins that may hold top-p's border
+    };
+  };
+  u64 span[8][kSpans];         // every rank's masses of the spans
+  unsigned span_lo[kSpans], span_hi[kSpans];     // this rank's, being summed
+  unsigned run_lo[kWarps], run_hi[kWarps];       // kept mass of each warp's run
+  u64 warp_a[kWarps], warp_b[kWarps];
+  u64 box[2][2][8];            // totals of the ranks: two boxes in turn, two values each
+  unsigned list_n, near_n;
+  unsigned doubt, border_doubt;  // a float32 decision that did not clear its bound (this rank's; the border's)
+  // found by one thread of the cluster, written to all ranks
+  int found;
+  u64 before;
+  u64 border;                  // (key, ~index) of the last element kept
+};
+
+// The CTA's shared memory: what its threads share, then its slice of the row.
+// (Taken from the array at each use, so that accesses stay shared-memory ones;
+// through a pointer kept in an object they would become generic.)
+extern __shared__ __align__(16) unsigned char sample_smem[];
+GBF_DEVICE Shared* mem() { return reinterpret_cast<Shared*>(sample_smem); }
+GBF_DEVICE uint4* stage() { return reinterpret_cast<uint4*>(sample_smem + sizeof(Shared)); }
 
 // Monotone 32-bit key of a float (larger float, larger key).
 GBF_DEVICE unsigned key_of(float x) {
@@ -91,49 +142,126 @@ GBF_DEVICE u64 rank_of(unsigned key, unsigned idx) { return (static_cast<u64>(ke
 struct RowScale {
   float top;               // largest logit
   float c_hi, c_lo;        // log2(e) / T
+  float c_bin, c_place;    // bins, and 64ths of a bin, per unit of logit
 };
 
-// round(2^43 exp((l - top) / T)); relative error below 2^-37 + 2^-43 / w.
-// (l - top) / T * log2(e) = ji / 64 + x + xl with |x| < 2^-6.99: 2^(ji / 64) from
-// the table, 2^(x + xl) - 1 by its series with the linear term in two parts.
-GBF_DEVICE u64 weight(const u64* pow, const RowScale& s, float l) {
-  if (l == s.top) return 1ull << kFix;
-  const float d = __fsub_rn(l, s.top);
-  const float t = __fmul_rn(d, s.c_hi);
-  if (!(t > -44.5f)) return 0;                          // below half a unit; also -inf
-  const float e = __fsub_rn(d, l);                      // d + d_lo = l - top exactly
-  const float d_lo = __fsub_rn(__fsub_rn(l, __fsub_rn(d, e)), __fadd_rn(s.top, e));
-  const float t_lo = __fmaf_rn(d_lo, s.c_hi, __fmaf_rn(d, s.c_lo, __fmaf_rn(d, s.c_hi, -t)));
-  const float q = __fadd_rn(__fmul_rn(t, 64.0f), 12582912.0f);       // 1.5 * 2^23: rounds to an integer
+GBF_DEVICE float2 two(float x) { return make_float2(x, x); }
+// b - a
+GBF_DEVICE float2 sub2(float2 b, float2 a) { return __ffma2_rn(a, two(-1.0f), b); }
+
+// From the table index ji, and the fraction's parts in the mantissas of qa and qb: the weight.
+constexpr float kUa = 12582912.0f / 536870912.0f, kUb = 12582912.0f / 274877906944.0f;   // 1.5 * 2^23 units
+GBF_DEVICE u64 assemble(const u64* pow, float nt, float q, float qa, float qb) {
   const int ji = __float_as_int(q) - 0x4b400000;
-  const float g = __fmaf_rn(__fsub_rn(q, 12582912.0f), -1.0f / 64.0f, t);
-  const float x = __fadd_rn(g, t_lo), xl = __fsub_rn(t_lo, __fsub_rn(x, g));
-  constexpr float kL = 0.693147180559945309f;           // ln 2 = kL + kLl
-  constexpr float kLl = static_cast<float>(0.693147180559945309417 - static_cast<double>(kL));
-  const float a = __fmul_rn(x, kL);
-  float b = __fmaf_rn(xl, kL, __fmaf_rn(x, kLl, __fmaf_rn(x, kL, -a)));
-  const float series = __fmaf_rn(x, __fmaf_rn(x, 0.00961812910763f, 0.0555041086648f), 0.240226506959f);
-  b = __fmaf_rn(__fmul_rn(x, x), series, b);
-  // a + b in units of 2^-38, read off the mantissas after adding 1.5 * 2^23 units (which holds up to 2^22 of
-  // them): a (below 2^-7) to 2^-29, then the rest (below 0.97 * 2^-16) to 2^-38
-  constexpr float kUa = 12582912.0f / 536870912.0f, kUb = 12582912.0f / 274877906944.0f;
-  const float qa = __fadd_rn(a, kUa);
-  const float rest = __fadd_rn(__fsub_rn(a, __fsub_rn(qa, kUa)), b);
-  const float qb = __fadd_rn(rest, kUb);
-  const int ia = __float_as_int(qa) - __float_as_int(kUa);
-  const int ib = __float_as_int(qb) - __float_as_int(kUb);
-  const long long i = static_cast<long long>(ia * 512 + ib);
+  const int i = (__float_as_int(qa) - __float_as_int(kUa)) * 512 + (__float_as_int(qb) - __float_as_int(kUb));
   const u64 p = pow[ji & 63];
-  const u64 w = p + static_cast<u64>((i * static_cast<long long>(p >> 12)) >> 26);
-  const int shift = -(ji >> 6);
-  return (w + ((1ull << shift) >> 1)) >> shift;
+  const long long part = static_cast<long long>(i) * static_cast<int>(p >> 13);
+  const u64 w = p * 2 + static_cast<u64>(part >> 24);               // twice the weight, before the octave
+  const u64 scaled = ((w >> (-(ji >> 6) & 63)) + 1) >> 1;
+  return nt < 44.5f ? scaled : 0;                                   // below half a unit (and -inf): zero
 }
 
-// Bin of a candidate: smaller logits never have a lower bin.
-GBF_DEVICE int bin_of(const RowScale& s, float l) {
-  if (l == s.top) return 0;
-  const float t = __fmul_rn(__fmul_rn(__fsub_rn(s.top, l), s.c_hi), kBinsPerOctave);
-  return t < static_cast<float>(kBins - 1) ? static_cast<int>(t) : kBins - 1;
+// round(2^43 exp((l - top) / T)) of two logits; relative error below 2^-36, and half a unit.
+// (l - top) / T * log2(e) = ji / 64 + x + xl with |x| < 2^-6.99: 2^(ji / 64) from
+// the table, 2^(x + xl) - 1 by its series with the linear term in two parts.
+GBF_DEVICE void weights(const u64* pow, const RowScale& s, float2 l, u64* w0, u64* w1) {
+  const float2 one = two(1.0f);
+  const float2 d = __fadd2_rn(l, two(-s.top));
+  const float2 e = sub2(d, l);                                      // d + d_lo = l - top exactly
+  const float2 d_lo = sub2(sub2(l, sub2(d, e)), __fadd2_rn(e, two(s.top)));
+  const float2 nt = __fmul2_rn(d, two(-s.c_hi));                    // -t, t = d c_hi rounded
+  float2 lo = __ffma2_rn(d, two(s.c_hi), nt);                       // what t lacks
+  lo = __ffma2_rn(d, two(s.c_lo), lo);
+  lo = __ffma2_rn(d_lo, two(s.c_hi), lo);
+  const float2 q = __ffma2_rn(nt, two(-64.0f), two(12582912.0f));   // 1.5 * 2^23: rounds to an integer
+  const float2 ng = __ffma2_rn(__fadd2_rn(q, two(-12582912.0f)), two(1.0f / 64.0f), nt);    // ji / 64 - t
+  const float2 x = sub2(lo, ng);
+  const float2 xl = sub2(lo, __fadd2_rn(x, ng));
+  constexpr float kL = 0.693147180559945309f;                       // ln 2 = kL + kLl
+  constexpr float kLl = static_cast<float>(0.693147180559945309417 - static_cast<double>(kL));
+  const float2 na = __fmul2_rn(x, two(-kL));                        // -a, a = x kL rounded
+  float2 b = __ffma2_rn(x, two(kL), na);
+  b = __ffma2_rn(x, two(kLl), b);
+  b = __ffma2_rn(xl, two(kL), b);
+  float2 series = __ffma2_rn(x, two(0.00961812910763f), two(0.0555041086648f));
+  series = __ffma2_rn(x, series, two(0.240226506959f));
+  b = __ffma2_rn(__fmul2_rn(x, x), series, b);
+  // a + b in units of 2^-38, read off the mantissas after adding 1.5 * 2^23 units (which holds up to 2^22 of
+  // them): a (below 2^-7) to 2^-29, then the rest (below 0.97 * 2^-16) to 2^-38
+  const float2 qa = sub2(two(kUa), na);
+  const float2 rest = sub2(b, __fadd2_rn(na, __ffma2_rn(two(-kUa), one, qa)));
+  const float2 qb = __fadd2_rn(rest, two(kUb));
+  *w0 = assemble(pow, nt.x, q.x, qa.x, qb.x);
+  *w1 = assemble(pow, nt.y, q.y, qa.y, qb.y);
+}
+
+// exp((l - top) / T) of two logits in float32, hi + lo within 2^-25: the same argument; 1 + x ln 2 exactly (in two
+// parts), the rest of the fraction's power by a polynomial (minimax on +-0.502: 2^-28.2; 2^-26.1 as evaluated).
+// Logits more than 60 octaves below the top count as 60 octaves below: `lowest`.
+struct Pair2 {
+  float2 hi, lo;
+};
+GBF_DEVICE Pair2 quick_weights(const RowScale& s, float2 l, float lowest) {
+  l.x = fmaxf(l.x, lowest);
+  l.y = fmaxf(l.y, lowest);
+  const float2 d = __fadd2_rn(l, two(-s.top));
+  const float2 e = sub2(d, l);
+  const float2 d_lo = sub2(sub2(l, sub2(d, e)), __fadd2_rn(e, two(s.top)));
+  const float2 nt = __fmul2_rn(d, two(-s.c_hi));
+  float2 lo = __ffma2_rn(d, two(s.c_hi), nt);
+  lo = __ffma2_rn(d, two(s.c_lo), lo);
+  lo = __ffma2_rn(d_lo, two(s.c_hi), lo);
+  const float2 q = sub2(two(12582912.0f), nt);                      // rounds t to an integer, n
+  const float2 ng = __fadd2_rn(__fadd2_rn(q, two(-12582912.0f)), nt);
+  const float2 x = sub2(lo, ng), xl = sub2(lo, __fadd2_rn(x, ng));
+  constexpr float kL = 0.693147180559945309f;
+  constexpr float kLl = static_cast<float>(0.693147180559945309417 - static_cast<double>(kL));
+  const float2 a = __fmul2_rn(x, two(kL));
+  float2 r = __ffma2_rn(x, two(0.00015320504f), two(0.0013390614f));
+  r = __ffma2_rn(x, r, two(0.0096185328f));
+  r = __ffma2_rn(x, r, two(0.055503614f));
+  r = __ffma2_rn(x, r, two(0.24022648f));
+  float2 b = __ffma2_rn(x, two(-kL), a);                            // -(what a lacks)
+  b = sub2(__fmul2_rn(xl, two(kL)), b);
+  b = __ffma2_rn(x, two(kLl), b);
+  b = __ffma2_rn(__fmul2_rn(x, x), r, b);
+  const float2 one = __fadd2_rn(a, two(1.0f));
+  b = __fadd2_rn(b, sub2(a, __fadd2_rn(one, two(-1.0f))));
+  const float2 hi = __fadd2_rn(one, b);                             // hi: the weight rounded to float32
+  b = sub2(b, sub2(hi, one));
+  // times 2^n: n stands in the low bits of q
+  const float2 scale = make_float2(__int_as_float((__float_as_int(q.x) << 23) + 0x3f800000),
+                                   __int_as_float((__float_as_int(q.y) << 23) + 0x3f800000));
+  return {__fmul2_rn(hi, scale), __fmul2_rn(b, scale)};
+}
+
+// A sum of weights that loses nothing: what each addition rounds off is added up beside it, with the weights' low
+// parts.
+struct Sum2 {
+  float2 s, c;
+  GBF_DEVICE void add(float2 w, float2 lo) {
+    const float2 t = __fadd2_rn(s, w), b = sub2(t, s);
+    c = __fadd2_rn(c, __fadd2_rn(__fadd2_rn(sub2(s, sub2(t, b)), sub2(w, b)), lo));
+    s = t;
+  }
+  GBF_DEVICE u64 fixed() const {
+    constexpr float k = static_cast<float>(1ull << kFix);
+    return __float2ull_rn(s.x * k) + __float2ull_rn(s.y * k) +
+           static_cast<u64>(__float2ll_rn(c.x * k) + __float2ll_rn(c.y * k));
+  }
+};
+GBF_DEVICE u64 fixed_of(float hi, float lo) {
+  constexpr float k = static_cast<float>(1ull << kFix);
+  return __float2ull_rn(hi * k) + static_cast<u64>(__float2ll_rn(lo * k));
+}
+// what two float32 sums of masses may be apart by: twice 2^-25 of them, and the conversions' roundings
+GBF_DEVICE u64 slack_of(u64 total) { return (total >> 24) + 4096; }
+
+// Place of a candidate in 64ths of a bin, half a bin ahead: its bin, and 0..63 within it.  Smaller logits never have a
+// lower place.
+GBF_DEVICE int place_of(const RowScale& s, float l) {
+  const float t = fminf(__fmul_rn(__fsub_rn(s.top, l), s.c_place), 64.0f * (kBins - 1) + 31.0f);
+  return __float_as_int(__fadd_rn(t, 12582912.0f)) - (0x4b400000 - 32);
 }
 
 template <typename T>
@@ -143,6 +271,7 @@ struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
   static constexpr unsigned kMinusInf = 0xff80u;
   static GBF_DEVICE void widen(uint4 v, float f[8]) { bf16x8_to_f32(v, f); }
+  static GBF_DEVICE uint4 pack(const float f[8]) { return f32x8_to_bf16x8(f); }
   static GBF_DEVICE unsigned bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 template <>
@@ -155,17 +284,28 @@ struct Elem<float> {
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
   }
+  static GBF_DEVICE uint4 pack(const float f[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
   static GBF_DEVICE unsigned bits(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
 };
 
-// A row as aligned 16-byte vectors.  Vector v holds elements v * N - shift ...;
-// what lies outside the row reads as -inf, and so does NaN.
-template <typename T>
+// NaN reads as -inf, -0 as +0 (equal logits have equal keys).
+template <int N>
+GBF_DEVICE void tidy(float f[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = fmaxf(f[i] + 0.0f, -INFINITY);
+}
+
+// A row as aligned 16-byte vectors of N elements, the first `shift` elements of
+// which lie before it; what lies outside the row reads as -inf.  Passes behind
+// the first one read pairs: pair j holds elements 2 j - shift and the next.
+// STAGED: this rank's vectors v0 ... are in shared memory, tidied.
+template <typename T, bool STAGED>
 struct Row {
   static constexpr int N = Elem<T>::N;
   const char* base;        // 16-byte aligned
-  int shift, vocab, vectors;
-  const uint4* staged;     // vectors [v0, ...) in shared memory, or null
+  int shift, vocab;
   int v0;
 
   GBF_DEVICE uint4 load(int v) const {
@@ -174,23 +314,48 @@ struct Row {
     unsigned w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = e0 + i;
-      const unsigned x = e >= 0 && e < vocab ? Elem<T>::bits(base, static_cast<int64_t>(v) * N + i) : Elem<T>::kMinusInf;
+      const unsigned x = element(e0 + i);
       if (N == 8) w[i >> 1] |= x << (16 * (i & 1));
       else w[i] = x;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  GBF_DEVICE void get(int v, float f[N]) const {
-    Elem<T>::widen(staged ? staged[v - v0] : load(v), f);
-    tidy(f);
+  GBF_DEVICE unsigned element(int e) const {
+    return e >= 0 && e < vocab ? Elem<T>::bits(base, static_cast<int64_t>(e) + shift) : Elem<T>::kMinusInf;
   }
-  // NaN reads as -inf, -0 as +0 (equal logits have equal keys)
-  static GBF_DEVICE void tidy(float f[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = f[i] == f[i] ? f[i] + 0.0f : -INFINITY;
+  GBF_DEVICE float2 pair(int j) const {
+    const int e = 2 * j - shift;
+    float f[2];
+    if (N == 8) {
+      const unsigned w = STAGED ? reinterpret_cast<const unsigned*>(stage())[j - v0 * 4]
+                                : e >= 0 && e + 1 < vocab ? reinterpret_cast<const unsigned*>(base)[j]
+                                                          : element(e) | element(e + 1) << 16;
+      f[0] = __uint_as_float(w << 16);
+      f[1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+      const uint2 w = STAGED ? reinterpret_cast<const uint2*>(stage())[j - v0 * 2]
+                             : e >= 0 && e + 1 < vocab ? reinterpret_cast<const uint2*>(base)[j]
+                                                       : make_uint2(element(e), element(e + 1));
+      f[0] = __uint_as_float(w.x);
+      f[1] = __uint_as_float(w.y);
+    }
+    if (!STAGED) tidy<2>(f);
+    return make_float2(f[0], f[1]);
+  }
+  GBF_DEVICE void get(int v, float f[N]) const {
+    Elem<T>::widen(STAGED ? stage()[v - v0] : load(v), f);
+    if (!STAGED) tidy<N>(f);
+  }
+  GBF_DEVICE float2 pair_or_none(int j, int end) const {
+    return j < end ? pair(j) : make_float2(-INFINITY, -INFINITY);
   }
 };
+
+GBF_DEVICE float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // shared 64-bit add as two 32-bit ones: the carry shows in the old low word
 GBF_DEVICE void add_mass(unsigned* lo, unsigned* hi, u64 w) {
@@ -199,6 +364,7 @@ GBF_DEVICE void add_mass(unsigned* lo, unsigned* hi, u64 w) {
   const unsigned up = wh + (old + wl < old ? 1u : 0u);
   if (up) atomicAdd(hi, up);
 }
+GBF_DEVICE u64 mass_of(unsigned lo, unsigned hi) { return (static_cast<u64>(hi) << 32) + lo; }
 
 GBF_DEVICE u64 warp_sum64(u64 v) {
 #pragma unroll
@@ -213,278 +379,344 @@ GBF_DEVICE u64 warp_max64(u64 v) {
   }
   return v;
 }
+GBF_DEVICE u64 warp_scan64(u64 v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// floor(x 2^64) for 0 <= x < 1: a 64-bit fraction, exact from 2^-40 on.  (Products of masses and float32 shares are
+// taken in integers; a float64 instruction would cost a block of 512 threads some 250 cycles.)
+GBF_DEVICE u64 fraction_of(float x) { return __float2ull_rz(x * 18446744073709551616.0f); }
+// ceil(share * total), at least 1
+GBF_DEVICE u64 share_of(float share, u64 total) {
+  if (!(share > 0.0f)) return 1;
+  if (share >= 1.0f) return ~0ull;
+  const u64 f = fraction_of(share), hi = __umul64hi(f, total) + (f * total != 0 ? 1 : 0);
+  return hi > 0 ? hi : 1;
+}
 
 // One row's cluster.
-template <typename T>
+template <typename T, bool STAGED>
 struct Sampler {
-  Shared* sh;
   cg::cluster_group cluster;
   unsigned rank, ranks;
-  Row<T> row;
+  Row<T, STAGED> row;
   RowScale scale;
-  int v0, v1;              // this rank's vectors
+  int j0, j1;              // this rank's pairs
   int tid, lane, warp;
+  int turn;                // box of the next exchange
 
-  GBF_DEVICE Shared* of(unsigned r) { return cluster.map_shared_rank(sh, r); }
+  GBF_DEVICE Shared* of(unsigned r) { return cluster.map_shared_rank(mem(), r); }
 
-  GBF_DEVICE void clear_hist() {
-    for (int i = tid; i < kBins; i += kThreads) sh->cnt[i] = sh->lo[i] = sh->hi[i] = 0;
+  GBF_DEVICE void clear() {
+    for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(mem()->hist)[i] = make_uint4(0, 0, 0, 0);
   }
+  GBF_DEVICE void weigh(float2 l, u64* w0, u64* w1) {
+    weights(mem()->pow, scale, l, w0, w1);
+    if (scale.top == INFINITY) {                         // the infinite logits share all of the mass
+      *w0 = l.x == INFINITY ? 1ull << kFix : 0;
+      *w1 = l.y == INFINITY ? 1ull << kFix : 0;
+    }
+  }
+  GBF_DEVICE int place(float l) {
+    return scale.top == INFINITY ? (l == INFINITY ? 32 : 64 * kBins - 1) : place_of(scale, l);
+  }
+  GBF_DEVICE int bin(float l) { return place(l) >> 6; }
 
-  // Sums this rank's share of the bins over all ranks, in order, and finds the
-  // bin in which the running count (by_mass false) or mass passes `target`.
-  // The total mass comes back in *all.  Three cluster barriers.
-  GBF_DEVICE void find_bin(bool by_mass, u64 base_cnt, u64 base_mass, u64 target, double share, u64* all) {
-    constexpr int kPer = kBins / kThreads;               // most bins per thread (one rank)
-    cluster.sync();                                      // histograms complete
-    const int mine = kBins / ranks, first = rank * mine;
-    const int per = (mine + kThreads - 1) / kThreads;
-    unsigned c = 0, bc[kPer];
-    u64 m = 0, bm[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = tid * per + i;
-      bc[i] = 0;
-      bm[i] = 0;
-      if (i >= per || j >= mine) continue;
-      for (unsigned r = 0; r < ranks; ++r) {
-        const Shared* o = of(r);
-        bc[i] += o->cnt[first + j];
-        bm[i] += (static_cast<u64>(o->hi[first + j]) << 32) + o->lo[first + j];
-      }
-      c += bc[i];
-      m += bm[i];
-    }
-    unsigned ci = c;
-    u64 mi = m;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned cu = __shfl_up_sync(0xffffffffu, ci, o);
-      const u64 mu = __shfl_up_sync(0xffffffffu, mi, o);
-      if (lane >= o) {
-        ci += cu;
-        mi += mu;
-      }
-    }
-    if (lane == 31) {
-      sh->warp_cnt[warp] = ci;
-      sh->warp_mass[warp] = mi;
+  // Sums over the block of every thread's a and b, the same in all threads.
+  GBF_DEVICE void block_sum(u64* a, u64* b) {
+    const u64 wa = warp_sum64(*a), wb = warp_sum64(*b);
+    __syncthreads();
+    if (lane == 0) {
+      mem()->warp_a[warp] = wa;
+      mem()->warp_b[warp] = wb;
     }
     __syncthreads();
-    unsigned cb = ci - c, tc = 0;
-    u64 mb = mi - m, tm = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        cb += sh->warp_cnt[w];
-        mb += sh->warp_mass[w];
-      }
-      tc += sh->warp_cnt[w];
-      tm += sh->warp_mass[w];
+    *a = warp_sum64(lane < kWarps ? mem()->warp_a[lane] : 0);
+    *b = warp_sum64(lane < kWarps ? mem()->warp_b[lane] : 0);
+  }
+  // Every rank's (a, b), the same in all threads of a rank, to all ranks'
+  // boxes; a cluster barrier.
+  GBF_DEVICE const u64 (*exchange(u64 a, u64 b))[8] {
+    if (tid < ranks) {
+      Shared* o = of(tid);
+      o->box[turn][0][rank] = a;
+      o->box[turn][1][rank] = b;
     }
-    if (tid == 0) {
-      sh->tot_cnt = tc;
-      sh->tot_mass = tm;
-    }
-    cluster.sync();                                      // totals of all ranks
-    u64 total = 0;
-    u64 cnt0 = base_cnt + cb, mass0 = base_mass + mb;
-    for (unsigned r = 0; r < ranks; ++r) {
-      const Shared* o = of(r);
-      if (r < rank) {
-        cnt0 += o->tot_cnt;
-        mass0 += o->tot_mass;
-      }
-      total += o->tot_mass;
-    }
-    *all = total;
-    if (share >= 0.0) {                                  // the target is a share of the total
-      const double x = ceil(share * static_cast<double>(total));
-      target = x < 1.0 ? 1ull : static_cast<u64>(x);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const u64 at = by_mass ? mass0 : cnt0;
-      const u64 by = by_mass ? bm[i] : static_cast<u64>(bc[i]);
-      if (by > 0 && at < target && at + by >= target) {  // one thread of the cluster, if any
-        for (unsigned r = 0; r < ranks; ++r) {
-          Shared* o = of(r);
-          o->found_bin = first + tid * per + i;
-          o->found_cnt = bc[i];
-          o->before_cnt = static_cast<unsigned>(cnt0);
-          o->before_mass = mass0;
-        }
-      }
-      cnt0 += bc[i];
-      mass0 += bm[i];
-    }
-    cluster.sync();                                      // the finding
+    cluster.sync();
+    const u64(*got)[8] = mem()->box[turn];
+    turn ^= 1;
+    return got;
   }
 
-  // Border of the order's shortest prefix that holds `target` elements (or
-  // that mass, or that share of the mass): sh->border and sh->kept_mass of all
-  // ranks.  The first histogram is in place; true when it was overwritten.
-  GBF_DEVICE bool select(bool by_mass, bool masses, u64 target, double share) {
-    u64 total;
-    if (tid == 0) sh->found_cnt = 0;
-    find_bin(by_mass, 0, 0, target, share, &total);
-    if (share >= 0.0) {
-      const double x = ceil(share * static_cast<double>(total));
-      target = x < 1.0 ? 1ull : static_cast<u64>(x);
+  // A warp's running sum over 64 values, each summed over the ranks' rows (lane
+  // l: values 2 l and 2 l + 1).
+  struct Scan {
+    float y, xy, incl, total;
+  };
+  struct Hit {
+    int at;                    // value at which the sum reaches a target; -1: it stays below
+    float before;
+  };
+  GBF_DEVICE Scan scan64(const float (*rows)[kGroup], float base) {
+    float x = 0.0f, y = 0.0f;
+    for (unsigned r = 0; r < ranks; ++r) {
+      const float2 v = reinterpret_cast<const float2*>(rows[r])[lane];
+      x += v.x;
+      y += v.y;
     }
-    unsigned n = sh->found_cnt;
-    if (n == 0) {                                        // fewer than `target`: nothing is cut off
-      if (tid == 0) {
-        sh->border = 0;
-        sh->kept_mass = total;
-      }
-      __syncthreads();
-      return false;
-    }
-    const int bin = static_cast<int>(sh->found_bin);
-    u64 lo = 0, hi = ~0ull;                              // ranks searched, once known
-    bool by_range = false;
-    if (n > kList) {
-      // the bin's range of ranks
-      u64 mn = ~0ull, mx = 0;
-      for (int v = v0 + tid; v < v1; v += kThreads) {
-        float f[Row<T>::N];
-        row.get(v, f);
+    Scan s{y, x + y, x + y, 0.0f};
 #pragma unroll
-        for (int i = 0; i < Row<T>::N; ++i)
-          if (f[i] != -INFINITY && bin_of(scale, f[i]) == bin) {
-            const u64 k = rank_of(key_of(f[i]), v * Row<T>::N - row.shift + i);
-            mn = k < mn ? k : mn;
-            mx = k > mx ? k : mx;
-          }
-      }
-      mn = ~warp_max64(~mn);
-      mx = warp_max64(mx);
-      if (lane == 0) {
-        sh->warp_mass[warp] = mx;
-        sh->warp_rank[warp] = mn;
-      }
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-          mx = sh->warp_mass[w] > mx ? sh->warp_mass[w] : mx;
-          mn = sh->warp_rank[w] < mn ? sh->warp_rank[w] : mn;
-        }
-        sh->range_lo = mn;
-        sh->range_hi = mx;
-      }
-      cluster.sync();
-      lo = ~0ull;
-      hi = 0;
-      for (unsigned r = 0; r < ranks; ++r) {
-        const Shared* o = of(r);
-        lo = o->range_lo < lo ? o->range_lo : lo;
-        hi = o->range_hi > hi ? o->range_hi : hi;
-      }
-      by_range = true;
-      for (int level = 0; n > kList && level < 8; ++level) {   // 11 of 64 bits each
-        int s = 0;
-        while (((hi - lo) >> s) >= kBins) ++s;
-        const u64 before_cnt = sh->before_cnt, before_mass = sh->before_mass;
-        cluster.sync();                                  // every rank is done with the last histogram and finding
-        clear_hist();
-        __syncthreads();
-        for (int v = v0 + tid; v < v1; v += kThreads) {
-          float f[Row<T>::N];
-          row.get(v, f);
-#pragma unroll
-          for (int i = 0; i < Row<T>::N; ++i) {
-            const u64 k = rank_of(key_of(f[i]), v * Row<T>::N - row.shift + i);
-            if (f[i] == -INFINITY || k < lo || k > hi) continue;
-            const int j = static_cast<int>((hi - k) >> s);
-            atomicAdd(&sh->cnt[j], 1u);
-            if (masses) add_mass(&sh->lo[j], &sh->hi[j], weight(sh->pow, scale, f[i]));
-          }
-        }
-        u64 unused;
-        find_bin(by_mass, before_cnt, before_mass, target, -1.0, &unused);
-        n = sh->found_cnt;
-        const u64 j = sh->found_bin;
-        const u64 new_hi = hi - (j << s), span = (1ull << s) - 1;
-        lo = new_hi - lo > span ? new_hi - span : lo;
-        hi = new_hi;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const float up = __shfl_up_sync(0xffffffffu, s.incl, o);
+      if (lane >= o) s.incl += up;
     }
-    // gather the candidates on rank 0 and rank them by comparison
-    const u64 before_cnt = sh->before_cnt, before_mass = sh->before_mass;
-    Shared* head = of(0);
-    if (rank == 0 && tid == 0) sh->list_n = 0;
+    s.incl += base;
+    s.total = __shfl_sync(0xffffffffu, s.incl, 31);
+    return s;
+  }
+  GBF_DEVICE Hit hit64(const Scan& s, float t) {
+    const unsigned m = __ballot_sync(0xffffffffu, s.incl >= t);
+    const int src = m ? __ffs(m) - 1 : 0;
+    const bool second = s.incl - s.y < t;                // (in the lane that reaches t)
+    const int at = 2 * lane + (second ? 1 : 0);
+    const float before = s.incl - (second ? s.y : s.xy);
+    Hit h{__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, before, src)};
+    if (!m) h.at = -1;
+    return h;
+  }
+  // The bins in which the running sum over bins 0, 1, ... and all ranks reaches
+  // two targets: by groups of 64 bins, then the bins of the groups they lie
+  // in.  value(j): this rank's of bin j.  Float32 sums: exact for counts (at
+  // most 2^20), and 2^-19 for masses that are known to 0.3 %.  Two barriers.
+  template <typename Value, typename Targets>
+  GBF_DEVICE void find_bins(Value value, Targets targets, Hit out[2]) {
+    static_assert(kBins == 8 * kThreads && kGroup * kGroup == kBins && kThreads == 8 * kGroup, "");
+    __syncthreads();                                     // this rank's histogram is complete
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += value(tid * 8 + i);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((tid & 7) < ranks) of(tid & 7)->search.group[rank][tid >> 3] = sum;
     cluster.sync();
-    for (int v = v0 + tid; v < v1; v += kThreads) {
-      float f[Row<T>::N];
-      row.get(v, f);
+    const Scan groups = scan64(mem()->search.group, 0.0f);
+    float t[2];
+    targets(groups.total, t);
 #pragma unroll
-      for (int i = 0; i < Row<T>::N; ++i) {
-        if (f[i] == -INFINITY) continue;
-        const unsigned key = key_of(f[i]), idx = v * Row<T>::N - row.shift + i;
-        const u64 k = rank_of(key, idx);
-        if (by_range ? (k < lo || k > hi) : bin_of(scale, f[i]) != bin) continue;
-        const unsigned at = atomicAdd(&head->list_n, 1u);
-        if (at < kList) {
-          head->list_key[at] = key;
-          head->list_idx[at] = idx;
-          head->list_w[at] = weight(sh->pow, scale, f[i]);
-        }
-      }
+    for (int k = 0; k < 2; ++k) {
+      out[k] = hit64(groups, t[k]);
+      const unsigned r = tid >> 6;
+      if (out[k].at >= 0 && r < ranks)
+        of(r)->search.bin[k][rank][tid & 63] = value(out[k].at * kGroup + (tid & 63));
     }
     cluster.sync();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (out[k].at >= 0) {
+        const Hit h = hit64(scan64(mem()->search.bin[k], out[k].before), t[k]);
+        out[k].before = h.before;
+        out[k].at = out[k].at * kGroup + (h.at < 0 ? kGroup - 1 : h.at);
+      }
+  }
+
+  // The same over kCells cells of masses in the histogram's memory, one target:
+  // mem()->found and mem()->before of all ranks.  Three barriers.
+  GBF_DEVICE void find_cell(u64 base, u64 target) {
+    constexpr int kMost = kCells / kThreads;
+    if (tid == 0) mem()->found = -1;
+    cluster.sync();
+    const int mine = kCells / ranks, first = rank * mine;
+    const int per = (mine + kThreads - 1) / kThreads;
+    u64 val[kMost], part = 0;
+#pragma unroll 1
+    for (int i = 0; i < kMost; ++i) {
+      u64 lo = 0, hi = 0;
+      if (i < per && tid * per + i < mine)
+        for (unsigned r = 0; r < ranks; ++r) {
+          lo += of(r)->hist[first + tid * per + i];
+          hi += of(r)->hist[kCells + first + tid * per + i];
+        }
+      val[i] = (hi << 32) + lo;
+      part += val[i];
+    }
+    const u64 incl = warp_scan64(part, lane);
+    if (lane == 31) mem()->warp_a[warp] = incl;
+    __syncthreads();
+    u64 at = base + incl - part, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += mem()->warp_a[w];
+      all += mem()->warp_a[w];
+    }
+    const u64(*box)[8] = exchange(all, 0);
+    for (unsigned r = 0; r < rank; ++r) at += box[0][r];
+#pragma unroll 1
+    for (int i = 0; i < kMost; ++i) {
+      if (at < target && at + val[i] >= target)          // one thread of the cluster, if any
+        for (unsigned r = 0; r < ranks; ++r) {
+          of(r)->found = first + tid * per + i;
+          of(r)->before = at;
+        }
+      at += val[i];
+    }
+    cluster.sync();
+  }
+
+  // Rank 0 ranks its list by comparison: the last of them before which less
+  // than `target` lies, to all ranks' borders.  Behind a barrier that completes
+  // the list; ends with one.
+  // slack > 0: the border is in doubt unless it clears the target by that much.
+  GBF_DEVICE void border_of_list(u64 before, u64 target, u64 slack) {
     if (rank == 0) {
-      const int found = static_cast<int>(sh->list_n < kList ? sh->list_n : kList);
-      u64 last = ~0ull, mass = 0;
-      for (int i = tid; i < found; i += kThreads) {
-        const u64 k = rank_of(sh->list_key[i], sh->list_idx[i]);
-        u64 cnt = before_cnt, w = before_mass;
-        for (int j = 0; j < found; ++j)
-          if (rank_of(sh->list_key[j], sh->list_idx[j]) > k) {
-            ++cnt;
-            w += sh->list_w[j];
-          }
-        if ((by_mass ? w : cnt) < target) {              // kept
-          last = k < last ? k : last;
-          mass += sh->list_w[i];
+      const int n = static_cast<int>(mem()->list_n);
+      u64 last = ~0ull;
+      bool sure = slack == 0;
+#pragma unroll 1
+      for (int i = tid; i < n; i += kThreads) {
+        const Candidate c = mem()->list[i];
+        const u64 k = (static_cast<u64>(c.key) << 32) | c.idx;
+        u64 at = before;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const Candidate o = mem()->list[j];
+          if (((static_cast<u64>(o.key) << 32) | o.idx) > k) at += o.w;
         }
+        if (at < target) last = k < last ? k : last;
+        if (at < target && at + c.w >= target) sure |= (at == 0 || at + slack < target) && at + c.w >= target + slack;
       }
       last = ~warp_max64(~last);
-      mass = warp_sum64(mass);
       __syncthreads();
-      if (lane == 0) {
-        sh->warp_mass[warp] = mass;
-        sh->warp_rank[warp] = last;
-      }
-      __syncthreads();
-      if (tid == 0) {
-        mass = before_mass;
-        last = ~0ull;
-        for (int w = 0; w < kWarps; ++w) {
-          mass += sh->warp_mass[w];
-          last = sh->warp_rank[w] < last ? sh->warp_rank[w] : last;
-        }
-        for (unsigned r = 0; r < ranks; ++r) {
-          of(r)->border = last;
-          of(r)->kept_mass = mass;
-        }
+      if (lane == 0) mem()->warp_a[warp] = last;
+      sure = __syncthreads_or(sure);
+      last = ~warp_max64(lane < kWarps ? ~mem()->warp_a[lane] : 0);
+      if (tid < ranks) {
+        of(tid)->border = last;
+        of(tid)->border_doubt = !sure;
       }
     }
     cluster.sync();
-    return by_range;
+  }
+
+  // The rank (key, ~index) of the last element before which less than `target`
+  // (elements, or mass) lies, to mem()->border of all ranks.  It is one of the
+  // elements with bins b0..b1 and ranks >= lo, before which `before` lies.
+  GBF_DEVICE void border_within(bool by_mass, int b0, int b1, u64 lo, u64 before, u64 target) {
+    u64 hi = ~0ull;
+    int s = 0;
+    // these bins' logits lie between these two, with room for the roundings
+    float l_hi = INFINITY, l_lo = -FLT_MAX;
+    if (scale.top != INFINITY) {
+      if (b0 > 0) l_hi = scale.top - (b0 - 1) / scale.c_bin;
+      if (b1 < kBins - 1) l_lo = fmaxf(scale.top - (b1 + 1) / scale.c_bin, -FLT_MAX);
+    }
+    // rounds: gather the candidates on rank 0; when there are too many, the range of their ranks, then (and again)
+    // that range cut into cells, of which the target's one stays, and gather again
+    enum { kGather, kRange, kCut };
+    int level = 0;
+    for (int todo = kGather;;) {
+      Shared* head = of(0);
+      u64 mn = ~0ull, mx = 0;
+      if (todo == kGather && rank == 0 && tid == 0) mem()->list_n = 0;
+      if (todo == kCut) clear();
+      cluster.sync();                                    // also: every rank is done with the last histogram
+      float2 next = row.pair_or_none(j0 + tid, j1);
+#pragma unroll 1
+      for (int j = j0 + tid; j < j1; j += kThreads) {
+        const float2 f = next;
+        next = row.pair_or_none(j + kThreads, j1);
+        bool on[2] = {f.x >= l_lo && f.x <= l_hi, f.y >= l_lo && f.y <= l_hi};
+        if (!on[0] && !on[1]) continue;
+        u64 k[2], w[2] = {1, 1};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float l = e ? f.y : f.x;
+          k[e] = rank_of(key_of(l), 2 * j + e - row.shift);
+          const int n = bin(l);
+          on[e] = on[e] && k[e] >= lo && k[e] <= hi && n >= b0 && n <= b1;
+        }
+        if (!on[0] && !on[1]) continue;
+        if (by_mass && todo != kRange) weigh(f, &w[0], &w[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!on[e]) continue;
+          if (todo == kGather) {
+            const unsigned at = atomicAdd(&head->list_n, 1u);
+            if (at < kList) head->list[at] = {static_cast<unsigned>(k[e] >> 32), static_cast<unsigned>(k[e]), w[e]};
+          } else if (todo == kRange) {
+            mn = k[e] < mn ? k[e] : mn;
+            mx = k[e] > mx ? k[e] : mx;
+          } else {
+            const int cell = static_cast<int>((hi - k[e]) >> s);
+            add_mass(&mem()->hist[cell], &mem()->hist[kCells + cell], w[e]);
+          }
+        }
+      }
+      if (todo == kGather) {
+        cluster.sync();
+        if (head->list_n <= kList || level == 8) break;
+        todo = level == 0 ? kRange : kCut;
+      } else if (todo == kRange) {
+        mn = ~warp_max64(~mn);
+        mx = warp_max64(mx);
+        __syncthreads();
+        if (lane == 0) {
+          mem()->warp_a[warp] = mx;
+          mem()->warp_b[warp] = mn;
+        }
+        __syncthreads();
+        mx = warp_max64(lane < kWarps ? mem()->warp_a[lane] : 0);
+        mn = ~warp_max64(lane < kWarps ? ~mem()->warp_b[lane] : 0);
+        const u64(*box)[8] = exchange(mn, mx);
+        lo = ~0ull;
+        hi = 0;
+        for (unsigned r = 0; r < ranks; ++r) {
+          lo = box[0][r] < lo ? box[0][r] : lo;
+          hi = box[1][r] > hi ? box[1][r] : hi;
+        }
+        todo = kCut;
+      } else {
+        find_cell(before, target);
+        if (mem()->found >= 0) {                            // (always: the target lies within)
+          before = mem()->before;
+          hi -= static_cast<u64>(mem()->found) << s;
+          const u64 span = (1ull << s) - 1;
+          lo = hi - lo > span ? hi - span : lo;
+        }
+        ++level;
+        todo = kGather;
+      }
+      if (todo == kCut) {
+        s = 0;
+        while (((hi - lo) >> s) >= kCells) ++s;
+      }
+    }
+    border_of_list(before, target, 0);
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int staged) {
+// border_within as a call (it is needed in two places and long), on a copy, so
+// that the caller's object stays in registers.
+template <typename T, bool STAGED>
+__device__ __noinline__ int border_call(Sampler<T, STAGED> s, bool by_mass, int b0, int b1, u64 lo, u64 before,
+                                        u64 target) {
+  s.border_within(by_mass, b0, b1, lo, before, target);
+  return s.turn;
+}
+
+template <typename T, bool STAGED>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   constexpr int N = Elem<T>::N;
-  extern __shared__ __align__(16) unsigned char dyn[];
-  Sampler<T> s{reinterpret_cast<Shared*>(dyn), cg::this_cluster()};
-  Shared* sh = s.sh;
+  Sampler<T, STAGED> s{cg::this_cluster()};
   s.rank = s.cluster.block_rank();
   s.ranks = s.cluster.num_blocks();
+  s.turn = 0;
   const int tid = s.tid = threadIdx.x, lane = s.lane = tid & 31, warp = s.warp = tid >> 5;
-  for (int i = tid; i < 64; i += kThreads) sh->pow[i] = kPow[i];
-  s.clear_hist();
+  if (tid < 64) mem()->pow[tid] = kPow[tid];
+  s.clear();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -494,30 +726,30 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
   s.row.base = at - off;
   s.row.shift = off / static_cast<int>(sizeof(T));
   s.row.vocab = a.vocab;
-  s.row.vectors = (s.row.shift + a.vocab + N - 1) / N;
-  s.row.staged = nullptr;
-  const int per = (s.row.vectors + s.ranks - 1) / s.ranks;
-  const int v0 = s.v0 = min(static_cast<int>(s.rank) * per, s.row.vectors);
-  const int v1 = s.v1 = min(v0 + per, s.row.vectors);
-  s.row.v0 = v0;
+  const int vectors = (s.row.shift + a.vocab + N - 1) / N;
+  const int per = (vectors + s.ranks - 1) / s.ranks;
+  const int v0 = s.row.v0 = min(static_cast<int>(s.rank) * per, vectors);
+  const int v1 = min(v0 + per, vectors);
+  s.j0 = v0 * (N / 2);
+  s.j1 = v1 * (N / 2);
+  const float temp = a.temperature ? a.temperature[b] : 1.0f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.0f;
+  const float mp = a.min_p ? a.min_p[b] : 0.0f;
+  const float u = a.uniform[b];
 
-  // pass 1: the only read of HBM; the largest logit and its lowest index
-  uint4* stage = reinterpret_cast<uint4*>(dyn + sizeof(Shared));
-  float best = -INFINITY;
-  unsigned best_i = 0;
+  // pass 1: the only read of HBM; the largest logit
+  float most = -INFINITY;
   auto look = [&](int v, uint4 raw) {
-    if (staged) stage[v - v0] = raw;
     float f[N];
     Elem<T>::widen(raw, f);
-    Row<T>::tidy(f);
+    tidy<N>(f);
+    if (STAGED) stage()[v - v0] = Elem<T>::pack(f);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (f[i] > best) {
-        best = f[i];
-        best_i = v * N - s.row.shift + i;
-      }
+    for (int i = 0; i < N; ++i) most = fmaxf(most, f[i]);
   };
   int v = v0 + tid;
+#pragma unroll 1
   for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
     uint4 raw[4];
 #pragma unroll
@@ -525,178 +757,377 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
 #pragma unroll
     for (int u = 0; u < 4; ++u) look(v + u * kThreads, raw[u]);
   }
+#pragma unroll 1
   for (; v < v1; v += kThreads) look(v, s.row.load(v));
-  u64 top = best == -INFINITY ? 0 : rank_of(key_of(best), best_i);
-  top = warp_max64(top);
-  if (lane == 0) sh->warp_mass[warp] = top;
+  // (as a key: largest over the lanes, the warps and the ranks; 0: no candidate)
+  unsigned top = __reduce_max_sync(0xffffffffu, most == -INFINITY ? 0u : key_of(most));
+  if (lane == 0) mem()->warp_a[warp] = top;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) top = sh->warp_mass[w] > top ? sh->warp_mass[w] : top;
-    sh->best = top;
+  top = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_a[lane]) : 0u);
+  {
+    const u64(*box)[8] = s.exchange(top, 0);
+    for (unsigned r = 0; r < s.ranks; ++r) top = max(top, static_cast<unsigned>(box[0][r]));
   }
-  s.cluster.sync();
-  if (staged) s.row.staged = stage;
-  top = 0;
-  for (unsigned r = 0; r < s.ranks; ++r) {
-    const u64 o = s.of(r)->best;
-    top = o > top ? o : top;
-  }
+  s.scale.top = of_key(top);
 
-  const float temp = a.temperature ? a.temperature[b] : 1.0f;
-  const int k = a.top_k ? a.top_k[b] : 0;
-  const float p = a.top_p ? a.top_p[b] : 1.0f;
-  const float mp = a.min_p ? a.min_p[b] : 0.0f;
-  const float u = a.uniform[b];
   const bool bad = !(temp >= 0.0f && temp < INFINITY) || !(p == p) || !(mp <= 1.0f) || !(u >= 0.0f && u < 1.0f);
-  if (bad || top == 0 || temp == 0.0f) {
+  if (bad || top == 0) {
     if (s.rank == 0 && tid == 0) {
-      const bool none = bad || top == 0;
-      if (none) raise_error(a.err, DEV_ERR_SAMPLING);
-      a.tokens[b] = none ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<unsigned>(top));
-      if (a.logprob) a.logprob[b] = none ? __uint_as_float(0x7fc00000u) : 0.0f;
+      raise_error(a.err, DEV_ERR_SAMPLING);
+      a.tokens[b] = -1;
+      if (a.logprob) a.logprob[b] = __uint_as_float(0x7fc00000u);
     }
-    s.cluster.sync();                                    // no rank leaves while others read its memory
     return;
   }
-  s.scale.top = of_key(static_cast<unsigned>(top >> 32));
+  if (temp == 0.0f) {                                    // the lowest index of the largest logit
+    unsigned first = 0xffffffffu;
+    if (most == s.scale.top)
+#pragma unroll 1
+      for (int j = s.j0 + tid * (N / 2); j < s.j1; j += kThreads * (N / 2)) {
+#pragma unroll 1
+        for (int e = 0; e < N / 2; ++e) {
+          const float2 f = s.row.pair(j + e);
+          const unsigned i = 2 * (j + e) - s.row.shift;
+          if (f.y == s.scale.top) first = min(first, i + 1);
+          if (f.x == s.scale.top) first = min(first, i);
+        }
+      }
+    first = __reduce_min_sync(0xffffffffu, first);
+    __syncthreads();
+    if (lane == 0) mem()->warp_a[warp] = first;
+    __syncthreads();
+    first = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_a[lane]) : 0xffffffffu);
+    const u64(*box)[8] = s.exchange(first, 0);
+    for (unsigned r = 0; r < s.ranks; ++r) first = min(first, static_cast<unsigned>(box[0][r]));
+    if (s.rank == 0 && tid == 0) {
+      a.tokens[b] = static_cast<int32_t>(first);
+      if (a.logprob) a.logprob[b] = 0.0f;
+    }
+    return;
+  }
+  const float heat = fmaxf(temp, kLeastTemperature);
   {
-    const double c = 1.4426950408889634 / static_cast<double>(temp);
-    s.scale.c_hi = c < 3.0e38 ? static_cast<float>(c) : 3.0e38f;
-    s.scale.c_lo = c < 3.0e38 ? static_cast<float>(c - static_cast<double>(s.scale.c_hi)) : 0.0f;
+    // log2(e) / T in two parts: the quotient of the high part, and the quotient of what it leaves
+    constexpr float kHi = 1.44269504088896341f;
+    constexpr float kLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kHi));
+    s.scale.c_hi = __fdiv_rn(kHi, heat);
+    s.scale.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-s.scale.c_hi, heat, kHi), kLo), heat);
+    s.scale.c_bin = s.scale.c_hi * kBinsPerOctave;
+    s.scale.c_place = s.scale.c_bin * 64.0f;
   }
+  const u64 least = mp > 0.0f ? __float2ull_ru(mp * static_cast<float>(1ull << kFix)) : 0;
 
-  // top-k and top-p: the border of the kept prefix
   const bool by_k = k > 0 && k < a.vocab, by_p = p < 1.0f;
-  u64 border = 0;
+  u64 border = 0;                                        // ranks below it are cut off
+  int b0 = 0, b1 = kBins - 1;                            // bins the border of top-p lies in
   if (by_k || by_p) {
-    auto histogram = [&]() {
-      for (int i = v0 + tid; i < v1; i += kThreads) {
-        float f[N];
-        s.row.get(i, f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          if (f[e] == -INFINITY) continue;
-          const int j = bin_of(s.scale, f[e]);
-          atomicAdd(&sh->cnt[j], 1u);
-          if (by_p)
-            add_mass(&sh->lo[j], &sh->hi[j], weight(sh->pow, s.scale, f[e]));
-        }
-      }
-    };
-    histogram();
-    bool again = false;
-    if (by_k) {
-      again = s.select(false, by_p, static_cast<u64>(k), -1.0);
-      border = sh->border;
-    }
-    if (by_p) {
-      double share = p > 0.0f ? static_cast<double>(p) : 0.0;
-      u64 target = 0;
-      if (by_k) {                                        // a share of what top-k kept
-        const double x = ceil(share * static_cast<double>(sh->kept_mass));
-        target = x < 1.0 ? 1ull : static_cast<u64>(x);
-        share = -1.0;
-        s.cluster.sync();                                // every rank has read its kept mass
-        if (again) {
-          s.clear_hist();
-          __syncthreads();
-          histogram();
-        }
-      }
-      s.select(true, true, target, share);
-      border = sh->border > border ? sh->border : border;
-    }
-  }
-  const u64 least = mp > 0.0f ? static_cast<u64>(ceil(static_cast<double>(mp) * static_cast<double>(1ull << kFix))) : 0;
-
-  // the kept mass in index order: a contiguous run of vectors per warp
-  auto kept = [&](float f, unsigned idx) -> u64 {
-    if (f == -INFINITY || rank_of(key_of(f), idx) < border) return 0;
-    const u64 w = weight(sh->pow, s.scale, f);
-    return w >= least ? w : 0;
-  };
-  const int run = (v1 - v0 + kWarps - 1) / kWarps;
-  const int w0 = min(v0 + warp * run, v1), w1 = min(w0 + run, v1);
-  auto lane_mass = [&](int i) {
-    u64 m = 0;
-    if (i < w1) {
+#pragma unroll 1
+    for (int i = v0 + tid; i < v1; i += kThreads) {
       float f[N];
       s.row.get(i, f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) m += kept(f[e], i * N - s.row.shift + e);
+      for (int e = 0; e < N; ++e)
+        if (f[e] != -INFINITY) {
+          const int at = s.place(f[e]);
+          atomicAdd(&mem()->hist[at >> 6], by_k ? 1u : (1u << 20) + (at & 63));
+        }
     }
-    return m;
-  };
-  u64 mass = 0;
-  for (int i = w0 + lane; i < w1; i += 32) mass += lane_mass(i);
-  mass = warp_sum64(mass);
-  __syncthreads();
-  if (lane == 0) sh->warp_mass[warp] = mass;
-  __syncthreads();
-  u64 before = 0, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh->warp_mass[w];
-    total += sh->warp_mass[w];
+    // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
+    typename Sampler<T, STAGED>::Hit hit[2];
+    s.find_bins(
+        [&](int j) {
+          const unsigned h = mem()->hist[j];
+          if (by_k) return static_cast<float>(h);
+          const float c = static_cast<float>(h >> 20), places = static_cast<float>(h & 0xfffffu);
+          return (c - 0.00541521235f / 64.0f * (places - 32.0f * c)) * exp2_approx(-j / kBinsPerOctave);
+        },
+        [&](float total, float* t) {
+          const float error = kBinError + kLastBinError * static_cast<float>(a.vocab);
+          const float r = (1.0f - error) / (1.0f + error);
+          t[0] = by_k ? static_cast<float>(k) : p * r * total;
+          t[1] = by_k ? INFINITY : p / r * total;
+        },
+        hit);
+    if (!by_k) {
+      b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;
+      b1 = hit[1].at < 0 ? kBins - 1 : hit[1].at;
+    } else if (hit[0].at >= 0) {                         // else fewer than k candidates
+      s.turn = border_call<T, STAGED>(s, false, hit[0].at, hit[0].at, 0, static_cast<u64>(hit[0].before), static_cast<u64>(k));
+      border = mem()->border;
+      b1 = hit[0].at;
+    }
   }
-  if (tid == 0) sh->tot_mass = total;
-  s.cluster.sync();
-  total = 0;
-  for (unsigned r = 0; r < s.ranks; ++r) {
-    const u64 o = s.of(r)->tot_mass;
-    if (r < s.rank) before += o;
-    total += o;
-  }
-  u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(total));
-  if (target >= total) target = total - 1;
-  if (before <= target && target < before + mass) {      // one warp of the cluster
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const u64 mine = lane_mass(i0 + lane);
-      u64 incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+
+  // A contiguous run of vectors per warp.
+  const int run_v = (v1 - v0 + kWarps - 1) / kWarps, run = run_v * (N / 2);
+  const int u0 = min(v0 + warp * run_v, v1), u1 = min(u0 + run_v, v1);
+  const int w0 = min(s.j0 + warp * run, s.j1), w1 = min(w0 + run, s.j1);
+  // a finite logit below this one has a weight below min_p by more than any rounding
+  float floor_l = -FLT_MAX;
+  if (mp > 0.0f && s.scale.top != INFINITY)
+    floor_l = fmaxf(__fadd_rd(s.scale.top, (log2f(mp) - 0.01f) / s.scale.c_hi * 1.0001f), -FLT_MAX);
+  const u64 k_border = border;
+  const float border_l = border ? of_key(static_cast<unsigned>(border >> 32)) : -FLT_MAX;
+  const float from_l = by_p ? border_l : fmaxf(border_l, floor_l);
+  const float lowest = fmaxf(s.scale.top - 60.0f / s.scale.c_hi, -FLT_MAX);
+  // float32 first: where there is much to weigh (top-k leaves little), and no two criteria meet in one sum
+  bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || s.scale.top == INFINITY;
+
+  for (;; exact = true) {
+    // The kept mass of each run.  With top-p, also the mass in all and above the border's bins; what lies in them
+    // goes to a list, and its mass to the span of bins.
+    // (a logit above above_l lies in a bin before b0, one below below_l behind b1)
+    float above_l = INFINITY, below_l = -FLT_MAX;
+    if (by_p && s.scale.top != INFINITY) {
+      if (b0 > 0) above_l = s.scale.top - (b0 - 1) / s.scale.c_bin;
+      if (b1 < kBins - 1) below_l = fmaxf(s.scale.top - (b1 + 1) / s.scale.c_bin, -FLT_MAX);
+    }
+    int coarse = 0;
+    while (((b1 - b0) >> coarse) >= kSpans) ++coarse;
+    if (tid < kSpans) mem()->span_lo[tid] = mem()->span_hi[tid] = 0;
+    if (tid == 0) mem()->near_n = mem()->doubt = 0;
+    __syncthreads();
+    u64 kept = 0, above = 0, all = 0;
+    // an element that may lie in the border's bins: true when it does
+    auto near = [&](float l, unsigned i, u64 w) {
+      const int n = s.bin(l);
+      if (n < b0) return false;
+      if (n <= b1) {
+        const int span = (n - b0) >> coarse;
+        add_mass(&mem()->span_lo[span], &mem()->span_hi[span], w);
+        const unsigned at = atomicAdd(&mem()->near_n, 1u);
+        if (at < kNear) mem()->near[at] = {key_of(l), 0xffffffffu - i, w};
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + incl > target);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          u64 run_mass = before + incl - mine;
-          float f[N];
-          s.row.get(i0 + lane, f);
-          bool done = false;
+      return true;
+    };
+    if (!exact) {
+      Sum2 sum{}, sum_above{};
+      const float mp_lo = mp * (1.0f - 0x1p-21f), mp_hi = mp * (1.0f + 0x1p-21f);
+#pragma unroll 1
+      for (int i = u0 + lane; i < u1; i += 32) {
+        float f[N];
+        s.row.get(i, f);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const unsigned idx = (i0 + lane) * N - s.row.shift + e;
-            run_mass += kept(f[e], idx);
-            if (!done && run_mass > target) {
-              done = true;
-              a.tokens[b] = static_cast<int32_t>(idx);
-              if (a.logprob) {
-                // ln(w / total) = (l - top) / T - ln(total / 2^43), both terms of one sign
-                const float d = f[e] == s.scale.top ? 0.0f : (f[e] - s.scale.top) / temp;
-                const u64 more = total - (1ull << kFix);
-                a.logprob[b] = d - log1pf(static_cast<float>(more) * (1.0f / static_cast<float>(1ull << kFix)));
-              }
+        for (int e = 0; e < N; e += 2) {
+          const float2 l = make_float2(f[e], f[e + 1]);
+          Pair2 w = quick_weights(s.scale, l, lowest);
+          if (by_p) {
+            sum.add(w.hi, w.lo);
+            const bool a0 = l.x > above_l, a1 = l.y > above_l;
+            sum_above.add(make_float2(a0 ? w.hi.x : 0.0f, a1 ? w.hi.y : 0.0f),
+                          make_float2(a0 ? w.lo.x : 0.0f, a1 ? w.lo.y : 0.0f));
+            const bool n0 = !a0 && l.x >= below_l, n1 = !a1 && l.y >= below_l;
+            if (n0 || n1) {
+              const unsigned at = static_cast<unsigned>(i * N + e - s.row.shift);
+              const u64 w0 = fixed_of(w.hi.x, w.lo.x), w1 = fixed_of(w.hi.y, w.lo.y);
+              if (n0 && !near(l.x, at, w0)) above += w0;
+              if (n1 && !near(l.y, at + 1, w1)) above += w1;
             }
+          } else {
+            if (mp > 0.0f) {
+              if ((w.hi.x > mp_lo && w.hi.x < mp_hi && w.hi.x != 1.0f) ||
+                  (w.hi.y > mp_lo && w.hi.y < mp_hi && w.hi.y != 1.0f))
+                mem()->doubt = 1;
+              if (w.hi.x < mp) w.hi.x = w.lo.x = 0.0f;
+              if (w.hi.y < mp) w.hi.y = w.lo.y = 0.0f;
+            }
+            sum.add(w.hi, w.lo);
           }
         }
-        break;
       }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+      if (by_p) {
+        all = sum.fixed();
+        above += sum_above.fixed();
+        kept = above;
+      } else {
+        kept = sum.fixed();
+      }
+    } else {
+#pragma unroll 1
+      for (int j = w0 + lane; j < w1; j += 64) {         // two pairs at once: a weight is a long chain
+        const float2 f0 = s.row.pair(j), f1 = s.row.pair_or_none(j + 32, w1);
+        if (f0.x < from_l && f0.y < from_l && f1.x < from_l && f1.y < from_l) continue;
+        u64 w[4];
+        s.weigh(f0, &w[0], &w[1]);
+        s.weigh(f1, &w[2], &w[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float l = e == 0 ? f0.x : e == 1 ? f0.y : e == 2 ? f1.x : f1.y;
+          const unsigned i = 2 * (j + 32 * (e / 2)) + (e & 1) - s.row.shift;
+          if (l < from_l || (l == border_l && rank_of(key_of(l), i) < k_border)) continue;
+          all += w[e];
+          if (by_p && l <= above_l && near(l, i, w[e])) continue;
+          above += w[e];
+          if (w[e] >= least) kept += w[e];
+        }
+      }
     }
+    kept = warp_sum64(kept);
+    if (lane == 0) {
+      mem()->run_lo[warp] = static_cast<unsigned>(kept);
+      mem()->run_hi[warp] = static_cast<unsigned>(kept >> 32);
+    }
+    if (by_p) {
+      s.block_sum(&above, &all);
+      // spans and whether the list holds them all to all ranks with the totals
+      if (tid < kSpans * 8 && (tid >> 5) < s.ranks)
+        s.of(tid >> 5)->span[s.rank][lane] = mass_of(mem()->span_lo[lane], mem()->span_hi[lane]);
+      const u64(*box)[8] = s.exchange(above, all | (mem()->near_n > kNear ? 1ull << 63 : 0));
+      above = all = 0;
+      bool many = false;
+      for (unsigned r = 0; r < s.ranks; ++r) {
+        above += box[0][r];
+        all += box[1][r] & ~(1ull << 63);
+        many |= (box[1][r] >> 63) != 0;
+      }
+      const u64 target = share_of(p, all);
+      u64 mass = 0;
+      for (unsigned r = 0; r < s.ranks; ++r) mass += mem()->span[r][lane];
+      const u64 incl = above + warp_scan64(mass, lane);
+      const unsigned reached = __ballot_sync(0xffffffffu, incl >= target);
+      if ((above >= target || reached == 0) && (b0 > 0 || b1 < kBins - 1)) {      // not in these bins: search them all
+        b0 = 0;
+        b1 = kBins - 1;
+        s.cluster.sync();                                // every rank has read its spans
+        continue;
+      }
+      const int hit = max(__ffs(reached) - 1, 0);
+      const u64 before = __shfl_sync(0xffffffffu, incl - mass, hit);
+      if (!many) {                                       // gather the span's elements from the lists
+        if (s.rank == 0 && tid == 0) mem()->list_n = 0;
+        s.cluster.sync();
+        Shared* head = s.of(0);
+        for (unsigned i = tid; i < mem()->near_n; i += kThreads) {
+          const Candidate c = mem()->near[i];
+          if (((s.bin(of_key(c.key)) - b0) >> coarse) != hit) continue;
+          const unsigned at = atomicAdd(&head->list_n, 1u);
+          if (at < kList) head->list[at] = c;
+        }
+        s.cluster.sync();
+        many = head->list_n > kList;
+      }
+      if (!many) {
+        s.border_of_list(before, target, exact ? 0 : slack_of(target));
+        if (!exact && mem()->border_doubt) continue;
+      } else {
+        s.cluster.sync();                                // every rank has read the list's size
+        if (!exact) continue;
+        s.turn = border_call<T, STAGED>(s, true, b0 + (hit << coarse), min(b0 + ((hit + 1) << coarse) - 1, b1),
+                                        k_border, before, target);
+      }
+      border = mem()->border;
+      // what is kept of the elements in the border's bins
+      auto keep = [&](unsigned key, unsigned not_idx, u64 w) {
+        if (((static_cast<u64>(key) << 32) | not_idx) < border || w < least) return;
+        const int of_run = (static_cast<int>((0xffffffffu - not_idx + s.row.shift) >> 1) - s.j0) / run;
+        add_mass(&mem()->run_lo[of_run], &mem()->run_hi[of_run], w);
+      };
+      if (mem()->near_n <= kNear) {
+        for (unsigned i = tid; i < mem()->near_n; i += kThreads)
+          keep(mem()->near[i].key, mem()->near[i].idx, mem()->near[i].w);
+      } else {
+#pragma unroll 1
+        for (int j = s.j0 + tid; j < s.j1; j += kThreads) {
+          const float2 f = s.row.pair(j);
+          const int n0 = s.bin(f.x), n1 = s.bin(f.y);
+          const bool on0 = f.x != -INFINITY && n0 >= b0 && n0 <= b1, on1 = f.y != -INFINITY && n1 >= b0 && n1 <= b1;
+          if (!on0 && !on1) continue;
+          u64 w[2];
+          s.weigh(f, &w[0], &w[1]);
+          const unsigned i = 2 * j - s.row.shift;
+          if (on0) keep(key_of(f.x), 0xffffffffu - i, w[0]);
+          if (on1) keep(key_of(f.y), 0xfffffffeu - i, w[1]);
+        }
+      }
+    }
+    __syncthreads();
+
+    // the draw: the rank, and in it the run, that the target lies in
+    const u64 mine = lane < kWarps ? mass_of(mem()->run_lo[lane], mem()->run_hi[lane]) : 0;
+    const u64 incl_runs = warp_scan64(mine, lane);
+    const u64 my_total = __shfl_sync(0xffffffffu, incl_runs, 31);
+    u64 before = 0, total = 0;
+    bool doubt = false;
+    {
+      const u64(*box)[8] = s.exchange(my_total, mem()->doubt);
+      for (unsigned r = 0; r < s.ranks; ++r) {
+        if (r < s.rank) before += box[0][r];
+        total += box[0][r];
+        doubt |= box[1][r] != 0;
+      }
+    }
+    if (doubt) continue;
+    const u64 target = __umul64hi(fraction_of(u), total);  // below total
+    const bool here = target >= before && target < before + my_total;
+    if (exact && !here) return;
+    int token = -1;
+    float token_l = 0.0f;
+    if (here) {
+      const int of_run = __ffs(__ballot_sync(0xffffffffu, before + incl_runs > target)) - 1;
+      before += __shfl_sync(0xffffffffu, incl_runs - mine, of_run);
+      const int r0 = s.j0 + of_run * run, r1 = min(r0 + run, s.j1);
+      const u64 slack = exact ? 0 : slack_of(total);
+#pragma unroll 1
+      for (int i0 = r0; i0 < r1; i0 += kThreads) {       // the whole CTA walks that run
+        const int j = i0 + tid;
+        u64 w[2] = {0, 0};
+        float2 f = make_float2(-INFINITY, -INFINITY);
+        if (j < r1) {
+          f = s.row.pair(j);
+          if (exact) {
+            s.weigh(f, &w[0], &w[1]);
+          } else {
+            const Pair2 q = quick_weights(s.scale, f, lowest);
+            w[0] = q.hi.x >= mp ? fixed_of(q.hi.x, q.lo.x) : 0;
+            w[1] = q.hi.y >= mp ? fixed_of(q.hi.y, q.lo.y) : 0;
+          }
+          const unsigned i = 2 * j - s.row.shift;
+          if (f.x == -INFINITY || rank_of(key_of(f.x), i) < border || w[0] < least) w[0] = 0;
+          if (f.y == -INFINITY || rank_of(key_of(f.y), i + 1) < border || w[1] < least) w[1] = 0;
+        }
+        u64 incl = warp_scan64(w[0] + w[1], lane);
+        __syncthreads();
+        if (lane == 31) mem()->warp_a[warp] = incl;
+        __syncthreads();
+        const u64 sums = warp_scan64(lane < kWarps ? mem()->warp_a[lane] : 0, lane);
+        incl += before + (warp ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0);
+        u64 at = incl - w[0] - w[1];
+        if (at <= target && target < incl) {             // one thread
+          const bool second = at + w[0] <= target;
+          if (second) at += w[0];
+          else incl = at + w[0];
+          if ((at == 0 || at + slack <= target) && target + slack < incl) {
+            token = 2 * j + (second ? 1 : 0) - s.row.shift;
+            token_l = second ? f.y : f.x;
+          }
+        }
+        before += __shfl_sync(0xffffffffu, sums, 31);
+        if (target < before) break;
+      }
+    }
+    if (!exact) {                                        // done unless the token lies too near its neighbours
+      const bool found = __syncthreads_or(token >= 0);
+      const u64(*box)[8] = s.exchange(found, 0);
+      for (unsigned r = 0; r < s.ranks; ++r) doubt |= box[0][r] != 0;
+      if (!doubt) continue;                              // (no rank has found it)
+    }
+    if (token >= 0) {
+      a.tokens[b] = token;
+      if (a.logprob) {
+        // ln(w / total) = (l - top) / T - ln(total / 2^43), both terms of one sign
+        const float d = token_l == s.scale.top ? 0.0f : (token_l - s.scale.top) / heat;
+        const u64 more = total > 1ull << kFix ? total - (1ull << kFix) : 0;
+        a.logprob[b] = d - log1pf(static_cast<float>(more) * (1.0f / static_cast<float>(1ull << kFix)));
+      }
+    }
+    return;
   }
-  s.cluster.sync();                                      // no rank leaves while others read its memory
 }
 
-template <typename T>
-cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
-  constexpr int N = Elem<T>::N;
-  const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
-  int ranks = 8;
-  const int64_t slice = (vectors + ranks - 1) / ranks * 16;
-  const int staged = slice <= kStageBytes ? 1 : 0;
-  const size_t smem = sizeof(Shared) + (staged ? static_cast<size_t>(slice) : 0);
-  const cudaError_t e = allow_smem<sample_kernel<T>>(static_cast<int>(sizeof(Shared)) + kStageBytes);
+template <typename T, bool STAGED>
+cudaError_t launch(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream) {
+  const cudaError_t e = allow_smem<sample_kernel<T, STAGED>>(static_cast<int>(sizeof(Shared)) +
+                                                             (STAGED ? kStageBytes : 0));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.batch * ranks));
@@ -712,13 +1143,23 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, staged);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a);
+}
+
+template <typename T>
+cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
+  constexpr int N = Elem<T>::N;
+  const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
+  const int ranks = 8;   // RANKS
+  const int64_t slice = (vectors + ranks - 1) / ranks * 16;
+  if (slice <= kStageBytes) return launch<T, true>(a, ranks, sizeof(Shared) + static_cast<size_t>(slice), stream);
+  return launch<T, false>(a, ranks, sizeof(Shared), stream);
 }
 
 }  // namespace
 
 cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t stream) {
-  return a.f32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);
+  return a.f32 ? plan<float>(a, stream) : plan<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace gbf
