@@ -29,9 +29,10 @@
 //      ppm and so the few bins the border can lie in; one pass over the weights
 //      then gives the total, the mass above those bins, and the masses within
 //      them;
-//   3. the border bin's few elements are gathered on one CTA and ranked by
-//      comparison; a bin with too many of them (equal or almost equal logits)
-//      is first cut by (logit, index).
+//   3. the few elements around the border (of a bin, or of 64ths of bins) are
+//      gathered on every CTA of the cluster and sorted there; where they are too
+//      many (thousands of equal or almost equal logits) they are first cut by
+//      (logit, index).
 // The pass of step 2 also sums each warp's run of the kept elements above the
 // border's bins, so the draw only adds the few within them.  A row that asks for
 // neither top-k nor top-p takes that pass alone.
@@ -68,11 +69,12 @@ constexpr int kCells = kBins / 2;           // mass histogram in the same memory
 // (46 ppm), as long as no more than 4095 elements of a CTA fall in it (otherwise the border turns out to lie outside the
 // bins searched, and all are).  Those of the last bin (weights below 2^-31.9) add vocab 2^-31.9 of the total at most.
 constexpr float kBinError = 60e-6f, kLastBinError = 2.6e-10f;
-constexpr int kList = 512;                  // candidates ranked by comparison
+constexpr int kList = 1024;                 // candidates that are sorted, an equal share of each rank's
 constexpr int kGroup = 64;                  // bins per group (and groups): the two steps of a search over the bins
-constexpr int kNear = 1024;                 // this rank's elements in the bins that may hold top-p's border
+constexpr int kFew = 128;                   // up to this many are compared with each other
+constexpr int kNear = 2048;                 // this rank's elements in the bins that may hold top-p's border
 constexpr int kFilterVectors = 512;         // slices of more 16-byte vectors are first done in float32
-constexpr int kSpans = 32;                  // parts the bins that may hold top-p's border are cut into
+constexpr int kSpans = 32;                  // parts that the bins that may hold top-p's border are cut into
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
 constexpr float kLeastTemperature = 1e-30f;
@@ -92,36 +94,29 @@ __device__ const u64 kPow[64] = {
     0xf5257d15248ull, 0xf7d0df730adull, 0xfa83b2db723ull, 0xfd3e0c0cf48ull,
 };
 
-struct Candidate {
-  unsigned key, idx;           // key, ~index: a rank
-  u64 w;
-};
-
 // What a row's threads share.  One per CTA; ranks read and write each other's.
 struct __align__(16) Shared {
   unsigned hist[kBins];
   u64 pow[64];
+  u64 list[kList];             // candidates of every rank, as (key, ~index)
   union {
     struct {
       float group[8][kGroup];  // every rank's sums of the groups of bins,
       float bin[2][8][kGroup]; // and of the bins of a group, for two targets
     } search;
-    struct {
-      Candidate list[kList];   // rank 0's: candidates gathered
-      Candidate near[kNear];   // this rank's elements in the bins that may hold top-p's border
-    };
+    u64 near[kNear];           // this rank's elements in the bins that may hold top-p's border
   };
   u64 span[8][kSpans];         // every rank's masses of the spans
   unsigned span_lo[kSpans], span_hi[kSpans];     // this rank's, being summed
   unsigned run_lo[kWarps], run_hi[kWarps];       // kept mass of each warp's run
   u64 warp_a[kWarps], warp_b[kWarps];
   u64 box[2][2][8];            // totals of the ranks: two boxes in turn, two values each
-  unsigned list_n, near_n;
-  unsigned doubt, border_doubt;  // a float32 decision that did not clear its bound (this rank's; the border's)
+  unsigned list_n[8];          // how many every rank has
+  unsigned mine_n, near_n;     // this rank's candidates, and elements near the border
+  unsigned doubt;              // a float32 decision of this rank that did not clear its bound
   // found by one thread of the cluster, written to all ranks
   int found;
   u64 before;
-  u64 border;                  // (key, ~index) of the last element kept
 };
 
 // The CTA's shared memory: what its threads share, then its slice of the row.
@@ -142,7 +137,8 @@ GBF_DEVICE u64 rank_of(unsigned key, unsigned idx) { return (static_cast<u64>(ke
 struct RowScale {
   float top;               // largest logit
   float c_hi, c_lo;        // log2(e) / T
-  float c_bin, c_place;    // bins, and 64ths of a bin, per unit of logit
+  float c_place;           // places (64ths of a bin) per unit of logit, and about its inverse
+  float c_inverse;
 };
 
 GBF_DEVICE float2 two(float x) { return make_float2(x, x); }
@@ -406,7 +402,7 @@ struct Sampler {
   unsigned rank, ranks;
   Row<T, STAGED> row;
   RowScale scale;
-  int j0, j1;              // this rank's pairs
+  int v0, v1, j0, j1;      // this rank's vectors, and pairs
   int tid, lane, warp;
   int turn;                // box of the next exchange
 
@@ -425,7 +421,6 @@ struct Sampler {
   GBF_DEVICE int place(float l) {
     return scale.top == INFINITY ? (l == INFINITY ? 32 : 64 * kBins - 1) : place_of(scale, l);
   }
-  GBF_DEVICE int bin(float l) { return place(l) >> 6; }
 
   // Sums over the block of every thread's a and b, the same in all threads.
   GBF_DEVICE void block_sum(u64* a, u64* b) {
@@ -566,98 +561,171 @@ struct Sampler {
     cluster.sync();
   }
 
-  // Rank 0 ranks its list by comparison: the last of them before which less
-  // than `target` lies, to all ranks' borders.  Behind a barrier that completes
-  // the list; ends with one.
-  // slack > 0: the border is in doubt unless it clears the target by that much.
-  GBF_DEVICE void border_of_list(u64 before, u64 target, u64 slack) {
-    if (rank == 0) {
-      const int n = static_cast<int>(mem()->list_n);
-      u64 last = ~0ull;
-      bool sure = slack == 0;
-#pragma unroll 1
-      for (int i = tid; i < n; i += kThreads) {
-        const Candidate c = mem()->list[i];
-        const u64 k = (static_cast<u64>(c.key) << 32) | c.idx;
-        u64 at = before;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-          const Candidate o = mem()->list[j];
-          if (((static_cast<u64>(o.key) << 32) | o.idx) > k) at += o.w;
-        }
-        if (at < target) last = k < last ? k : last;
-        if (at < target && at + c.w >= target) sure |= (at == 0 || at + slack < target) && at + c.w >= target + slack;
-      }
-      last = ~warp_max64(~last);
-      __syncthreads();
-      if (lane == 0) mem()->warp_a[warp] = last;
-      sure = __syncthreads_or(sure);
-      last = ~warp_max64(lane < kWarps ? ~mem()->warp_a[lane] : 0);
-      if (tid < ranks) {
-        of(tid)->border = last;
-        of(tid)->border_doubt = !sure;
-      }
-    }
+  // A candidate of this rank to every rank's list.
+  GBF_DEVICE void offer(u64 k) {
+    const unsigned share = kList / ranks, at = atomicAdd(&mem()->mine_n, 1u);
+    if (at < share)
+      for (unsigned r = 0; r < ranks; ++r) of(r)->list[rank * share + at] = k;
+  }
+  // Closes the lists (the threads' offers are behind a barrier of the block): a
+  // cluster barrier; false when one of them is too short.
+  GBF_DEVICE bool close_lists() {
+    if (tid < ranks) of(tid)->list_n[rank] = mem()->mine_n;
     cluster.sync();
+    bool fits = true;
+    for (unsigned r = 0; r < ranks; ++r) fits = fits && mem()->list_n[r] <= kList / ranks;
+    return fits;
+  }
+  struct Border {
+    u64 rank;                  // (key, ~index) of the last element kept
+    bool sure;                 // it clears the target by the slack (or slack is 0)
+  };
+  // Ranks the lists' candidates, the same in every rank, in the histogram's memory
+  // (a few by comparison with each other, more by a bitonic sort, larger first):
+  // the last of them before which less than `target` lies, `before` lying before
+  // all.  value(l): what a candidate counts for.
+  template <typename Value>
+  GBF_DEVICE Border border_of_lists(u64 before, u64 target, u64 slack, Value value) {
+    static_assert(2 * kList * sizeof(u64) <= sizeof(unsigned) * kBins && kFew <= kThreads, "");
+    u64* order = reinterpret_cast<u64*>(mem()->hist);
+    unsigned n = 0;
+    for (unsigned r = 0; r < ranks; ++r) {
+      const unsigned c = min(mem()->list_n[r], kList / ranks);
+      for (unsigned i = tid; i < c; i += kThreads) order[n + i] = mem()->list[r * (kList / ranks) + i];
+      n += c;
+    }
+    u64 last = ~0ull;
+    bool sure = false;
+    auto decide = [&](u64 k, u64 at, u64 w) {
+      if (at >= target) return;
+      last = k;
+      sure = at + w >= target + slack && (at == 0 || at + slack < target);
+    };
+    if (n <= kFew) {
+      u64* weight = order + kList;
+      __syncthreads();
+      u64 k = 0, w = 0, at = before;
+      if (tid < n) {
+        k = order[tid];
+        weight[tid] = w = value(of_key(static_cast<unsigned>(k >> 32)));
+      }
+      __syncthreads();
+      if (tid < n) {
+#pragma unroll 4
+        for (unsigned j = 0; j < n; ++j)
+          if (order[j] > k) at += weight[j];
+        decide(k, at, w);
+      }
+      return conclude(last, sure);
+    }
+    unsigned size = 2 * kFew;
+    while (size < n) size *= 2;
+    for (unsigned i = n + tid; i < size; i += kThreads) order[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (unsigned width = 2; width <= size; width *= 2)
+#pragma unroll 1
+      for (unsigned step = width / 2; step > 0; step /= 2) {
+        if (tid < size / 2) {
+          const unsigned i = 2 * tid - (tid & (step - 1)), j = i + step;
+          const u64 x = order[i], y = order[j];
+          if ((x < y) == ((i & width) == 0)) {
+            order[i] = y;
+            order[j] = x;
+          }
+        }
+        __syncthreads();
+      }
+    // the border: two candidates per thread
+    constexpr int kPer = kList / kThreads;
+    u64 w[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const unsigned j = tid * kPer + i;
+      w[i] = j < n ? value(of_key(static_cast<unsigned>(order[j] >> 32))) : 0;
+      sum += w[i];
+    }
+    const u64 incl = warp_scan64(sum, lane);
+    if (lane == 31) mem()->warp_a[warp] = incl;
+    __syncthreads();
+    const u64 warps = warp_scan64(lane < kWarps ? mem()->warp_a[lane] : 0, lane);
+    u64 at = before + incl - sum + (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const unsigned j = tid * kPer + i;
+      if (j < n) decide(order[j], at, w[i]);
+      at += w[i];
+    }
+    return conclude(last, sure);
+  }
+  // the smallest of the threads' borders
+  GBF_DEVICE Border conclude(u64 last, bool sure) {
+    last = ~warp_max64(~last);
+    __syncthreads();
+    if (lane == 0) mem()->warp_a[warp] = last;
+    Border out;
+    out.sure = __syncthreads_or(sure);
+    out.rank = ~warp_max64(lane < kWarps ? ~mem()->warp_a[lane] : 0);
+    return out;
   }
 
   // The rank (key, ~index) of the last element before which less than `target`
-  // (elements, or mass) lies, to mem()->border of all ranks.  It is one of the
-  // elements with bins b0..b1 and ranks >= lo, before which `before` lies.
-  GBF_DEVICE void border_within(bool by_mass, int b0, int b1, u64 lo, u64 before, u64 target) {
+  // (elements, or mass) lies.  It is one of the elements with places p0..p1 and
+  // ranks >= lo, before which `before` lies.
+  GBF_DEVICE u64 border_within(bool by_mass, int p0, int p1, u64 lo, u64 before, u64 target) {
     u64 hi = ~0ull;
     int s = 0;
-    // these bins' logits lie between these two, with room for the roundings
+    // these places' logits lie between these two, with room for the roundings
     float l_hi = INFINITY, l_lo = -FLT_MAX;
     if (scale.top != INFINITY) {
-      if (b0 > 0) l_hi = scale.top - (b0 - 1) / scale.c_bin;
-      if (b1 < kBins - 1) l_lo = fmaxf(scale.top - (b1 + 1) / scale.c_bin, -FLT_MAX);
+      if (p0 >= 64) l_hi = scale.top - (p0 - 64) * scale.c_inverse;
+      if (p1 < 64 * (kBins - 1)) l_lo = fmaxf(scale.top - (p1 + 64) * scale.c_inverse, -FLT_MAX);
     }
-    // rounds: gather the candidates on rank 0; when there are too many, the range of their ranks, then (and again)
-    // that range cut into cells, of which the target's one stays, and gather again
+    // rounds: gather the candidates; when there are too many, the range of their ranks, then (and again) that range
+    // cut into cells, of which the target's one stays, and gather again
     enum { kGather, kRange, kCut };
     int level = 0;
     for (int todo = kGather;;) {
-      Shared* head = of(0);
       u64 mn = ~0ull, mx = 0;
-      if (todo == kGather && rank == 0 && tid == 0) mem()->list_n = 0;
+      if (todo == kGather && tid == 0) mem()->mine_n = 0;
       if (todo == kCut) clear();
-      cluster.sync();                                    // also: every rank is done with the last histogram
-      float2 next = row.pair_or_none(j0 + tid, j1);
+      if (todo == kGather) __syncthreads();
+      else cluster.sync();                               // every rank is done with the last histogram
 #pragma unroll 1
-      for (int j = j0 + tid; j < j1; j += kThreads) {
-        const float2 f = next;
-        next = row.pair_or_none(j + kThreads, j1);
-        bool on[2] = {f.x >= l_lo && f.x <= l_hi, f.y >= l_lo && f.y <= l_hi};
-        if (!on[0] && !on[1]) continue;
-        u64 k[2], w[2] = {1, 1};
+      for (int v = v0 + tid; v < v1; v += kThreads) {
+        float f[Row<T, STAGED>::N];
+        row.get(v, f);
+        bool any = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float l = e ? f.y : f.x;
-          k[e] = rank_of(key_of(l), 2 * j + e - row.shift);
-          const int n = bin(l);
-          on[e] = on[e] && k[e] >= lo && k[e] <= hi && n >= b0 && n <= b1;
-        }
-        if (!on[0] && !on[1]) continue;
-        if (by_mass && todo != kRange) weigh(f, &w[0], &w[1]);
+        for (int e = 0; e < Row<T, STAGED>::N; ++e) any = any || (f[e] >= l_lo && f[e] <= l_hi);
+        if (!any) continue;
+#pragma unroll 1
+        for (int e = 0; e < Row<T, STAGED>::N; e += 2) {
+          const int j = v * (Row<T, STAGED>::N / 2) + e / 2;
+          const float2 q = row.pair(j);
+          u64 w[2] = {1, 1};
+          if (by_mass && todo == kCut) weigh(q, &w[0], &w[1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (!on[e]) continue;
-          if (todo == kGather) {
-            const unsigned at = atomicAdd(&head->list_n, 1u);
-            if (at < kList) head->list[at] = {static_cast<unsigned>(k[e] >> 32), static_cast<unsigned>(k[e]), w[e]};
-          } else if (todo == kRange) {
-            mn = k[e] < mn ? k[e] : mn;
-            mx = k[e] > mx ? k[e] : mx;
-          } else {
-            const int cell = static_cast<int>((hi - k[e]) >> s);
-            add_mass(&mem()->hist[cell], &mem()->hist[kCells + cell], w[e]);
+          for (int i = 0; i < 2; ++i) {
+            const float l = i ? q.y : q.x;
+            const u64 k = rank_of(key_of(l), 2 * j + i - row.shift);
+            const int n = place(l);
+            if (l < l_lo || l > l_hi || k < lo || k > hi || n < p0 || n > p1) continue;
+            if (todo == kGather) {
+              offer(k);
+            } else if (todo == kRange) {
+              mn = k < mn ? k : mn;
+              mx = k > mx ? k : mx;
+            } else {
+              const int cell = static_cast<int>((hi - k) >> s);
+              add_mass(&mem()->hist[cell], &mem()->hist[kCells + cell], w[i]);
+            }
           }
         }
       }
       if (todo == kGather) {
-        cluster.sync();
-        if (head->list_n <= kList || level == 8) break;
+        __syncthreads();
+        if (close_lists() || level == 8) break;
         todo = level == 0 ? kRange : kCut;
       } else if (todo == kRange) {
         mn = ~warp_max64(~mn);
@@ -680,7 +748,7 @@ struct Sampler {
         todo = kCut;
       } else {
         find_cell(before, target);
-        if (mem()->found >= 0) {                            // (always: the target lies within)
+        if (mem()->found >= 0) {                         // (always: the target lies within)
           before = mem()->before;
           hi -= static_cast<u64>(mem()->found) << s;
           const u64 span = (1ull << s) - 1;
@@ -694,17 +762,25 @@ struct Sampler {
         while (((hi - lo) >> s) >= kCells) ++s;
       }
     }
-    border_of_list(before, target, 0);
+    return border_of_lists(before, target, 0, [&](float l) {
+             u64 w0 = 1, w1;
+             if (by_mass) weigh(two(l), &w0, &w1);
+             return w0;
+           }).rank;
   }
 };
 
 // border_within as a call (it is needed in two places and long), on a copy, so
 // that the caller's object stays in registers.
+struct BorderTurn {
+  u64 border;
+  int turn;
+};
 template <typename T, bool STAGED>
-__device__ __noinline__ int border_call(Sampler<T, STAGED> s, bool by_mass, int b0, int b1, u64 lo, u64 before,
-                                        u64 target) {
-  s.border_within(by_mass, b0, b1, lo, before, target);
-  return s.turn;
+__device__ __noinline__ BorderTurn border_call(Sampler<T, STAGED> s, bool by_mass, int p0, int p1, u64 lo, u64 before,
+                                               u64 target) {
+  const u64 border = s.border_within(by_mass, p0, p1, lo, before, target);
+  return {border, s.turn};
 }
 
 template <typename T, bool STAGED>
@@ -728,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.row.vocab = a.vocab;
   const int vectors = (s.row.shift + a.vocab + N - 1) / N;
   const int per = (vectors + s.ranks - 1) / s.ranks;
-  const int v0 = s.row.v0 = min(static_cast<int>(s.rank) * per, vectors);
-  const int v1 = min(v0 + per, vectors);
+  const int v0 = s.v0 = s.row.v0 = min(static_cast<int>(s.rank) * per, vectors);
+  const int v1 = s.v1 = min(v0 + per, vectors);
   s.j0 = v0 * (N / 2);
   s.j1 = v1 * (N / 2);
   const float temp = a.temperature ? a.temperature[b] : 1.0f;
@@ -737,6 +813,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const float p = a.top_p ? a.top_p[b] : 1.0f;
   const float mp = a.min_p ? a.min_p[b] : 0.0f;
   const float u = a.uniform[b];
+
+  const float heat = fmaxf(temp, kLeastTemperature);
+  {
+    // log2(e) / T in two parts: the quotient of the high part, and the quotient of what it leaves
+    constexpr float kHi = 1.44269504088896341f;
+    constexpr float kLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kHi));
+    s.scale.c_hi = __fdiv_rn(kHi, heat);
+    s.scale.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-s.scale.c_hi, heat, kHi), kLo), heat);
+    s.scale.c_place = s.scale.c_hi * (kBinsPerOctave * 64.0f);
+    s.scale.c_inverse = heat * (0.693147180559945f / (kBinsPerOctave * 64.0f));
+  }
 
   // pass 1: the only read of HBM; the largest logit
   float most = -INFINITY;
@@ -805,16 +892,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     return;
   }
-  const float heat = fmaxf(temp, kLeastTemperature);
-  {
-    // log2(e) / T in two parts: the quotient of the high part, and the quotient of what it leaves
-    constexpr float kHi = 1.44269504088896341f;
-    constexpr float kLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kHi));
-    s.scale.c_hi = __fdiv_rn(kHi, heat);
-    s.scale.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-s.scale.c_hi, heat, kHi), kLo), heat);
-    s.scale.c_bin = s.scale.c_hi * kBinsPerOctave;
-    s.scale.c_place = s.scale.c_bin * 64.0f;
-  }
   const u64 least = mp > 0.0f ? __float2ull_ru(mp * static_cast<float>(1ull << kFix)) : 0;
 
   const bool by_k = k > 0 && k < a.vocab, by_p = p < 1.0f;
@@ -852,8 +929,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;
       b1 = hit[1].at < 0 ? kBins - 1 : hit[1].at;
     } else if (hit[0].at >= 0) {                         // else fewer than k candidates
-      s.turn = border_call<T, STAGED>(s, false, hit[0].at, hit[0].at, 0, static_cast<u64>(hit[0].before), static_cast<u64>(k));
-      border = mem()->border;
+      const BorderTurn found = border_call<T, STAGED>(s, false, 64 * hit[0].at, 64 * hit[0].at + 63, 0,
+                                                      static_cast<u64>(hit[0].before), static_cast<u64>(k));
+      border = found.border;
+      s.turn = found.turn;
       b1 = hit[0].at;
     }
   }
@@ -861,15 +940,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // A contiguous run of vectors per warp.
   const int run_v = (v1 - v0 + kWarps - 1) / kWarps, run = run_v * (N / 2);
   const int u0 = min(v0 + warp * run_v, v1), u1 = min(u0 + run_v, v1);
-  const int w0 = min(s.j0 + warp * run, s.j1), w1 = min(w0 + run, s.j1);
   // a finite logit below this one has a weight below min_p by more than any rounding
   float floor_l = -FLT_MAX;
   if (mp > 0.0f && s.scale.top != INFINITY)
-    floor_l = fmaxf(__fadd_rd(s.scale.top, (log2f(mp) - 0.01f) / s.scale.c_hi * 1.0001f), -FLT_MAX);
+    floor_l = fmaxf(__fadd_rd(s.scale.top, (log2f(mp) - 0.01f) * heat * 0.69322f), -FLT_MAX);
   const u64 k_border = border;
   const float border_l = border ? of_key(static_cast<unsigned>(border >> 32)) : -FLT_MAX;
   const float from_l = by_p ? border_l : fmaxf(border_l, floor_l);
-  const float lowest = fmaxf(s.scale.top - 60.0f / s.scale.c_hi, -FLT_MAX);
+  const float lowest = fmaxf(s.scale.top - 41.5f * heat, -FLT_MAX);
   // float32 first: where there is much to weigh (top-k leaves little), and no two criteria meet in one sum
   bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || s.scale.top == INFINITY;
 
@@ -879,24 +957,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // (a logit above above_l lies in a bin before b0, one below below_l behind b1)
     float above_l = INFINITY, below_l = -FLT_MAX;
     if (by_p && s.scale.top != INFINITY) {
-      if (b0 > 0) above_l = s.scale.top - (b0 - 1) / s.scale.c_bin;
-      if (b1 < kBins - 1) below_l = fmaxf(s.scale.top - (b1 + 1) / s.scale.c_bin, -FLT_MAX);
+      if (b0 > 0) above_l = s.scale.top - 64 * (b0 - 1) * s.scale.c_inverse;
+      if (b1 < kBins - 1) below_l = fmaxf(s.scale.top - 64 * (b1 + 2) * s.scale.c_inverse, -FLT_MAX);
     }
-    int coarse = 0;
-    while (((b1 - b0) >> coarse) >= kSpans) ++coarse;
+    const int p0 = 64 * b0, p1 = 64 * b1 + 63;           // the bins' places, in spans of 2^coarse
+    const int coarse = max(0, 32 - __clz(p1 - p0) - 5);
     if (tid < kSpans) mem()->span_lo[tid] = mem()->span_hi[tid] = 0;
-    if (tid == 0) mem()->near_n = mem()->doubt = 0;
+    if (tid == 0) mem()->near_n = mem()->mine_n = mem()->doubt = 0;
     __syncthreads();
     u64 kept = 0, above = 0, all = 0;
+    auto weight_of = [&](float l) {                      // the weight that this round's sums are made of
+      u64 w0, w1;
+      if (exact) {
+        s.weigh(two(l), &w0, &w1);
+      } else {
+        const Pair2 w = quick_weights(s.scale, two(l), lowest);
+        w0 = fixed_of(w.hi.x, w.lo.x);
+      }
+      return w0;
+    };
     // an element that may lie in the border's bins: true when it does
     auto near = [&](float l, unsigned i, u64 w) {
-      const int n = s.bin(l);
-      if (n < b0) return false;
-      if (n <= b1) {
-        const int span = (n - b0) >> coarse;
+      const int n = s.place(l);
+      if (n < p0) return false;
+      if (n <= p1) {
+        const int span = (n - p0) >> coarse;
         add_mass(&mem()->span_lo[span], &mem()->span_hi[span], w);
         const unsigned at = atomicAdd(&mem()->near_n, 1u);
-        if (at < kNear) mem()->near[at] = {key_of(l), 0xffffffffu - i, w};
+        if (at < kNear) mem()->near[at] = rank_of(key_of(l), i);
       }
       return true;
     };
@@ -944,21 +1032,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     } else {
 #pragma unroll 1
-      for (int j = w0 + lane; j < w1; j += 64) {         // two pairs at once: a weight is a long chain
-        const float2 f0 = s.row.pair(j), f1 = s.row.pair_or_none(j + 32, w1);
-        if (f0.x < from_l && f0.y < from_l && f1.x < from_l && f1.y < from_l) continue;
-        u64 w[4];
-        s.weigh(f0, &w[0], &w[1]);
-        s.weigh(f1, &w[2], &w[3]);
+      for (int i = u0 + lane; i < u1; i += 32) {
+        float f[N];
+        s.row.get(i, f);
+        bool any = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float l = e == 0 ? f0.x : e == 1 ? f0.y : e == 2 ? f1.x : f1.y;
-          const unsigned i = 2 * (j + 32 * (e / 2)) + (e & 1) - s.row.shift;
-          if (l < from_l || (l == border_l && rank_of(key_of(l), i) < k_border)) continue;
-          all += w[e];
-          if (by_p && l <= above_l && near(l, i, w[e])) continue;
-          above += w[e];
-          if (w[e] >= least) kept += w[e];
+        for (int e = 0; e < N; ++e) any = any || f[e] >= from_l;
+        if (!any) continue;
+#pragma unroll
+        for (int q = 0; q < N; q += 4) {                 // two pairs at once: a weight is a long chain
+          u64 w[4];
+          s.weigh(make_float2(f[q], f[q + 1]), &w[0], &w[1]);
+          s.weigh(make_float2(f[q + 2], f[q + 3]), &w[2], &w[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float l = f[q + e];
+            const unsigned at = static_cast<unsigned>(i * N + q + e - s.row.shift);
+            if (l < from_l || (l == border_l && rank_of(key_of(l), at) < k_border)) continue;
+            all += w[e];
+            if (by_p && l <= above_l && near(l, at, w[e])) continue;
+            above += w[e];
+            if (w[e] >= least) kept += w[e];
+          }
         }
       }
     }
@@ -993,50 +1088,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       const int hit = max(__ffs(reached) - 1, 0);
       const u64 before = __shfl_sync(0xffffffffu, incl - mass, hit);
-      if (!many) {                                       // gather the span's elements from the lists
-        if (s.rank == 0 && tid == 0) mem()->list_n = 0;
-        s.cluster.sync();
-        Shared* head = s.of(0);
+      if (!many) {                                       // the span's elements, from the list
         for (unsigned i = tid; i < mem()->near_n; i += kThreads) {
-          const Candidate c = mem()->near[i];
-          if (((s.bin(of_key(c.key)) - b0) >> coarse) != hit) continue;
-          const unsigned at = atomicAdd(&head->list_n, 1u);
-          if (at < kList) head->list[at] = c;
+          const u64 c = mem()->near[i];
+          if (((s.place(of_key(static_cast<unsigned>(c >> 32))) - p0) >> coarse) == hit) s.offer(c);
         }
-        s.cluster.sync();
-        many = head->list_n > kList;
+        __syncthreads();
+        many = !s.close_lists();
       }
       if (!many) {
-        s.border_of_list(before, target, exact ? 0 : slack_of(target));
-        if (!exact && mem()->border_doubt) continue;
+        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target), weight_of);
+        if (!exact && !found.sure) continue;
+        border = found.rank;
       } else {
-        s.cluster.sync();                                // every rank has read the list's size
+        s.cluster.sync();                                // every rank has read the lists' sizes
         if (!exact) continue;
-        s.turn = border_call<T, STAGED>(s, true, b0 + (hit << coarse), min(b0 + ((hit + 1) << coarse) - 1, b1),
-                                        k_border, before, target);
+        const BorderTurn found = border_call<T, STAGED>(
+            s, true, p0 + (hit << coarse), min(p0 + ((hit + 1) << coarse) - 1, p1), k_border, before, target);
+        border = found.border;
+        s.turn = found.turn;
       }
-      border = mem()->border;
       // what is kept of the elements in the border's bins
-      auto keep = [&](unsigned key, unsigned not_idx, u64 w) {
-        if (((static_cast<u64>(key) << 32) | not_idx) < border || w < least) return;
-        const int of_run = (static_cast<int>((0xffffffffu - not_idx + s.row.shift) >> 1) - s.j0) / run;
+      auto keep = [&](u64 rank) {
+        if (rank < border) return;
+        const u64 w = weight_of(of_key(static_cast<unsigned>(rank >> 32)));
+        if (w < least) return;
+        const int of_run = (static_cast<int>((0xffffffffu - static_cast<unsigned>(rank) + s.row.shift) >> 1) - s.j0) / run;
         add_mass(&mem()->run_lo[of_run], &mem()->run_hi[of_run], w);
       };
       if (mem()->near_n <= kNear) {
-        for (unsigned i = tid; i < mem()->near_n; i += kThreads)
-          keep(mem()->near[i].key, mem()->near[i].idx, mem()->near[i].w);
+#pragma unroll 1
+        for (unsigned i = tid; i < mem()->near_n; i += kThreads) keep(mem()->near[i]);
       } else {
 #pragma unroll 1
-        for (int j = s.j0 + tid; j < s.j1; j += kThreads) {
-          const float2 f = s.row.pair(j);
-          const int n0 = s.bin(f.x), n1 = s.bin(f.y);
-          const bool on0 = f.x != -INFINITY && n0 >= b0 && n0 <= b1, on1 = f.y != -INFINITY && n1 >= b0 && n1 <= b1;
-          if (!on0 && !on1) continue;
-          u64 w[2];
-          s.weigh(f, &w[0], &w[1]);
-          const unsigned i = 2 * j - s.row.shift;
-          if (on0) keep(key_of(f.x), 0xffffffffu - i, w[0]);
-          if (on1) keep(key_of(f.y), 0xfffffffeu - i, w[1]);
+        for (int i = 2 * s.j0 + tid; i < 2 * s.j1; i += kThreads) {
+          const float2 f = s.row.pair(i / 2);
+          const float l = i & 1 ? f.y : f.x;
+          const int n = s.place(l);
+          if (l != -INFINITY && n >= p0 && n <= p1) keep(rank_of(key_of(l), i - s.row.shift));
         }
       }
     }
