@@ -9,21 +9,23 @@
 // as the bound for any group of up to some hundred heads.
 //
 // Work split: the unit is a tile of 16 cached tokens of one (request, KV head)
-// item.  All items' tiles in a row (requests, then KV heads, then tokens) are
-// cut into equal contiguous ranges, one per CTA of a grid that just fills the
-// GPU, so a ragged batch loads every SM alike and no length needs to be known
-// on the host.  Each CTA finds its range itself: a scan over the lengths.  An
-// item whose tiles lie in one CTA is finished there; one that a range border
-// cuts leaves a partial (max, sum, unnormalised output, float32) per CTA in
-// the workspace, and a second small kernel joins the partials in CTA order,
-// so results do not depend on timing.
+// item, and kOwn units per item for what an item costs by itself.  All
+// items' units in a row (requests, then KV heads, then tokens) are cut into
+// equal contiguous ranges, one per CTA of a grid that just fills the GPU, so a
+// ragged batch loads every SM alike and no length needs to be known on the
+// host.  Each CTA finds its range itself: a scan over the lengths.  An item
+// whose tiles lie in one CTA is finished there; one that a range border cuts
+// leaves a partial (max, sum, unnormalised output, float32) per CTA in the
+// workspace, and a second small kernel joins the partials in CTA order, so
+// results do not depend on timing.
 //
 // Inside a CTA the warps take a range's tiles in turn and never wait for one
 // another within an item: each has its own ring of stages (16 K rows and 16 V
 // rows) filled by 16-byte cp.async, its own running maximum and sum, and its
 // own accumulators; the ring runs on across item borders, so the next item's
 // rows are on their way while the warps' results are joined through shared
-// memory.  Scores are mma.m16n8k16 with the group's heads as the 16 rows and
+// memory.  A short item is one warp's alone: the warps take such items in turn
+// and finish them without a barrier.  Scores are mma.m16n8k16 with the group's heads as the 16 rows and
 // the tokens as columns; the score accumulators are then, element for
 // element, the A operand of the product with V.
 //
@@ -39,6 +41,10 @@ namespace gbf {
 namespace {
 
 constexpr int kTile = 16;              // tokens per tile
+// An item is one warp's alone (joining the warps costs about as much as four tiles) when it has at most 4 tiles, 8
+// where a CTA has two items on average, and up to 16 as long as that is a 16th of the CTA's units.
+constexpr int kSoloOne = 4, kSoloTwo = 8, kSoloMost = 16;
+constexpr int kOwn = 4;                // units an item counts beside its tiles
 constexpr int kSms = 152;
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -106,7 +112,7 @@ GBF_DEVICE void mma_bf16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
 // ------------------------------------------------------------- the work split
 
 struct Request {
-  int len, lo, tiles;     // cached tokens [lo, len), their tiles (at least one: an empty row still writes its output)
+  int len, lo, tiles;     // cached tokens [lo, len) and their tiles; an item is kOwn + tiles units, the tiles last
 };
 
 GBF_DEVICE Request request_of(const PagedAttnArgs& a, int b) {
@@ -117,7 +123,6 @@ GBF_DEVICE Request request_of(const PagedAttnArgs& a, int b) {
   if (r.len > room) r.len = static_cast<int>(room);
   r.lo = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
   r.tiles = (r.len - r.lo + kTile - 1) / kTile;
-  if (r.tiles < 1) r.tiles = 1;
   return r;
 }
 
@@ -142,7 +147,7 @@ GBF_DEVICE Place locate(const PagedAttnArgs& a, int64_t c, bool report) {
   int64_t mine = 0;
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
-    mine += request_of(a, b).tiles;
+    mine += request_of(a, b).tiles + kOwn;
     const int len = a.lens[b];
     bad |= len < 0 || len > static_cast<int64_t>(a.max_blocks) * a.block_size;
   }
@@ -171,7 +176,7 @@ GBF_DEVICE Place locate(const PagedAttnArgs& a, int64_t c, bool report) {
     int64_t rest = u - base;
     int b = b0;
     for (;;) {
-      const int64_t n = static_cast<int64_t>(request_of(a, b).tiles) * items;
+      const int64_t n = static_cast<int64_t>(request_of(a, b).tiles + kOwn) * items;
       if (rest < n) break;
       rest -= n;
       ++b;
@@ -195,23 +200,45 @@ struct Cursor {
   Request r;
   int b, item;            // request; (KV head, row tile) within it
   int t0, t1;             // the segment: tiles of the item that lie in the range
-  int t;                  // this warp's tile
+  int t, step;            // this warp's tile, and to its next one
+  int turn, solo_turn;    // warps' turns: at the segment's first tile; at the next short item
+  int most_solo;
+  bool whole, solo;       // the segment is the whole item; and one warp's
+  bool mine;              // this warp takes part in it
   bool done;
 
   GBF_DEVICE void start(const PagedAttnArgs& a, const Place& p, int64_t units, int warp) {
     b = p.b;
     r = request_of(a, b);
-    item = static_cast<int>(p.rest / r.tiles);
-    t0 = static_cast<int>(p.rest - static_cast<int64_t>(item) * r.tiles);
+    const int64_t n = r.tiles + kOwn;
+    item = static_cast<int>(p.rest / n);
     left = units;
+    turn = solo_turn = 0;
+    most_solo = p.share * a.batch * a.hkv * a.chunks >= 2 * p.units ? kSoloTwo : kSoloOne;
+    if (p.share >> 4 > most_solo) most_solo = p.share >> 4 < kSoloMost ? static_cast<int>(p.share >> 4) : kSoloMost;
     done = false;
-    cut();
-    t = t0 + warp;
+    enter(static_cast<int>(p.rest - item * n), warp);
   }
-  GBF_DEVICE void cut() {
-    const int64_t n = r.tiles - t0 < left ? r.tiles - t0 : left;
-    t1 = t0 + static_cast<int>(n);
+  // the segment that begins at unit u of the item
+  GBF_DEVICE void enter(int u, int warp) {
+    const int64_t rest = r.tiles + kOwn - u, n = rest < left ? rest : left;
+    const int end = u + static_cast<int>(n);
     left -= n;
+    t0 = u > kOwn ? u - kOwn : 0;
+    t1 = end > kOwn ? end - kOwn : 0;
+    whole = t0 == 0 && t1 == r.tiles && (t1 > 0 || u == 0);
+    solo = whole && t1 <= most_solo;
+    if (solo) {
+      mine = solo_turn == warp;
+      solo_turn = (solo_turn + 1) % NW;
+      t = mine ? t0 : t1;
+      step = 1;
+    } else {
+      mine = t1 > t0;     // (a range may begin or end in an item's own units)
+      t = t0 + ((warp - turn) & (NW - 1));
+      turn = (turn + t1 - t0) & (NW - 1);
+      step = NW;
+    }
   }
   // the next segment of the range; false behind the last one
   GBF_DEVICE bool next_segment(const PagedAttnArgs& a, int warp) {
@@ -223,9 +250,7 @@ struct Cursor {
       item = 0;
       r = request_of(a, ++b);
     }
-    t0 = 0;
-    cut();
-    t = warp;
+    enter(0, warp);
     return true;
   }
   // skip segments that hold no tile of this warp
@@ -233,7 +258,7 @@ struct Cursor {
     while (!done && t >= t1) next_segment(a, warp);
   }
   GBF_DEVICE void advance(const PagedAttnArgs& a, int warp) {
-    t += NW;
+    t += step;
     settle(a, warp);
   }
 };
@@ -252,6 +277,14 @@ GBF_DEVICE void store_out4(const PagedAttnArgs& a, int64_t at, float4 o) {
     w.y = f32x2_to_bf16x2(o.z, o.w);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = w;
   }
+}
+
+GBF_DEVICE void store_out2(const PagedAttnArgs& a, int64_t at, float2 o) {
+  if (a.out_fp8)
+    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + at) =
+        f32x2_to_e4m3x2(o.x * a.inv_out_scale, o.y * a.inv_out_scale);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = f32x2_to_bf16x2(o.x, o.y);
 }
 
 // DP: head width padded to 64, 128 or 256.  WIDE: 9..16 heads per row tile
@@ -285,7 +318,7 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
     __syncwarp();
   }
 
-  const int64_t row_bytes = static_cast<int64_t>(a.hkv) * a.d * 2;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.hkv) * a.d * 2;
   const int chunk_col = lane % CPR;              // this lane's 16-byte column, and row within a copy
   const int chunk_row = lane / CPR;
   const bool col_on = chunk_col * 8 < a.d;
@@ -320,21 +353,20 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
     if (!load.done) {
       const bool ok = inside && entry >= 0 && entry < a.num_blocks;
       if (inside && !ok) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
-      const int row = ok ? entry * a.block_size + offset : -1;
+      const uint32_t row = ok ? static_cast<uint32_t>(entry * a.block_size + offset) : 0u;
       const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       if (lane == 0) sm_valid[warp][stage] = valid;
       const int head = load.item / a.chunks;
       const int64_t col = static_cast<int64_t>(head) * a.d * 2 + chunk_col * 16;
       const char* kp = static_cast<const char*>(a.k) + col;
       const char* vp = static_cast<const char*>(a.v) + col;
-      const uint32_t dst = stages_u + stage * stage_bytes<DP>();
+      const uint32_t dst = stages_u + stage * stage_bytes<DP>() + chunk_row * (DP * 2);
 #pragma unroll
       for (int i = 0; i < kTile / RPI; ++i) {
         const int tr = i * RPI + chunk_row;
-        const int src = __shfl_sync(0xffffffffu, row, tr);
-        const int64_t off = src < 0 ? 0 : src * row_bytes;
-        const uint32_t n = src < 0 ? 0u : 16u;
-        const uint32_t at = dst + tr * (DP * 2) + ((chunk_col ^ (tr & 7)) << 4);
+        const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, tr)) * row_bytes;
+        const uint32_t n = (valid >> tr) & 1u ? 16u : 0u;     // what is masked arrives as zeros
+        const uint32_t at = dst + i * RPI * (DP * 2) + ((chunk_col ^ (tr & 7)) << 4);
         if (col_on) {
           cp_async16(at, kp + off, n);
           cp_async16(at + kTile * DP * 2, vp + off, n);
@@ -357,9 +389,20 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
   const int k_tok = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
   const int v_tok = (lane & 7) + (((lane >> 3) & 1) << 3), v_chunk = lane >> 4;
   const int g = lane >> 2, t4 = lane & 3;        // accumulator row, column pair
+  // the swizzle moves a chunk within its 128-byte line only: four offsets each, the lines are constants apart
+  uint32_t k_at[4], v_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k_at[i] = stages_u + k_tok * (DP * 2) + (((i * 2 + k_chunk) ^ (k_tok & 7)) << 4);
+    v_at[i] = stages_u + kTile * DP * 2 + v_tok * (DP * 2) + (((i * 2 + v_chunk) ^ (v_tok & 7)) << 4);
+  }
 
   int stage = 0, parity = 0;
   for (;;) {                                     // segments
+    if (!work.mine) {
+      if (!work.next_segment(a, warp)) break;
+      continue;
+    }
     const int head = work.item / a.chunks, row0 = (work.item - head * a.chunks) * 16;
     const int rows = a.group - row0 < 16 ? a.group - row0 : 16;
     const int64_t q_row0 = static_cast<int64_t>(work.b) * a.hq + static_cast<int64_t>(head) * a.group + row0;
@@ -387,11 +430,11 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
       l[h] = 0.0f;
     }
 
-    for (; work.t < work.t1; work.t += NW) {
+    for (; work.t < work.t1; work.t += work.step) {
       cp_async_wait<NS - 2>();
       __syncwarp();
       const uint32_t valid = sm_valid[warp][stage];
-      const uint32_t kbase = stages_u + stage * stage_bytes<DP>();
+      const uint32_t base = stage * stage_bytes<DP>();
       issue(stage == 0 ? NS - 1 : stage - 1);    // into the stage the previous tile has left
       fetch_entry();
 
@@ -401,7 +444,7 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t kf[4];
-        ldmatrix4(kf, kbase + k_tok * (DP * 2) + (((ks * 2 + k_chunk) ^ (k_tok & 7)) << 4));
+        ldmatrix4(kf, base + k_at[ks & 3] + (ks >> 2) * 128);
         const uint32_t a1 = WIDE ? qf[ks][1] : 0u, a3 = WIDE ? qf[ks][3] : 0u;
         mma_bf16(s[0], qf[ks][0], a1, qf[ks][HALVES], a3, kf[0], kf[1]);
         mma_bf16(s[1], qf[ks][0], a1, qf[ks][HALVES], a3, kf[2], kf[3]);
@@ -452,11 +495,10 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
         }
       }
 
-      const uint32_t vbase = kbase + kTile * DP * 2;
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t vf[4];
-        ldmatrix4_trans(vf, vbase + v_tok * (DP * 2) + (((n * 2 + v_chunk) ^ (v_tok & 7)) << 4));
+        ldmatrix4_trans(vf, base + v_at[n & 3] + (n >> 2) * 128);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           if (WIDE) {
@@ -472,17 +514,41 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
       stage = stage + 1 == NS ? 0 : stage + 1;
     }
 
-    // ---- the warps' results of this segment, joined through shared memory
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    if (work.solo) {                             // nothing to join: from the registers to the output
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const int row = g + 8 * h;
+        const float inv = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
+        if (row < rows) {
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n) {
+            float2 v = WIDE ? make_float2(o[n][h * 2], o[n][h * 2 + 1])
+                            : make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+            v.x *= inv;
+            v.y *= inv;
+            const int c = n * 8 + t4 * 2;
+            if (c < a.d) store_out2(a, (q_row0 + row) * a.d + c, v);
+          }
+          if (t4 == 0 && a.lse) a.lse[q_row0 + row] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
+        }
+      }
+      if (!work.next_segment(a, warp)) break;
+      continue;
+    }
+
+    // ---- the warps' results of this segment, joined through shared memory
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h)
       if (t4 == 0) {
         sm_m[parity][warp][g + 8 * h] = m[h];
         sm_l[parity][warp][g + 8 * h] = l[h];
       }
-    }
-    const bool whole = work.t0 == 0 && work.t1 == work.r.tiles;
+    const bool whole = work.whole;
     float* part = a.ws + (2 * static_cast<int64_t>(blockIdx.x) + (work.t0 == 0 ? 1 : 0)) * partial_floats<DP, WIDE>();
 #pragma unroll
     for (int pass = 0; pass < 2 * HALVES; ++pass) {
@@ -559,12 +625,11 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAt
   int item = 0, c0 = 0, c1 = 0;
   if (on) {
     const Request r = request_of(a, p.b);
-    item = static_cast<int>(p.rest / r.tiles);
-    const int64_t t = p.rest - static_cast<int64_t>(item) * r.tiles;
-    const int64_t begin = c * p.share - t;
-    c0 = static_cast<int>(begin / p.share);
-    c1 = static_cast<int>((begin + r.tiles - 1) / p.share);
-    on = t > 0 && c == c0 + 1;
+    item = static_cast<int>(p.rest / (r.tiles + kOwn));
+    const int64_t u = p.rest - static_cast<int64_t>(item) * (r.tiles + kOwn), begin = c * p.share - u;
+    c0 = static_cast<int>((begin + kOwn) / p.share);        // CTAs of the item's first and last tile
+    c1 = static_cast<int>((begin + kOwn + r.tiles - 1) / p.share);
+    on = u > kOwn && c == c0 + 1;
   }
   const int head = item / a.chunks, row0 = (item - head * a.chunks) * 16, row = blockIdx.y;
   on = on && row0 + row < a.group;
@@ -635,8 +700,8 @@ cudaError_t launch(PagedAttnArgs a, cudaStream_t stream) {
   a.min_units = NW;
   const int64_t most = static_cast<int64_t>(a.max_blocks) * a.block_size;
   const int64_t seen = a.window > 0 && a.window < most ? a.window : most;
-  const int64_t tiles = seen / kTile + 1;
-  const int64_t units = tiles * a.batch * a.hkv * a.chunks;
+  const int64_t tiles = (seen + kTile - 1) / kTile;
+  const int64_t units = (tiles + kOwn) * a.batch * a.hkv * a.chunks;
   int64_t ctas = (units + NW - 1) / NW;
   if (ctas > kSms * Plan<DP>::kPerSm) ctas = kSms * Plan<DP>::kPerSm;
   a.ctas = static_cast<int>(ctas);
