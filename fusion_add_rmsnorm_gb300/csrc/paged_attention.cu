@@ -53,7 +53,7 @@ template <int DP>
 struct Plan;
 template <>
 struct Plan<64> {
-  static constexpr int kWarps = 4, kStages = 4, kPerSm = 3;
+  static constexpr int kWarps = 4, kStages = 6, kPerSm = 2;
 };
 template <>
 struct Plan<128> {
@@ -464,25 +464,13 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
         float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = fmaxf(top, m[h]);
-        const float ref = top == -INFINITY ? 0.0f : top;     // nothing seen yet: every weight is zero
-        const float shrink = exp2_approx(m[h] - ref);
-        m[h] = top;
-        float p[4], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = exp2_approx(x[i] - ref);
-          sum += p[i];
-        }
-        l[h] = l[h] * shrink + sum;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint32_t hi = f32x2_to_bf16x2(p[2 * n], p[2 * n + 1]);
-          p_hi[h][n] = hi;
-          p_lo[h][n] = f32x2_to_bf16x2(p[2 * n] - __uint_as_float(hi << 16),
-                                       p[2 * n + 1] - __uint_as_float(hi & 0xffff0000u));
-        }
-        if (__any_sync(0xffffffffu, shrink != 1.0f)) {
+        // the reference follows the maximum only when that is more than 2^8 ahead: weights up to 2^8 are as good as
+        // weights up to 1, and rescaling the accumulators is left out for most tiles
+        if (__any_sync(0xffffffffu, top > m[h] + 8.0f)) {
+          const float next = top > m[h] + 8.0f ? top : m[h];
+          const float shrink = next == -INFINITY ? 1.0f : exp2_approx(m[h] - next);
+          m[h] = next;
+          l[h] *= shrink;
 #pragma unroll
           for (int n = 0; n < DP / 8; ++n) {
             o[n][h * 2] *= shrink;
@@ -492,6 +480,21 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
               o[n][3] *= shrink;
             }
           }
+        }
+        const float ref = m[h] == -INFINITY ? 0.0f : m[h];     // nothing seen yet: every weight is zero
+        float p[4], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = exp2_approx(x[i] - ref);
+          sum += p[i];
+        }
+        l[h] += sum;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t hi = f32x2_to_bf16x2(p[2 * n], p[2 * n + 1]);
+          p_hi[h][n] = hi;
+          p_lo[h][n] = f32x2_to_bf16x2(p[2 * n] - __uint_as_float(hi << 16),
+                                       p[2 * n + 1] - __uint_as_float(hi & 0xffff0000u));
         }
       }
 
