@@ -81,9 +81,10 @@ struct PagedSlotsArgs {
   int64_t table_stride;
   int32_t num_blocks, tokens;
   int batch, max_blocks, block_size;
+  int wide;                 // slots and pos are 16-byte aligned (set by the launcher)
 };
 
-cudaError_t launch_paged_slots(const PagedSlotsArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_slots(PagedSlotsArgs a, cudaStream_t stream);
 
 // ----------------------------------------------------------------- sampling
 struct SampleArgs {

@@ -12,10 +12,12 @@
 // call is latency, so each CTA scans the whole batch by itself and keeps the
 // sums in shared memory, and every write after that is independent.  Tokens
 // and blocks find their request by bisection of the sums, which costs the same
-// for a batch of decode rows and for one long prompt.  A call with many tokens
-// runs as one cluster of eight CTAs that share the writes (one barrier between
-// the last read of ctx and ring and the first write, so that both may be
-// updated in place); a small one as a single CTA.
+// for a batch of decode rows and for one long prompt.  A small call is a single
+// CTA.  In one with many tokens a thread takes four of them in a row for one
+// bisection, and several CTAs share the writes: as many as the tokens fill,
+// independent of one another, when seq_lens and ring_out have memory of their
+// own; one cluster of eight, with a barrier between the last read of ctx and
+// ring and the first write, when one of them is updated in place.
 #include "common.cuh"
 #include "decode.h"
 
@@ -26,11 +28,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSlotThreads = 1024;
-constexpr int kSlotWarps = kSlotThreads / 32;
-constexpr int kPerThread = kSlotsMaxBatch / kSlotThreads;
 constexpr int kSlotsCluster = 8;
-constexpr int kSlotsClusterTokens = 4096;   // more tokens than this: a cluster
+constexpr int kSlotsGrid = 152;
+constexpr int kSlotsAlone = 512;            // more tokens than this: several CTAs
 
 GBF_DEVICE int clamp31(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : static_cast<int>(v); }
 
@@ -47,8 +47,13 @@ GBF_DEVICE int find_last(const int* first, int n, int x) {
 
 GBF_DEVICE int ceil_div(int64_t n, int d) { return static_cast<int>((n + d - 1) / d); }
 
-template <bool CLUSTER>
-__global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedSlotsArgs a) {
+enum Share { kAlone, kCluster, kGrid };      // one CTA; a cluster with a barrier; CTAs that do not wait for one another
+
+// THREADS per CTA, each with up to PER requests of the scan.
+template <int THREADS, int PER, Share SHARE>
+__global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsArgs a) {
+  constexpr int kSlotThreads = THREADS, kSlotWarps = THREADS / 32, kPerThread = PER;
+  constexpr int kRow = SHARE == kAlone ? 1 : 4;          // tokens in a row per thread
   extern __shared__ int dyn[];
   const int n = a.batch;
   int* first_tok = dyn;                 // [n + 1] tokens of the requests before
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedSl
   int64_t at[3], total[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const int64_t mine = sums[k][lane];
+    const int64_t mine = lane < kSlotWarps ? sums[k][lane] : 0;
     int64_t before = lane < warp ? mine : 0, all = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -156,12 +161,16 @@ __global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedSl
   // every read of ctx, add and ring is done
   if (taken > 0) atomicMax(&s_taken, taken);
   unsigned rank = 0, ranks = 1;
-  if (CLUSTER) {
+  if (SHARE == kCluster) {
     cg::cluster_group cluster = cg::this_cluster();
     rank = cluster.block_rank();
     ranks = cluster.num_blocks();
     cluster.sync();
   } else {
+    if (SHARE == kGrid) {
+      rank = blockIdx.x;
+      ranks = gridDim.x;
+    }
     __syncthreads();
   }
   taken = s_taken;
@@ -207,35 +216,54 @@ __global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedSl
   // tokens: a new block's id is read from the ring, not from the table entry that another thread writes
   const int tokens = first_tok[n] < a.tokens ? first_tok[n] : a.tokens;
   if (worker == 0 && first_tok[n] > a.tokens) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
-  for (int64_t t = worker; t < tokens; t += workers) {
-    const int b = find_last(first_tok, n, static_cast<int>(t));
-    const int c = ctx[b];
-    const int64_t p = static_cast<int64_t>(c < 0 ? ~c : c) + (t - first_tok[b]);
-    int32_t slot = -1;
-    if (c >= 0) {
-      const int blk = static_cast<int>(p / bs), have = ceil_div(c, bs);
-      const int32_t id = blk < have ? a.table[b * a.table_stride + blk]
-                                    : a.free_ring[ring_at(static_cast<int64_t>(first_new[b]) + blk - have)];
-      if (id >= 0 && id < a.num_blocks) slot = id * bs + static_cast<int>(p - static_cast<int64_t>(blk) * bs);
-      else raise_error(a.err, DEV_ERR_BLOCK_RANGE);
+  for (int64_t t0 = worker * kRow; t0 < tokens; t0 += workers * kRow) {
+    int b = find_last(first_tok, n, static_cast<int>(t0)), last_blk = -1, last_b = -1;
+    int32_t id = -1;
+    int32_t slot[kRow], pos[kRow];
+#pragma unroll
+    for (int i = 0; i < kRow; ++i) {
+      slot[i] = pos[i] = -1;
+      const int t = static_cast<int>(t0) + i;
+      if (t >= tokens) continue;
+      while (first_tok[b + 1] <= t) ++b;                 // (requests without tokens are passed over)
+      const int c = ctx[b];
+      const int64_t p = static_cast<int64_t>(c < 0 ? ~c : c) + (t - first_tok[b]);
+      pos[i] = clamp31(p);
+      if (c < 0) continue;
+      const int blk = static_cast<int>(p / bs);
+      if (blk != last_blk || b != last_b) {
+        const int have = ceil_div(c, bs);
+        id = blk < have ? a.table[b * a.table_stride + blk]
+                        : a.free_ring[ring_at(static_cast<int64_t>(first_new[b]) + blk - have)];
+        last_blk = blk;
+        last_b = b;
+        if (id < 0 || id >= a.num_blocks) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
+      }
+      if (id >= 0 && id < a.num_blocks) slot[i] = id * bs + static_cast<int>(p - static_cast<int64_t>(blk) * bs);
     }
-    a.slots[t] = slot;
-    a.pos[t] = clamp31(p);
+    if (kRow == 4 && t0 + kRow <= tokens && a.wide) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1 % kRow], slot[2 % kRow], slot[3 % kRow]);
+      *reinterpret_cast<int4*>(a.pos + t0) = make_int4(pos[0], pos[1 % kRow], pos[2 % kRow], pos[3 % kRow]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRow; ++i)
+        if (t0 + i < tokens) {
+          a.slots[t0 + i] = slot[i];
+          a.pos[t0 + i] = pos[i];
+        }
+    }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_paged_slots(const PagedSlotsArgs& a, cudaStream_t stream) {
-  const size_t smem = (4 * static_cast<size_t>(a.batch) + 3) * sizeof(int);
-  const bool cluster = a.tokens > kSlotsClusterTokens;
-  auto kernel = cluster ? paged_slots_kernel<true> : paged_slots_kernel<false>;
-  constexpr int most = (4 * kSlotsMaxBatch + 3) * static_cast<int>(sizeof(int));
-  const cudaError_t e = cluster ? allow_smem<paged_slots_kernel<true>>(most) : allow_smem<paged_slots_kernel<false>>(most);
+template <int THREADS, int PER, Share SHARE>
+cudaError_t launch(const PagedSlotsArgs& a, size_t smem, cudaStream_t stream) {
+  constexpr int most = (4 * THREADS * PER + 3) * static_cast<int>(sizeof(int));
+  const cudaError_t e = allow_smem<paged_slots_kernel<THREADS, PER, SHARE>>(most);
   if (e != cudaSuccess) return e;
+  const int fill = (a.tokens + 4 * THREADS - 1) / (4 * THREADS);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster ? kSlotsCluster : 1);
-  cfg.blockDim = dim3(kSlotThreads);
+  cfg.gridDim = dim3(SHARE == kAlone ? 1 : SHARE == kCluster ? kSlotsCluster : fill < kSlotsGrid ? fill : kSlotsGrid);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -246,8 +274,20 @@ cudaError_t launch_paged_slots(const PagedSlotsArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  cfg.numAttrs = SHARE == kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, paged_slots_kernel<THREADS, PER, SHARE>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_slots(PagedSlotsArgs a, cudaStream_t stream) {
+  const size_t smem = (4 * static_cast<size_t>(a.batch) + 3) * sizeof(int);
+  a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
+  const bool in_place = a.seq == a.ctx || a.ring_out == a.ring, small = a.batch <= 512;
+  if (a.tokens <= kSlotsAlone)
+    return small ? launch<256, 2, kAlone>(a, smem, stream) : launch<1024, 8, kAlone>(a, smem, stream);
+  if (in_place) return launch<1024, 8, kCluster>(a, smem, stream);
+  return small ? launch<256, 2, kGrid>(a, smem, stream) : launch<1024, 8, kGrid>(a, smem, stream);
 }
 
 }  // namespace gbf
