@@ -78,6 +78,7 @@ constexpr int kSpans = 32;                  // parts that the bins that may hold
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
 constexpr float kLeastTemperature = 1e-30f;
+constexpr int kSms = 152;
 
 // 2^43 * 2^(j / 64)
 __device__ const u64 kPow[64] = {
@@ -1239,7 +1240,13 @@ template <typename T>
 cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
   constexpr int N = Elem<T>::N;
   const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
-  const int ranks = 8;   // RANKS
+  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (61 rows of 50257: 21 us with four,
+  // 25 with eight); a batch that takes several waves has rows cut less, because a CTA spends some 20 us beside its
+  // elements (256 rows of 128000 float32: 225 us with four, 267 with eight, 303 with one).
+  int ranks = 8;
+  while (ranks > 1 && a.batch * ranks > 2 * kSms) ranks /= 2;
+  const int least = a.vocab > 96 * 1024 ? 4 : a.vocab > 48 * 1024 ? 2 : 1;
+  if (ranks < least) ranks = least;
   const int64_t slice = (vectors + ranks - 1) / ranks * 16;
   if (slice <= kStageBytes) return launch<T, true>(a, ranks, sizeof(Shared) + static_cast<size_t>(slice), stream);
   return launch<T, false>(a, ranks, sizeof(Shared), stream);
