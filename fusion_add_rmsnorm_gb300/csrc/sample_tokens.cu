@@ -35,7 +35,9 @@
 //      (logit, index).
 // The pass of step 2 also sums each warp's run of the kept elements above the
 // border's bins, so the draw only adds the few within them.  A row that asks for
-// neither top-k nor top-p takes that pass alone.
+// neither top-k nor top-p takes that pass alone.  A row whose top-k border lies
+// among its first 1024 elements is simpler: they are gathered on one CTA and
+// sorted, and all the rest is done on that list.
 //
 // The exact weight is the dear part (some 45 integer instructions, which run at
 // half rate), so a long slice is first done in float32 with an error bound: the
@@ -254,6 +256,13 @@ GBF_DEVICE u64 fixed_of(float hi, float lo) {
 // what two float32 sums of masses may be apart by: twice 2^-25 of them, and the conversions' roundings
 GBF_DEVICE u64 slack_of(u64 total) { return (total >> 24) + 4096; }
 
+// ln(w / total) = (l - top) / T - ln(total / 2^43), both terms of one sign.
+GBF_DEVICE float log_share(const RowScale& s, float l, float heat, u64 total) {
+  const float d = l == s.top ? 0.0f : (l - s.top) / heat;
+  const u64 more = total > 1ull << kFix ? total - (1ull << kFix) : 0;
+  return d - log1pf(static_cast<float>(more) * (1.0f / static_cast<float>(1ull << kFix)));
+}
+
 // Place of a candidate in 64ths of a bin, half a bin ahead: its bin, and 0..63 within it.  Smaller logits never have a
 // lower place.
 GBF_DEVICE int place_of(const RowScale& s, float l) {
@@ -456,7 +465,7 @@ struct Sampler {
   };
   struct Hit {
     int at;                    // value at which the sum reaches a target; -1: it stays below
-    float before;
+    float before, upto;        // the sum before it, and with it
   };
   GBF_DEVICE Scan scan64(const float (*rows)[kGroup], float base) {
     float x = 0.0f, y = 0.0f;
@@ -480,8 +489,8 @@ struct Sampler {
     const int src = m ? __ffs(m) - 1 : 0;
     const bool second = s.incl - s.y < t;                // (in the lane that reaches t)
     const int at = 2 * lane + (second ? 1 : 0);
-    const float before = s.incl - (second ? s.y : s.xy);
-    Hit h{__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, before, src)};
+    const float before = s.incl - (second ? s.y : s.xy), upto = second ? s.incl : s.incl - s.y;
+    Hit h{__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, before, src), __shfl_sync(0xffffffffu, upto, src)};
     if (!m) h.at = -1;
     return h;
   }
@@ -516,6 +525,7 @@ struct Sampler {
       if (out[k].at >= 0) {
         const Hit h = hit64(scan64(mem()->search.bin[k], out[k].before), t[k]);
         out[k].before = h.before;
+        out[k].upto = h.upto;
         out[k].at = out[k].at * kGroup + (h.at < 0 ? kGroup - 1 : h.at);
       }
   }
@@ -562,11 +572,11 @@ struct Sampler {
     cluster.sync();
   }
 
-  // A candidate of this rank to every rank's list.
-  GBF_DEVICE void offer(u64 k) {
+  // A candidate of this rank to the list of every rank, or of the first `heads`.
+  GBF_DEVICE void offer(u64 k, unsigned heads) {
     const unsigned share = kList / ranks, at = atomicAdd(&mem()->mine_n, 1u);
     if (at < share)
-      for (unsigned r = 0; r < ranks; ++r) of(r)->list[rank * share + at] = k;
+      for (unsigned r = 0; r < heads; ++r) of(r)->list[rank * share + at] = k;
   }
   // Closes the lists (the threads' offers are behind a barrier of the block): a
   // cluster barrier; false when one of them is too short.
@@ -581,6 +591,75 @@ struct Sampler {
     u64 rank;                  // (key, ~index) of the last element kept
     bool sure;                 // it clears the target by the slack (or slack is 0)
   };
+  // The lists of all ranks in one row; how many there are.
+  GBF_DEVICE unsigned pack(u64* order) {
+    unsigned n = 0;
+    for (unsigned r = 0; r < ranks; ++r) {
+      const unsigned c = min(mem()->list_n[r], kList / ranks);
+      for (unsigned i = tid; i < c; i += kThreads) order[n + i] = mem()->list[r * (kList / ranks) + i];
+      n += c;
+    }
+    return n;
+  }
+  // Sorts n <= kList values, larger first: bitonic, a warp's 64 values in its lanes
+  // as long as the steps stay within them.  Zeros go behind, up to a power of two.
+  __device__ __noinline__ static void sort_down(u64* order, unsigned n) {
+    static_assert(kList == 2 * kThreads, "");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned size = 64;
+    while (size < n) size *= 2;
+    for (unsigned i = n + tid; i < size; i += kThreads) order[i] = 0;
+    __syncthreads();
+    const unsigned i0 = warp * 64 + lane, i1 = i0 + 32;
+    const bool on = static_cast<unsigned>(warp) * 64 < size;
+    u64 x = on ? order[i0] : 0, y = on ? order[i1] : 0;
+    auto keep = [](u64 mine, u64 other, bool larger) { return (mine > other) == larger ? mine : other; };
+#pragma unroll 1
+    for (unsigned width = 2; width <= size; width *= 2) {
+      if (width > 64) {                                  // steps across warps: through shared memory
+        if (on) {
+          order[i0] = x;
+          order[i1] = y;
+        }
+#pragma unroll 1
+        for (unsigned step = width / 2; step >= 64; step /= 2) {
+          __syncthreads();
+          if (static_cast<unsigned>(tid) < size / 2) {
+            const unsigned i = 2 * tid - (tid & (step - 1)), j = i + step;
+            const u64 p = order[i], q = order[j];
+            if ((p < q) == ((i & width) == 0)) {
+              order[i] = q;
+              order[j] = p;
+            }
+          }
+        }
+        __syncthreads();
+        if (on) {
+          x = order[i0];
+          y = order[i1];
+        }
+      }
+      if (width >= 64) {                                 // the lane's own two
+        const bool down = (i0 & width) == 0;
+        const u64 larger = x > y ? x : y, smaller = x > y ? y : x;
+        x = down ? larger : smaller;
+        y = down ? smaller : larger;
+      }
+#pragma unroll 1
+      for (unsigned step = width / 2 < 16 ? width / 2 : 16; step > 0; step /= 2) {
+        const u64 ox = __shfl_xor_sync(0xffffffffu, x, step), oy = __shfl_xor_sync(0xffffffffu, y, step);
+        const bool low = (lane & step) == 0;
+        x = keep(x, ox, low == ((i0 & width) == 0));
+        y = keep(y, oy, low == ((i1 & width) == 0));
+      }
+    }
+    if (on) {
+      order[i0] = x;
+      order[i1] = y;
+    }
+    __syncthreads();
+  }
+
   // Ranks the lists' candidates, the same in every rank, in the histogram's memory
   // (a few by comparison with each other, more by a bitonic sort, larger first):
   // the last of them before which less than `target` lies, `before` lying before
@@ -589,12 +668,7 @@ struct Sampler {
   GBF_DEVICE Border border_of_lists(u64 before, u64 target, u64 slack, Value value) {
     static_assert(2 * kList * sizeof(u64) <= sizeof(unsigned) * kBins && kFew <= kThreads, "");
     u64* order = reinterpret_cast<u64*>(mem()->hist);
-    unsigned n = 0;
-    for (unsigned r = 0; r < ranks; ++r) {
-      const unsigned c = min(mem()->list_n[r], kList / ranks);
-      for (unsigned i = tid; i < c; i += kThreads) order[n + i] = mem()->list[r * (kList / ranks) + i];
-      n += c;
-    }
+    const unsigned n = pack(order);
     u64 last = ~0ull;
     bool sure = false;
     auto decide = [&](u64 k, u64 at, u64 w) {
@@ -619,24 +693,7 @@ struct Sampler {
       }
       return conclude(last, sure);
     }
-    unsigned size = 2 * kFew;
-    while (size < n) size *= 2;
-    for (unsigned i = n + tid; i < size; i += kThreads) order[i] = 0;
-    __syncthreads();
-#pragma unroll 1
-    for (unsigned width = 2; width <= size; width *= 2)
-#pragma unroll 1
-      for (unsigned step = width / 2; step > 0; step /= 2) {
-        if (tid < size / 2) {
-          const unsigned i = 2 * tid - (tid & (step - 1)), j = i + step;
-          const u64 x = order[i], y = order[j];
-          if ((x < y) == ((i & width) == 0)) {
-            order[i] = y;
-            order[j] = x;
-          }
-        }
-        __syncthreads();
-      }
+    sort_down(order, n);
     // the border: two candidates per thread
     constexpr int kPer = kList / kThreads;
     u64 w[kPer], sum = 0;
@@ -668,6 +725,72 @@ struct Sampler {
     out.sure = __syncthreads_or(sure);
     out.rank = ~warp_max64(lane < kWarps ? ~mem()->warp_a[lane] : 0);
     return out;
+  }
+
+  // An exclusive sum over the block of each thread's value, and the total.
+  GBF_DEVICE u64 block_before(u64 v, u64* total) {
+    const u64 incl = warp_scan64(v, lane);
+    __syncthreads();
+    if (lane == 31) mem()->warp_a[warp] = incl;
+    __syncthreads();
+    const u64 warps = warp_scan64(lane < kWarps ? mem()->warp_a[lane] : 0, lane);
+    *total = __shfl_sync(0xffffffffu, warps, 31);
+    return incl - v + (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0);
+  }
+
+  // The row's draw when the lists hold its first elements, top-k's border among
+  // them: on one CTA, without the others.  In the thread that returns true.
+  GBF_DEVICE bool draw_of_lists(unsigned k, bool by_p, float p, u64 least, float u, unsigned* token, float* l, u64* mass) {
+    u64* order = reinterpret_cast<u64*>(mem()->hist);
+    u64* by_index = order + kList;
+    u64* weight = mem()->near;
+    const unsigned n = pack(order), kept = min(n, k);
+    sort_down(order, n);
+    constexpr int kPer = kList / kThreads;
+    u64 w[kPer], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const unsigned j = tid * kPer + i;
+      const float l0 = j < kept ? of_key(static_cast<unsigned>(order[j] >> 32)) : -INFINITY;
+      const float l1 = j + 1 < kept ? of_key(static_cast<unsigned>(order[j + 1] >> 32)) : -INFINITY;
+      weigh(make_float2(l0, l1), &w[i], &w[i + 1]);
+      sum += w[i] + w[i + 1];
+    }
+    u64 at = block_before(sum, &total);
+    const u64 target = by_p ? share_of(p, total) : ~0ull;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const unsigned j = tid * kPer + i;
+      const bool on = j < kept && at < target && w[i] >= least;
+      at += w[i];
+      weight[j] = w[i];
+      by_index[j] = on ? (order[j] << 32) | j : 0;         // ~index above: lower indexes first
+    }
+    __syncthreads();
+    sort_down(by_index, n);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const unsigned j = tid * kPer + i;
+      const u64 x = j < n ? by_index[j] : 0;
+      w[i] = x ? weight[static_cast<unsigned>(x)] : 0;
+      sum += w[i];
+    }
+    at = block_before(sum, &total);
+    *mass = total;
+    const u64 aim = __umul64hi(fraction_of(u), total);
+    bool here = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (at <= aim && aim < at + w[i]) {
+        const u64 x = by_index[tid * kPer + i];
+        *token = 0xffffffffu - static_cast<unsigned>(x >> 32);
+        *l = of_key(static_cast<unsigned>(order[static_cast<unsigned>(x)] >> 32));
+        here = true;
+      }
+      at += w[i];
+    }
+    return here;
   }
 
   // The rank (key, ~index) of the last element before which less than `target`
@@ -713,7 +836,7 @@ struct Sampler {
             const int n = place(l);
             if (l < l_lo || l > l_hi || k < lo || k > hi || n < p0 || n > p1) continue;
             if (todo == kGather) {
-              offer(k);
+              offer(k, ranks);
             } else if (todo == kRange) {
               mn = k < mn ? k : mn;
               mx = k > mx ? k : mx;
@@ -793,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.turn = 0;
   const int tid = s.tid = threadIdx.x, lane = s.lane = tid & 31, warp = s.warp = tid >> 5;
   if (tid < 64) mem()->pow[tid] = kPow[tid];
+  if (tid == 0) mem()->mine_n = 0;
   s.clear();
   pdl_wait();
   pdl_launch_dependents();
@@ -930,6 +1054,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;
       b1 = hit[1].at < 0 ? kBins - 1 : hit[1].at;
     } else if (hit[0].at >= 0) {                         // else fewer than k candidates
+      if (hit[0].upto <= kList) {                          // all that top-k may keep to one list
+        const int p1 = 64 * hit[0].at + 63;
+        const float from =
+            s.scale.top == INFINITY ? -FLT_MAX : fmaxf(s.scale.top - (p1 + 64) * s.scale.c_inverse, -FLT_MAX);
+#pragma unroll 1
+        for (int i = v0 + tid; i < v1; i += kThreads) {
+          float f[N];
+          s.row.get(i, f);
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (f[e] >= from && s.place(f[e]) <= p1)
+              s.offer(rank_of(key_of(f[e]), static_cast<unsigned>(i * N + e - s.row.shift)), 1);
+        }
+        __syncthreads();
+        if (s.close_lists()) {                             // (else a rank has more than its share of them)
+          if (s.rank != 0) return;
+          unsigned token;
+          float l;
+          u64 mass;
+          if (s.draw_of_lists(k, by_p, p, least, u, &token, &l, &mass)) {
+            a.tokens[b] = static_cast<int32_t>(token);
+            if (a.logprob) a.logprob[b] = log_share(s.scale, l, heat, mass);
+          }
+          return;
+        }
+        s.cluster.sync();                                  // every rank has read the lists' sizes
+      }
       const BorderTurn found = border_call<T, STAGED>(s, false, 64 * hit[0].at, 64 * hit[0].at + 63, 0,
                                                       static_cast<u64>(hit[0].before), static_cast<u64>(k));
       border = found.border;
@@ -1092,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (!many) {                                       // the span's elements, from the list
         for (unsigned i = tid; i < mem()->near_n; i += kThreads) {
           const u64 c = mem()->near[i];
-          if (((s.place(of_key(static_cast<unsigned>(c >> 32))) - p0) >> coarse) == hit) s.offer(c);
+          if (((s.place(of_key(static_cast<unsigned>(c >> 32))) - p0) >> coarse) == hit) s.offer(c, s.ranks);
         }
         __syncthreads();
         many = !s.close_lists();
@@ -1203,12 +1354,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (token >= 0) {
       a.tokens[b] = token;
-      if (a.logprob) {
-        // ln(w / total) = (l - top) / T - ln(total / 2^43), both terms of one sign
-        const float d = token_l == s.scale.top ? 0.0f : (token_l - s.scale.top) / heat;
-        const u64 more = total > 1ull << kFix ? total - (1ull << kFix) : 0;
-        a.logprob[b] = d - log1pf(static_cast<float>(more) * (1.0f / static_cast<float>(1ull << kFix)));
-      }
+      if (a.logprob) a.logprob[b] = log_share(s.scale, token_l, heat, total);
     }
     return;
   }
