@@ -35,9 +35,14 @@
 //      (logit, index).
 // The pass of step 2 also sums each warp's run of the kept elements above the
 // border's bins, so the draw only adds the few within them.  A row that asks for
-// neither top-k nor top-p takes that pass alone.  A row whose top-k border lies
-// among its first 1024 elements is simpler: they are gathered on one CTA and
-// sorted, and all the rest is done on that list.
+// neither top-k nor top-p takes that pass alone.
+//
+// A row whose top-k border lies among its first 1024 elements is simpler: they
+// are gathered on one CTA and sorted, and all the rest is done on that list.
+// For a short top-k there is no histogram either: pass 1 gives the largest
+// logits of as many disjoint groups of lanes as top-k keeps elements or more, and
+// the smallest of those is a lower bound of the k-th largest logit.  With n
+// groups it leaves about n ln n elements, in whatever order the logits come.
 //
 // The exact weight is the dear part (some 45 integer instructions, which run at
 // half rate), so a long slice is first done in float32 with an error bound: the
@@ -428,6 +433,10 @@ struct Sampler {
       *w1 = l.y == INFINITY ? 1ull << kFix : 0;
     }
   }
+  // a logit below those of all places up to place - 64
+  GBF_DEVICE float logit_of(int place) {
+    return scale.top == INFINITY ? -FLT_MAX : fmaxf(scale.top - place * scale.c_inverse, -FLT_MAX);
+  }
   GBF_DEVICE int place(float l) {
     return scale.top == INFINITY ? (l == INFINITY ? 32 : 64 * kBins - 1) : place_of(scale, l);
   }
@@ -603,8 +612,10 @@ struct Sampler {
   }
   // Sorts n <= kList values, larger first: bitonic, a warp's 64 values in its lanes
   // as long as the steps stay within them.  Zeros go behind, up to a power of two.
-  __device__ __noinline__ static void sort_down(u64* order, unsigned n) {
+  // They stand `from` values into the histogram's memory.
+  __device__ __noinline__ static void sort_down(unsigned from, unsigned n) {
     static_assert(kList == 2 * kThreads, "");
+    u64* order = reinterpret_cast<u64*>(mem()->hist) + from;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned size = 64;
     while (size < n) size *= 2;
@@ -693,7 +704,7 @@ struct Sampler {
       }
       return conclude(last, sure);
     }
-    sort_down(order, n);
+    sort_down(0, n);
     // the border: two candidates per thread
     constexpr int kPer = kList / kThreads;
     u64 w[kPer], sum = 0;
@@ -745,7 +756,7 @@ struct Sampler {
     u64* by_index = order + kList;
     u64* weight = mem()->near;
     const unsigned n = pack(order), kept = min(n, k);
-    sort_down(order, n);
+    sort_down(0, n);
     constexpr int kPer = kList / kThreads;
     u64 w[kPer], sum = 0, total;
 #pragma unroll
@@ -758,22 +769,22 @@ struct Sampler {
     }
     u64 at = block_before(sum, &total);
     const u64 target = by_p ? share_of(p, total) : ~0ull;
+    unsigned most = 0;                                     // kept by all criteria: the first so many
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const unsigned j = tid * kPer + i;
       const bool on = j < kept && at < target && w[i] >= least;
       at += w[i];
       weight[j] = w[i];
-      by_index[j] = on ? (order[j] << 32) | j : 0;         // ~index above: lower indexes first
+      by_index[j] = (order[j] << 32) | j;                  // ~index above: lower indexes first
+      most += __syncthreads_count(on);
     }
-    __syncthreads();
-    sort_down(by_index, n);
+    sort_down(kList, most);
     sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const unsigned j = tid * kPer + i;
-      const u64 x = j < n ? by_index[j] : 0;
-      w[i] = x ? weight[static_cast<unsigned>(x)] : 0;
+      w[i] = j < most ? weight[static_cast<unsigned>(by_index[j])] : 0;
       sum += w[i];
     }
     at = block_before(sum, &total);
@@ -916,7 +927,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.turn = 0;
   const int tid = s.tid = threadIdx.x, lane = s.lane = tid & 31, warp = s.warp = tid >> 5;
   if (tid < 64) mem()->pow[tid] = kPow[tid];
-  if (tid == 0) mem()->mine_n = 0;
   s.clear();
   pdl_wait();
   pdl_launch_dependents();
@@ -950,7 +960,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     s.scale.c_inverse = heat * (0.693147180559945f / (kBinsPerOctave * 64.0f));
   }
 
-  // pass 1: the only read of HBM; the largest logit
+  // top-k: lanes per group, with at least k groups in the cluster
+  const bool by_k = k > 0 && k < a.vocab, by_p = p < 1.0f;
+  const int lanes = kThreads * static_cast<int>(s.ranks);
+  const int group = !by_k ? 0 : k <= lanes / 32 ? 32 : k <= lanes / 4 ? 4 : k <= lanes ? 1 : 0;
+
+  // pass 1: the only read of HBM; the largest logit, and the smallest of the groups' largest ones
   float most = -INFINITY;
   auto look = [&](int v, uint4 raw) {
     float f[N];
@@ -971,15 +986,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 #pragma unroll 1
   for (; v < v1; v += kThreads) look(v, s.row.load(v));
-  // (as a key: largest over the lanes, the warps and the ranks; 0: no candidate)
-  unsigned top = __reduce_max_sync(0xffffffffu, most == -INFINITY ? 0u : key_of(most));
-  if (lane == 0) mem()->warp_a[warp] = top;
+  // (as keys, over the lanes, the warps and the ranks; 0: no candidate)
+  const unsigned mine = most == -INFINITY ? 0u : key_of(most);
+  unsigned top = __reduce_max_sync(0xffffffffu, mine), low = mine;
+  if (group == 4) {
+    low = max(low, __shfl_xor_sync(0xffffffffu, low, 1));
+    low = max(low, __shfl_xor_sync(0xffffffffu, low, 2));
+  }
+  low = group == 32 ? top : __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) {
+    mem()->warp_a[warp] = top;
+    mem()->warp_b[warp] = low;
+  }
   __syncthreads();
   top = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_a[lane]) : 0u);
+  low = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_b[lane]) : 0xffffffffu);
   {
-    const u64(*box)[8] = s.exchange(top, 0);
-    for (unsigned r = 0; r < s.ranks; ++r) top = max(top, static_cast<unsigned>(box[0][r]));
+    const u64(*box)[8] = s.exchange(top, low);
+    for (unsigned r = 0; r < s.ranks; ++r) {
+      top = max(top, static_cast<unsigned>(box[0][r]));
+      low = min(low, static_cast<unsigned>(box[1][r]));
+    }
   }
+  const float floor_k = group > 0 && low > 0 ? of_key(low) : -FLT_MAX;
   s.scale.top = of_key(top);
 
   const bool bad = !(temp >= 0.0f && temp < INFINITY) || !(p == p) || !(mp <= 1.0f) || !(u >= 0.0f && u < 1.0f);
@@ -1019,74 +1048,89 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   const u64 least = mp > 0.0f ? __float2ull_ru(mp * static_cast<float>(1ull << kFix)) : 0;
 
-  const bool by_k = k > 0 && k < a.vocab, by_p = p < 1.0f;
-  u64 border = 0;                                        // ranks below it are cut off
-  int b0 = 0, b1 = kBins - 1;                            // bins the border of top-p lies in
-  if (by_k || by_p) {
+  // The row's draw from the elements with logits >= from and places <= p1, top-k's border among them: gathered on rank 0.
+  // False when a rank has more than its share of them.
+  auto draw_first = [&](float from, int p1) {
+    if (tid == 0) mem()->mine_n = 0;
+    __syncthreads();
 #pragma unroll 1
     for (int i = v0 + tid; i < v1; i += kThreads) {
       float f[N];
       s.row.get(i, f);
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (f[e] != -INFINITY) {
-          const int at = s.place(f[e]);
-          atomicAdd(&mem()->hist[at >> 6], by_k ? 1u : (1u << 20) + (at & 63));
-        }
+        if (f[e] >= from && s.place(f[e]) <= p1)
+          s.offer(rank_of(key_of(f[e]), static_cast<unsigned>(i * N + e - s.row.shift)), 1);
     }
-    // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
-    typename Sampler<T, STAGED>::Hit hit[2];
-    s.find_bins(
-        [&](int j) {
-          const unsigned h = mem()->hist[j];
-          if (by_k) return static_cast<float>(h);
-          const float c = static_cast<float>(h >> 20), places = static_cast<float>(h & 0xfffffu);
-          return (c - 0.00541521235f / 64.0f * (places - 32.0f * c)) * exp2_approx(-j / kBinsPerOctave);
-        },
-        [&](float total, float* t) {
-          const float error = kBinError + kLastBinError * static_cast<float>(a.vocab);
-          const float r = (1.0f - error) / (1.0f + error);
-          t[0] = by_k ? static_cast<float>(k) : p * r * total;
-          t[1] = by_k ? INFINITY : p / r * total;
-        },
-        hit);
-    if (!by_k) {
-      b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;
-      b1 = hit[1].at < 0 ? kBins - 1 : hit[1].at;
-    } else if (hit[0].at >= 0) {                         // else fewer than k candidates
-      if (hit[0].upto <= kList) {                          // all that top-k may keep to one list
-        const int p1 = 64 * hit[0].at + 63;
-        const float from =
-            s.scale.top == INFINITY ? -FLT_MAX : fmaxf(s.scale.top - (p1 + 64) * s.scale.c_inverse, -FLT_MAX);
+    __syncthreads();
+    if (!s.close_lists()) {
+      s.cluster.sync();                                    // every rank has read the lists' sizes
+      return false;
+    }
+    unsigned token;
+    float l;
+    u64 mass;
+    if (s.rank == 0 && s.draw_of_lists(k, by_p, p, least, u, &token, &l, &mass)) {
+      a.tokens[b] = static_cast<int32_t>(token);
+      if (a.logprob) a.logprob[b] = log_share(s.scale, l, heat, mass);
+    }
+    return true;
+  };
+  u64 border = 0;                                        // ranks below it are cut off
+  int b0 = 0, b1 = kBins - 1;                            // bins the border of top-p lies in
+  typename Sampler<T, STAGED>::Hit hit[2];
+  hit[0].at = -1;
+  // first without a histogram, where the groups leave few elements; then with one
+  bool counted = !(group > 0 && lanes / group <= kFew && (low > 0 || a.vocab <= kList));
+  for (;; counted = true) {
+    float from = floor_k;
+    int p1 = 64 * kBins;
+    bool listed = !counted;
+    if (counted && (by_k || by_p)) {
 #pragma unroll 1
-        for (int i = v0 + tid; i < v1; i += kThreads) {
-          float f[N];
-          s.row.get(i, f);
+      for (int i = v0 + tid; i < v1; i += kThreads) {
+        float f[N];
+        s.row.get(i, f);
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (f[e] >= from && s.place(f[e]) <= p1)
-              s.offer(rank_of(key_of(f[e]), static_cast<unsigned>(i * N + e - s.row.shift)), 1);
-        }
-        __syncthreads();
-        if (s.close_lists()) {                             // (else a rank has more than its share of them)
-          if (s.rank != 0) return;
-          unsigned token;
-          float l;
-          u64 mass;
-          if (s.draw_of_lists(k, by_p, p, least, u, &token, &l, &mass)) {
-            a.tokens[b] = static_cast<int32_t>(token);
-            if (a.logprob) a.logprob[b] = log_share(s.scale, l, heat, mass);
+        for (int e = 0; e < N; ++e)
+          if (f[e] >= floor_k) {
+            const int at = s.place(f[e]);
+            atomicAdd(&mem()->hist[at >> 6], by_k ? 1u : (1u << 20) + (at & 63));
           }
-          return;
-        }
-        s.cluster.sync();                                  // every rank has read the lists' sizes
       }
-      const BorderTurn found = border_call<T, STAGED>(s, false, 64 * hit[0].at, 64 * hit[0].at + 63, 0,
-                                                      static_cast<u64>(hit[0].before), static_cast<u64>(k));
-      border = found.border;
-      s.turn = found.turn;
-      b1 = hit[0].at;
+      // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
+      s.find_bins(
+          [&](int j) {
+            const unsigned h = mem()->hist[j];
+            if (by_k) return static_cast<float>(h);
+            const float c = static_cast<float>(h >> 20), places = static_cast<float>(h & 0xfffffu);
+            return (c - 0.00541521235f / 64.0f * (places - 32.0f * c)) * exp2_approx(-j / kBinsPerOctave);
+          },
+          [&](float total, float* t) {
+            const float error = kBinError + kLastBinError * static_cast<float>(a.vocab);
+            const float r = (1.0f - error) / (1.0f + error);
+            t[0] = by_k ? static_cast<float>(k) : p * r * total;
+            t[1] = by_k ? INFINITY : p / r * total;
+          },
+          hit);
+      if (by_k) {
+        listed = hit[0].at >= 0 && hit[0].upto <= kList;
+        from = fmaxf(s.logit_of(64 * hit[0].at + 128), floor_k);
+        p1 = 64 * hit[0].at + 63;
+      } else {
+        b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;
+        b1 = hit[1].at < 0 ? kBins - 1 : hit[1].at;
+      }
     }
+    if (listed && draw_first(from, p1)) return;
+    if (counted) break;
+  }
+  if (by_k && hit[0].at >= 0) {                          // (else fewer than k candidates)
+    const BorderTurn found = border_call<T, STAGED>(s, false, 64 * hit[0].at, 64 * hit[0].at + 63, 0,
+                                                    static_cast<u64>(hit[0].before), static_cast<u64>(k));
+    border = found.border;
+    s.turn = found.turn;
+    b1 = hit[0].at;
   }
 
   // A contiguous run of vectors per warp.
