@@ -486,7 +486,9 @@ GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void*
   if (n_q_heads % n_kv_heads != 0)
     return fail(GBF_EINVAL, "%s: n_q_heads (%d) must be a multiple of n_kv_heads (%d)", fn, n_q_heads, n_kv_heads);
   if (table_stride < max_blocks) return fail(GBF_EINVAL, "%s: table_stride must be >= max_blocks", fn);
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(GBF_EINVAL, "%s: scale must be finite and > 0", fn);
+  const float scale_log2 = scale * 1.44269504088896341f;
+  if (!(scale_log2 > 0.0f) || !std::isfinite(scale_log2))
+    return fail(GBF_EINVAL, "%s: scale must be > 0, and finite times log2(e)", fn);
   if (!(out_scale >= 0.0f) || !std::isfinite(out_scale))
     return fail(GBF_EINVAL, "%s: out_scale must be finite and >= 0", fn);
   if (out_scale > 0.0f && !std::isfinite(1.0f / out_scale))
@@ -539,7 +541,7 @@ GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void*
   a.window = static_cast<int>(window < lim ? window : 0);     // longer than any length: the whole length
   a.out_fp8 = out_scale > 0.0f ? 1 : 0;
   a.inv_out_scale = out_scale > 0.0f ? 1.0f / out_scale : 0.0f;
-  a.scale_log2 = scale * 1.44269504088896341f;
+  a.scale_log2 = scale_log2;
   return launch_status(gbf::launch_paged_attention(a, static_cast<cudaStream_t>(stream)), fn);
 }
 

@@ -54,6 +54,7 @@ struct PagedAttnArgs {
   float scale_log2;         // softmax scale * log2(e)
   float inv_out_scale;
   // set by the launcher
+  int room;                 // longest length: max_blocks * block_size, and positions of a tile stay below 2^31
   int block_shift;          // log2(block_size), or -1
   int group, chunks;        // query heads per KV head; row tiles they are cut into
   int min_units;            // least token tiles per CTA

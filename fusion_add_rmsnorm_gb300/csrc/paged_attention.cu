@@ -118,9 +118,8 @@ struct Request {
 GBF_DEVICE Request request_of(const PagedAttnArgs& a, int b) {
   Request r;
   r.len = a.lens[b];
-  const int64_t room = static_cast<int64_t>(a.max_blocks) * a.block_size;
   if (r.len < 0) r.len = 0;
-  if (r.len > room) r.len = static_cast<int>(room);
+  if (r.len > a.room) r.len = a.room;
   r.lo = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
   r.tiles = (r.len - r.lo + kTile - 1) / kTile;
   return r;
@@ -149,7 +148,7 @@ GBF_DEVICE Place locate(const PagedAttnArgs& a, int64_t c, bool report) {
   for (int b = b0; b < b1; ++b) {
     mine += request_of(a, b).tiles + kOwn;
     const int len = a.lens[b];
-    bad |= len < 0 || len > static_cast<int64_t>(a.max_blocks) * a.block_size;
+    bad |= len < 0 || len > a.room;
   }
   if (bad && report) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
   mine *= items;
@@ -701,8 +700,7 @@ cudaError_t launch(PagedAttnArgs a, cudaStream_t stream) {
   cudaError_t e = allow_smem<paged_attention_kernel<DP, WIDE>>(smem_bytes<DP>());
   if (e != cudaSuccess) return e;
   a.min_units = NW;
-  const int64_t most = static_cast<int64_t>(a.max_blocks) * a.block_size;
-  const int64_t seen = a.window > 0 && a.window < most ? a.window : most;
+  const int64_t seen = a.window > 0 && a.window < a.room ? a.window : a.room;
   const int64_t tiles = (seen + kTile - 1) / kTile;
   const int64_t units = (tiles + kOwn) * a.batch * a.hkv * a.chunks;
   int64_t ctas = (units + NW - 1) / NW;
@@ -726,6 +724,8 @@ int64_t paged_attention_workspace(int hq, int hkv, int d) {
 cudaError_t launch_paged_attention(PagedAttnArgs a, cudaStream_t stream) {
   a.group = a.hq / a.hkv;
   a.chunks = (a.group + 15) / 16;
+  const int64_t room = static_cast<int64_t>(a.max_blocks) * a.block_size, most = 0x7fffffff - kTile;
+  a.room = static_cast<int>(room < most ? room : most);
   a.block_shift = -1;
   for (int s = 0; s < 31; ++s)
     if (a.block_size == 1 << s) a.block_shift = s;

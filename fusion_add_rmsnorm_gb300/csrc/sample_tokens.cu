@@ -201,13 +201,11 @@ GBF_DEVICE void weights(const u64* pow, const RowScale& s, float2 l, u64* w0, u6
 
 // exp((l - top) / T) of two logits in float32, hi + lo within 2^-25: the same argument; 1 + x ln 2 exactly (in two
 // parts), the rest of the fraction's power by a polynomial (minimax on +-0.502: 2^-28.2; 2^-26.1 as evaluated).
-// Logits more than 60 octaves below the top count as 60 octaves below: `lowest`.
+// Zero more than 60 octaves below the top (and for -inf).
 struct Pair2 {
   float2 hi, lo;
 };
-GBF_DEVICE Pair2 quick_weights(const RowScale& s, float2 l, float lowest) {
-  l.x = fmaxf(l.x, lowest);
-  l.y = fmaxf(l.y, lowest);
+GBF_DEVICE Pair2 quick_weights(const RowScale& s, float2 l) {
   const float2 d = __fadd2_rn(l, two(-s.top));
   const float2 e = sub2(d, l);
   const float2 d_lo = sub2(sub2(l, sub2(d, e)), __fadd2_rn(e, two(s.top)));
@@ -236,7 +234,10 @@ GBF_DEVICE Pair2 quick_weights(const RowScale& s, float2 l, float lowest) {
   // times 2^n: n stands in the low bits of q
   const float2 scale = make_float2(__int_as_float((__float_as_int(q.x) << 23) + 0x3f800000),
                                    __int_as_float((__float_as_int(q.y) << 23) + 0x3f800000));
-  return {__fmul2_rn(hi, scale), __fmul2_rn(b, scale)};
+  Pair2 w{__fmul2_rn(hi, scale), __fmul2_rn(b, scale)};
+  if (!(nt.x < 60.0f)) w.hi.x = w.lo.x = 0.0f;
+  if (!(nt.y < 60.0f)) w.hi.y = w.lo.y = 0.0f;
+  return w;
 }
 
 // A sum of weights that loses nothing: what each addition rounds off is added up beside it, with the weights' low
@@ -1143,7 +1144,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const u64 k_border = border;
   const float border_l = border ? of_key(static_cast<unsigned>(border >> 32)) : -FLT_MAX;
   const float from_l = by_p ? border_l : fmaxf(border_l, floor_l);
-  const float lowest = fmaxf(s.scale.top - 41.5f * heat, -FLT_MAX);
   // float32 first: where there is much to weigh (top-k leaves little), and no two criteria meet in one sum
   bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || s.scale.top == INFINITY;
 
@@ -1167,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (exact) {
         s.weigh(two(l), &w0, &w1);
       } else {
-        const Pair2 w = quick_weights(s.scale, two(l), lowest);
+        const Pair2 w = quick_weights(s.scale, two(l));
         w0 = fixed_of(w.hi.x, w.lo.x);
       }
       return w0;
@@ -1194,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
           const float2 l = make_float2(f[e], f[e + 1]);
-          Pair2 w = quick_weights(s.scale, l, lowest);
+          Pair2 w = quick_weights(s.scale, l);
           if (by_p) {
             sum.add(w.hi, w.lo);
             const bool a0 = l.x > above_l, a1 = l.y > above_l;
@@ -1362,7 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (exact) {
             s.weigh(f, &w[0], &w[1]);
           } else {
-            const Pair2 q = quick_weights(s.scale, f, lowest);
+            const Pair2 q = quick_weights(s.scale, f);
             w[0] = q.hi.x >= mp ? fixed_of(q.hi.x, q.lo.x) : 0;
             w[1] = q.hi.y >= mp ? fixed_of(q.hi.y, q.lo.y) : 0;
           }

@@ -253,8 +253,9 @@ GBF_API int gbf_copy(const void* src, void* dst, int64_t bytes, void* stream);
 /*
  * gbf_device_status -- synchronise `stream`, then read and clear the current
  * device's error word.  Returns GBF_OK, GBF_ETIMEOUT (a bounded wait gave up)
- * or GBF_EDEVICE (a cache slot was out of range, or the two CTAs of a GEMM
- * tensor-core pair were given different TMEM bases), or GBF_ELAUNCH if the
+ * or GBF_EDEVICE (a cache slot was out of range, the two CTAs of a GEMM
+ * tensor-core pair were given different TMEM bases, or a decode-step operator
+ * caught one of the faults gbfuse_decode.h lists), or GBF_ELAUNCH if the
  * synchronisation itself reported a CUDA error.
  */
 GBF_API int gbf_device_status(void* stream);

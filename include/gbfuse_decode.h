@@ -60,6 +60,7 @@ extern "C" {
  * tokens than `tokens`, a ring state out of range or one that would hold more
  * than num_blocks sets it too; the excess is not written.
  * Requires batch <= 8192, block_size >= 1, num_blocks * block_size < 2^31.
+ * batch == 0 enqueues nothing and writes nothing.
  */
 GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch, int32_t* block_table,
                              int64_t table_stride, int64_t max_blocks, int block_size, int32_t* free_ring,
@@ -83,12 +84,12 @@ GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, i
  * lse: device float32 [batch, n_q_heads] or NULL.  workspace: device memory of
  * gbfd_paged_attention_workspace() bytes, whose contents need not be set and do
  * not outlive the call; calls that may run at the same time need their own.
- * A length outside [0, max_blocks * block_size] is clamped, and a position
+ * A length outside [0, max_blocks * block_size] (or above 2^31 - 17) is clamped, and a position
  * whose block id lies outside the cache is left out; both set the device error
  * word.  Rows of the cache no position refers to are not read.
  * Requires head_dim % 16 == 0, head_dim <= 256, n_q_heads % n_kv_heads == 0,
  * cache_rows < 2^31, 16-byte aligned q, k_cache, v_cache, out, workspace; scale
- * finite and > 0.  out and lse may not overlap each other or an input.
+ * > 0 and finite.  batch == 0 enqueues nothing.  out and lse may not overlap each other or an input.
  */
 GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void* v_cache, int64_t cache_rows,
                                  const int32_t* block_table, int64_t table_stride, int64_t max_blocks,
@@ -112,7 +113,7 @@ GBF_API int64_t gbfd_paged_attention_workspace(int n_q_heads, int n_kv_heads, in
  *   min-p keeps, of those, the ones with w_i >= min_p (<= 0: all);
  *   the token is, in index order, the first at which the running kept mass
  *     passes u times the kept mass.
- * T = 0 takes the largest logit (the lowest index of equals) whatever else is
+ * Temperatures below 1e-30 count as 1e-30.  T = 0 takes the largest logit (the lowest index of equals) whatever else is
  * set.  Weights are 43-bit fixed-point numbers and their sums exact, so the
  * token does not depend on the order of summation.  logprob = ln(w / kept mass)
  * of the token, 0 for T = 0.  -inf and NaN logits are no candidates.

@@ -168,6 +168,39 @@ def test_extreme_parameters(gbf):
     assert gbf.device_status()[0] == gbf.OK
 
 
+@pytest.mark.parametrize("scale,shift", [(1e30, 0.0), (1e9, 1e12), (1e-30, 0.0), (3e37, -3e38), (1e-3, 1e6), (1e-38, 0.0)])
+def test_logits_of_any_size(gbf, scale, shift):
+    """Logits whose differences are far larger or smaller than 1, or lost in their size."""
+    rng = np.random.default_rng(17)
+    with np.errstate(over="ignore"):                          # some become infinite
+        l = (rng.standard_normal((8, 20000)) * scale + shift).astype(np.float32)
+    l[3, 5:] = l[3, 4]
+    u = rng.random(8).astype(np.float32)
+    for t in (1.0, float(np.float32(min(scale, 1e20)))):
+        t = np.full(8, max(t, 1e-29), np.float32)
+        for q in (dict(), dict(top_p=np.full(8, 0.7)), dict(top_k=np.full(8, 40)), dict(min_p=np.full(8, 0.1))):
+            check(l, u, run(gbf, l, u, True, temperature=t, **q), temperature=t, **q, skip=4)
+    assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("f32,batch", [(True, 3), (False, 3), (True, 160), (False, 160)])
+def test_long_runs_of_equals(gbf, f32, batch):
+    """Tens of thousands of equal logits in one CTA's slice, one CTA or several per
+    row: a bin overflows its counter, the lists overflow, the border is found by
+    logit and index."""
+    rng = np.random.default_rng(18)
+    vocab = 70001
+    row = np.full(vocab, 2.0, np.float32)
+    row[::7] = 1.0
+    row[::11] = -np.inf
+    l, u = np.tile(row, (batch, 1)), rng.random(batch).astype(np.float32)
+    k, p = rng.integers(1, vocab, batch), (0.05 + 0.9 * rng.random(batch)).astype(np.float32)
+    some = np.r_[0:2, batch - 1]
+    for q in (dict(top_k=k), dict(top_p=p), dict(top_k=k, top_p=p), dict()):
+        tokens, lps = run(gbf, l, u, f32, **q)
+        check(l[some], u[some], (tokens[some], lps[some]), **{n: v[some] for n, v in q.items()}, skip=3)
+
+
 def test_parameters_out_of_range_are_reported(gbf):
     rng = np.random.default_rng(14)
     l, u = logits(rng, 4, 500, False), np.full(4, 0.5, np.float32)
