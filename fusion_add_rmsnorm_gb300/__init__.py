@@ -9,7 +9,9 @@ wrapper checks what the C library cannot: every operand holds exactly the
 elements the call will read or write (ValueError otherwise), is a contiguous
 torch tensor of the element type the call reads, on the current device.
 There is no CPU path: importing this package fails when the compiled library
-is missing, and every call fails without a CUDA device.
+is missing, and every call fails without a CUDA device.  The wrappers of the
+decode-step calls (paged_slots, paged_attention, sample_tokens) are compiled,
+because those calls are about as short as their checks would be in Python.
 
 Build the library with `python -c "import __graft_entry__ as g; g.build()"`
 (or `python fusion_add_rmsnorm_gb300/build.py`).
@@ -75,6 +77,13 @@ class GbfError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"status {status}: {message}")
         self.status = status
+
+
+# the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
+from . import decode_binding as _decode     # noqa: E402
+from .decode_binding import paged_attention, paged_slots, sample_tokens     # noqa: E402, F401
+
+_decode.set_error(GbfError)
 
 
 def _check(status):
@@ -275,145 +284,12 @@ def bn_fold(w, b, gamma, beta, mean, var, eps, w_out, b_out, stream=None):
                                    _stream(stream)))
 
 
-# The decode-step calls are a few microseconds long, so their wrappers check an
-# operand in one pass and look the device and the stream up once per call.
-
-def _operand(t, n, dtype, name, device):
-    """Data pointer of a dense operand of n elements of `dtype` on `device`, the
-    current CUDA device; None passes through (an optional operand)."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.numel() != n:
-        raise ValueError(f"{name}: holds {t.numel()} elements, the call needs {n}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.get_device() != device and device >= 0:
-        _wrong_device(t, name, device)
-    return t.data_ptr()
-
-
-def _wrong_device(t, name, device):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be on a CUDA device")
-    raise ValueError(f"{name}: is on cuda:{t.get_device()}, the current device is cuda:{device}")
-
-
-def _strided(t, batch, dtype, name, device):
-    """(data pointer, row length, row stride) of a [batch, n] operand whose rows may
-    be apart (a column range of a wider tensor)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dim() != 2 or (batch is not None and t.shape[0] != batch):
-        raise ValueError(f"{name}: expected [{'batch' if batch is None else batch}, n], got {list(t.shape)}")
-    rows, width = t.shape
-    apart, step = t.stride()
-    if width > 1 and step != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if rows <= 1:
-        apart = width
-    elif apart < width:
-        raise ValueError(f"{name}: rows may not overlap")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != device and device >= 0:
-        _wrong_device(t, name, device)
-    return t.data_ptr(), width, apart
-
-
-def _device_of(t, name):
-    """The current CUDA device, or -1 when `t`, the call's first operand, is on none
-    (there may be none): the other operands' extents are checked all the same, and
-    the call ends in _raw_stream."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    return torch._C._cuda_getDevice() if t.is_cuda else -1
-
-
-def _raw_stream(stream, device):
-    """cudaStream_t of `stream`, by default of the current torch stream.  The last
-    argument of a call to be evaluated, so the last check too."""
-    if device < 0:
-        raise ValueError("the operands must be on a CUDA device")
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-
-
-def paged_slots(ctx_lens, new_lens, block_table, free_ring, ring, block_size, seq_lens, ring_out, slots, pos,
-                start=None, stream=None):
-    """gbfd_paged_slots: block tables, slot maps and positions of one step from
-    the requests' lengths.  ctx_lens, new_lens, seq_lens [batch]; block_table
-    [batch, max_blocks] (rows may be apart); free_ring [num_blocks]; ring,
-    ring_out [2]; slots, pos [tokens]; start [batch + 1] or None; all int32."""
-    d = _device_of(ctx_lens, "ctx_lens")
-    batch, blocks, tokens = ctx_lens.numel(), _numel(free_ring, "free_ring"), _numel(slots, "slots")
-    table_p, width, apart = _strided(block_table, batch, _I32, "block_table", d)
-    return _check(_lib.gbfd_paged_slots(
-        _operand(ctx_lens, batch, _I32, "ctx_lens", d), _operand(new_lens, batch, _I32, "new_lens", d), batch, table_p,
-        apart, width, block_size,
-        _operand(free_ring, blocks, _I32, "free_ring", d), _operand(ring, 2, _I32, "ring", d), blocks,
-        _operand(seq_lens, batch, _I32, "seq_lens", d), _operand(ring_out, 2, _I32, "ring_out", d),
-        _operand(slots, tokens, _I32, "slots", d), _operand(pos, tokens, _I32, "pos", d), tokens,
-        _operand(start, batch + 1, _I32, "start", d), _raw_stream(stream, d)))
-
-
 def paged_attention_workspace(n_q_heads, n_kv_heads, head_dim):
     """Bytes of workspace paged_attention needs with these heads, for any batch."""
     n = _lib.gbfd_paged_attention_workspace(n_q_heads, n_kv_heads, head_dim)
     if n <= 0:
         raise ValueError(f"heads not supported: {n_q_heads} query, {n_kv_heads} KV, head_dim {head_dim}")
     return n
-
-
-def paged_attention(q, k_cache, v_cache, block_table, seq_lens, block_size, out, workspace, scale=None, window=0,
-                    lse=None, out_scale=None, stream=None):
-    """gbfd_paged_attention: out[b] = attention of q[b] over the seq_lens[b]
-    cached positions of request b.  q [batch, n_q_heads, head_dim]; k_cache,
-    v_cache [cache_rows, n_kv_heads, head_dim]; block_table [batch, max_blocks]
-    (rows may be apart); out as q in bf16, or uint8 E4M3 codes with out_scale;
-    workspace: any dense tensor of at least paged_attention_workspace() bytes;
-    scale defaults to head_dim ** -0.5."""
-    d = _device_of(q, "q")
-    if q.dim() != 3:
-        raise ValueError(f"q: expected [batch, n_q_heads, head_dim], got {list(q.shape)}")
-    batch, hq, dim = q.shape
-    _numel(k_cache, "k_cache")
-    if k_cache.dim() != 3 or k_cache.shape[2] != dim:
-        raise ValueError(f"k_cache: expected [cache_rows, n_kv_heads, {dim}], got {list(k_cache.shape)}")
-    rows, hkv, _ = k_cache.shape
-    n, cached, room = q.numel(), k_cache.numel(), _numel(workspace, "workspace")
-    if out_scale is not None and not out_scale > 0.0:
-        raise ValueError(f"out_scale: must be > 0, got {out_scale}")
-    table_p, width, apart = _strided(block_table, batch, _I32, "block_table", d)
-    return _check(_lib.gbfd_paged_attention(
-        _operand(q, n, _BF16, "q", d), _operand(k_cache, cached, _BF16, "k_cache", d),
-        _operand(v_cache, cached, _BF16, "v_cache", d), rows, table_p, apart, width, block_size,
-        _operand(seq_lens, batch, _I32, "seq_lens", d), batch, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
-        window, _operand(out, n, _BF16 if out_scale is None else _U8, "out", d),
-        0.0 if out_scale is None else out_scale, _operand(lse, batch * hq, _F32, "lse", d),
-        _operand(workspace, room, workspace.dtype, "workspace", d), room * workspace.element_size(),
-        _raw_stream(stream, d)))
-
-
-def sample_tokens(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
-                  stream=None):
-    """gbfd_sample_tokens: tokens[b] drawn from logits[b] (bf16 or float32
-    [batch, vocab], rows may be apart) with the given uniform[b] and, where the
-    tensors are given, temperature, top_k (int32), top_p and min_p of each row."""
-    d = _device_of(logits, "logits")
-    kind = logits.dtype
-    if kind is not _BF16 and kind is not _F32:
-        raise TypeError(f"logits: expected torch.bfloat16 or torch.float32, got {kind}")
-    logits_p, vocab, apart = _strided(logits, None, kind, "logits", d)
-    batch = logits.shape[0]
-    return _check(_lib.gbfd_sample_tokens(
-        logits_p, 1 if kind is _F32 else 0, batch, vocab, apart, _operand(uniform, batch, _F32, "uniform", d),
-        _operand(temperature, batch, _F32, "temperature", d), _operand(top_k, batch, _I32, "top_k", d),
-        _operand(top_p, batch, _F32, "top_p", d), _operand(min_p, batch, _F32, "min_p", d),
-        _operand(tokens, batch, _I32, "tokens", d), _operand(logprob, batch, _F32, "logprob", d),
-        _raw_stream(stream, d)))
 
 
 def copy(src, dst, nbytes=None, stream=None):

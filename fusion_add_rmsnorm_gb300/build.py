@@ -1,23 +1,30 @@
-"""Build libgbfuse.so in-tree with nvcc for sm_103a.
+"""Build libgbfuse.so in-tree with nvcc for sm_103a, and the compiled part of the
+Python binding with the host compiler.
 
 Each CUDA translation unit under csrc/ is compiled to an object in parallel,
 then linked into fusion_add_rmsnorm_gb300/libgbfuse.so with the CUDA runtime
 linked statically (the library loads without a GPU driver; kernels need one).
 Objects go to fusion_add_rmsnorm_gb300/_build/ (git-ignored).  A source whose
 object is newer than the source and every header is not recompiled.
+binding/decode_binding.cpp (the wrappers of the decode-step calls) becomes
+fusion_add_rmsnorm_gb300/decode_binding.so against the installed torch.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgbfuse.so")
+BINDING_SRC = os.path.join(HERE, "binding", "decode_binding.cpp")
+BINDING = os.path.join(HERE, "decode_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
@@ -60,9 +67,11 @@ def build(verbose=False, extra_flags=()):
         return r.stderr if verbose else None
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(compile_binding, hdr_mtime)
         for out in ex.map(compile_one, zip(srcs, objs)):
             if out:
                 sys.stderr.write(out)
+        binding_obj = binding.result()
     if not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         tmp = LIB + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -70,7 +79,40 @@ def build(verbose=False, extra_flags=()):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    link_binding(binding_obj)
     return LIB
+
+
+def _torch_dir():
+    # found, not imported: the paths are all that is needed
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def compile_binding(hdr_mtime):
+    obj = os.path.join(BUILD, "decode_binding.o")
+    torch_mtime = os.path.getmtime(os.path.join(_torch_dir(), "version.py"))     # another torch is another ABI
+    if _stale(BINDING_SRC, obj, max(hdr_mtime, torch_mtime)):
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+        inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(_torch_dir(), "include"), cuda]
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{p}" for p in inc], "-c", BINDING_SRC,
+              "-o", obj], "g++ on decode_binding.cpp")
+    return obj
+
+
+def link_binding(obj):
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
+        return
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{lib}", "-ltorch_python", "-lc10", "-lc10_cuda", "-ltorch_cpu", f"-L{HERE}",
+          "-l:libgbfuse.so", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"], "link of decode_binding.so")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

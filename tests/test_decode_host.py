@@ -146,3 +146,36 @@ def test_sample_tokens_operands(gbf):
     raises("CUDA device", gbf.sample_tokens, **good)
     with pytest.raises(TypeError, match="logits"):
         gbf.sample_tokens(**{**good, "logits": torch.zeros(3, 40, dtype=torch.float16)})
+
+
+def test_compiled_wrappers_arguments(gbf):
+    slots = dict(ctx_lens=i32(3), new_lens=i32(3), block_table=i32(3, 4), free_ring=i32(16), ring=i32(2), block_size=16,
+                 seq_lens=i32(3), ring_out=i32(2), slots=i32(5), pos=i32(5))
+    attn = dict(q=bf(2, 8, 64), k_cache=bf(32, 2, 64), v_cache=bf(32, 2, 64), block_table=i32(2, 2), seq_lens=i32(2),
+                block_size=16, out=bf(2, 8, 64), workspace=u8(1 << 22))
+    draw = dict(logits=bf(3, 40), uniform=f32(3), tokens=i32(3))
+    for fn, good in ((gbf.paged_slots, slots), (gbf.paged_attention, attn), (gbf.sample_tokens, draw)):
+        raises("CUDA device", fn, *good.values())                       # by position, the optional ones left out
+        for name in good:
+            with pytest.raises(TypeError, match=name):                  # a required argument left out
+                fn(**{k: v for k, v in good.items() if k != name})
+            with pytest.raises(TypeError, match=name):                  # not what the argument takes
+                fn(**{**good, name: "x"})
+        first = next(iter(good))
+        with pytest.raises(TypeError, match=first):
+            fn(*good.values(), **{first: good[first]})                  # given twice
+        with pytest.raises(TypeError, match="blocks"):
+            fn(**good, blocks=1)                                        # no such argument
+        with pytest.raises(TypeError, match="at most"):
+            fn(*[None] * 20)
+    for name in ("ctx_lens", "block_table", "slots", "free_ring"):
+        with pytest.raises(TypeError, match=name):
+            gbf.paged_slots(**{**slots, name: slots[name].long()})
+    with pytest.raises(TypeError, match="block_size"):
+        gbf.paged_slots(**{**slots, "block_size": 16.0})
+    raises("block_size", gbf.paged_slots, **{**slots, "block_size": 1 << 33})
+    # an out_scale that is 0 in float32 would ask for bf16 output, twice the bytes that `out` holds
+    for bad in (1e-60, -1.0, float("nan")):
+        raises("out_scale", gbf.paged_attention, **{**attn, "out": u8(2, 8, 64), "out_scale": bad})
+    with pytest.raises(TypeError, match="out"):
+        gbf.paged_attention(**{**attn, "out_scale": 1.0})
