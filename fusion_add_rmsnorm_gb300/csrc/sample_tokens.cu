@@ -46,10 +46,10 @@
 //
 // The exact weight is the dear part (some 45 integer instructions, which run at
 // half rate), so a long slice is first done in float32 with an error bound: the
-// weight to 2^-23 in float32 arithmetic alone, compensated sums, and every
-// decision checked against twice that bound.  A row in which all decisions
-// clear it is done; the others (a few in a hundred with nuclei of 10^4 tokens)
-// are done again exactly.
+// weight to 2^-32 in pairs of float32, compensated sums, and every decision
+// checked against twice that bound.  A row in which all decisions clear it is
+// done; the others (one in some thousands with nuclei of 10^5 tokens) are done
+// again exactly.
 //
 // Ranks hand each other totals by remote stores into boxes (read locally behind
 // the next barrier).
@@ -83,6 +83,7 @@ constexpr int kNear = 2048;                 // this rank's elements in the bins 
 constexpr int kFilterVectors = 512;         // slices of more 16-byte vectors are first done in float32
 constexpr int kSpans = 32;                  // parts that the bins that may hold top-p's border are cut into
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
+constexpr int kQuickFix = 42;               // 2^42: the unit of the float32 pass's sums
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
 constexpr float kLeastTemperature = 1e-30f;
 constexpr int kSms = 152;
@@ -106,6 +107,7 @@ __device__ const u64 kPow[64] = {
 struct __align__(16) Shared {
   unsigned hist[kBins];
   u64 pow[64];
+  float2 sixteenth[16];        // 2^(j / 16) in two parts
   u64 list[kList];             // candidates of every rank, as (key, ~index)
   union {
     struct {
@@ -147,6 +149,8 @@ struct RowScale {
   float c_hi, c_lo;        // log2(e) / T
   float c_place;           // places (64ths of a bin) per unit of logit, and about its inverse
   float c_inverse;
+  float cut;               // 60 octaves below the top
+  int n_top;               // see quick_weights
 };
 
 GBF_DEVICE float2 two(float x) { return make_float2(x, x); }
@@ -199,45 +203,47 @@ GBF_DEVICE void weights(const u64* pow, const RowScale& s, float2 l, u64* w0, u6
   *w1 = assemble(pow, nt.y, q.y, qa.y, qb.y);
 }
 
-// exp((l - top) / T) of two logits in float32, hi + lo within 2^-25: the same argument; 1 + x ln 2 exactly (in two
-// parts), the rest of the fraction's power by a polynomial (minimax on +-0.502: 2^-28.2; 2^-26.1 as evaluated).
-// Zero more than 60 octaves below the top (and for -inf).
+// The float32 pass's weights: exp(l / T) of two logits over 2^N, in float32 hi + lo within 2^-32 (2^-33.7 seen over 10^7
+// logits), N as for the largest logit (scale.n_top), whose weight lies in [1/2, 1.02).  The argument l / T log2(e) =
+// m + x + xl with m a multiple of 1/16, which a rounding addition leaves in the low bits of q; |x| <= 2^-5, exactly;
+// 2^m from the table and an exponent, 2^(x + xl) - 1 = a + b: the linear term in two parts, the rest by a polynomial
+// (minimax, 2^-36).  Logits more than 60 octaves below the top are taken as those there: 2^-60 each is lost in any sum.
+// For rows with |top| / T log2(e) < 2^14 (xl's own rounding: 2^-34).
+constexpr float kMagic = 786432.0f;         // 1.5 * 2^19: a float of 1/16 ulp
+constexpr float kQuickRange = 16384.0f, kQuickHeat = 1e30f;
 struct Pair2 {
   float2 hi, lo;
 };
-GBF_DEVICE Pair2 quick_weights(const RowScale& s, float2 l) {
-  const float2 d = __fadd2_rn(l, two(-s.top));
-  const float2 e = sub2(d, l);
-  const float2 d_lo = sub2(sub2(l, sub2(d, e)), __fadd2_rn(e, two(s.top)));
-  const float2 nt = __fmul2_rn(d, two(-s.c_hi));
-  float2 lo = __ffma2_rn(d, two(s.c_hi), nt);
-  lo = __ffma2_rn(d, two(s.c_lo), lo);
-  lo = __ffma2_rn(d_lo, two(s.c_hi), lo);
-  const float2 q = sub2(two(12582912.0f), nt);                      // rounds t to an integer, n
-  const float2 ng = __fadd2_rn(__fadd2_rn(q, two(-12582912.0f)), nt);
-  const float2 x = sub2(lo, ng), xl = sub2(lo, __fadd2_rn(x, ng));
+GBF_DEVICE Pair2 quick_weights(const float2* sixteenth, const RowScale& s, float2 l) {
+  l = make_float2(fmaxf(l.x, s.cut), fmaxf(l.y, s.cut));
+  const float2 np = __fmul2_rn(l, two(-s.c_hi));                    // (negative parts where an instruction needs them)
+  const float2 q = sub2(two(kMagic), np);
+  const float2 nx = __fadd2_rn(__fadd2_rn(q, two(-kMagic)), np);    // exact
+  float2 xl = __ffma2_rn(l, two(s.c_hi), np);                       // what the product lacks
+  xl = __ffma2_rn(l, two(s.c_lo), xl);
+  const float2 x = sub2(xl, nx);
+  xl = sub2(xl, __fadd2_rn(x, nx));
   constexpr float kL = 0.693147180559945309f;
   constexpr float kLl = static_cast<float>(0.693147180559945309417 - static_cast<double>(kL));
-  const float2 a = __fmul2_rn(x, two(kL));
-  float2 r = __ffma2_rn(x, two(0.00015320504f), two(0.0013390614f));
-  r = __ffma2_rn(x, r, two(0.0096185328f));
-  r = __ffma2_rn(x, r, two(0.055503614f));
-  r = __ffma2_rn(x, r, two(0.24022648f));
-  float2 b = __ffma2_rn(x, two(-kL), a);                            // -(what a lacks)
-  b = sub2(__fmul2_rn(xl, two(kL)), b);
+  const float2 a = __fmul2_rn(x, two(kL)), na = __fmul2_rn(x, two(-kL));
+  float2 b = __ffma2_rn(x, two(kL), na);
   b = __ffma2_rn(x, two(kLl), b);
+  b = __ffma2_rn(xl, two(kL), b);
+  float2 r = __ffma2_rn(x, two(0.00961828f), two(0.05550509f));
+  r = __ffma2_rn(x, r, two(0.2402265f));
   b = __ffma2_rn(__fmul2_rn(x, x), r, b);
-  const float2 one = __fadd2_rn(a, two(1.0f));
-  b = __fadd2_rn(b, sub2(a, __fadd2_rn(one, two(-1.0f))));
-  const float2 hi = __fadd2_rn(one, b);                             // hi: the weight rounded to float32
-  b = sub2(b, sub2(hi, one));
-  // times 2^n: n stands in the low bits of q
-  const float2 scale = make_float2(__int_as_float((__float_as_int(q.x) << 23) + 0x3f800000),
-                                   __int_as_float((__float_as_int(q.y) << 23) + 0x3f800000));
-  Pair2 w{__fmul2_rn(hi, scale), __fmul2_rn(b, scale)};
-  if (!(nt.x < 60.0f)) w.hi.x = w.lo.x = 0.0f;
-  if (!(nt.y < 60.0f)) w.hi.y = w.lo.y = 0.0f;
-  return w;
+  const int q0 = __float_as_int(q.x), q1 = __float_as_int(q.y);
+  const float2 t0 = sixteenth[q0 & 15], t1 = sixteenth[q1 & 15];    // 2^(j / 16), hi and lo
+  const unsigned e0 = static_cast<unsigned>((q0 >> 4) - s.n_top) << 23, e1 = static_cast<unsigned>((q1 >> 4) - s.n_top) << 23;
+  const float2 hi = make_float2(__uint_as_float(__float_as_uint(t0.x) + e0), __uint_as_float(__float_as_uint(t1.x) + e1));
+  const float2 lo = make_float2(__uint_as_float(__float_as_uint(t0.y) + e0), __uint_as_float(__float_as_uint(t1.y) + e1));
+  const float2 nz = __fmul2_rn(hi, na);
+  float2 rest = __ffma2_rn(hi, a, nz);
+  rest = __ffma2_rn(hi, b, rest);
+  rest = __ffma2_rn(lo, a, rest);
+  rest = __fadd2_rn(rest, lo);
+  const float2 w = sub2(hi, nz);
+  return {w, sub2(rest, __fadd2_rn(nz, sub2(w, hi)))};
 }
 
 // A sum of weights that loses nothing: what each addition rounds off is added up beside it, with the weights' low
@@ -250,23 +256,25 @@ struct Sum2 {
     s = t;
   }
   GBF_DEVICE u64 fixed() const {
-    constexpr float k = static_cast<float>(1ull << kFix);
+    constexpr float k = static_cast<float>(1ull << kQuickFix);
     return __float2ull_rn(s.x * k) + __float2ull_rn(s.y * k) +
            static_cast<u64>(__float2ll_rn(c.x * k) + __float2ll_rn(c.y * k));
   }
 };
 GBF_DEVICE u64 fixed_of(float hi, float lo) {
-  constexpr float k = static_cast<float>(1ull << kFix);
+  constexpr float k = static_cast<float>(1ull << kQuickFix);
   return __float2ull_rn(hi * k) + static_cast<u64>(__float2ll_rn(lo * k));
 }
-// what two float32 sums of masses may be apart by: twice 2^-25 of them, and the conversions' roundings
-GBF_DEVICE u64 slack_of(u64 total) { return (total >> 24) + 4096; }
+// What a float32 sum of masses and a share of another may be apart by: twice 2^-32 of them and as much again for the sums'
+// own roundings; and of the conversions to integers one unit for each thread's sums (twice 8 * 512) and each element near
+// the border (8 * kNear).
+GBF_DEVICE u64 slack_of(u64 total) { return (total >> 30) + 32768; }
 
-// ln(w / total) = (l - top) / T - ln(total / 2^43), both terms of one sign.
-GBF_DEVICE float log_share(const RowScale& s, float l, float heat, u64 total) {
+// ln(w / total) = (l - top) / T - ln(total / the top's weight), both terms of one sign.
+GBF_DEVICE float log_share(const RowScale& s, float l, float heat, u64 total, u64 of_top) {
   const float d = l == s.top ? 0.0f : (l - s.top) / heat;
-  const u64 more = total > 1ull << kFix ? total - (1ull << kFix) : 0;
-  return d - log1pf(static_cast<float>(more) * (1.0f / static_cast<float>(1ull << kFix)));
+  const u64 more = total > of_top ? total - of_top : 0;
+  return d - log1pf(static_cast<float>(more) / static_cast<float>(of_top));
 }
 
 // Place of a candidate in 64ths of a bin, half a bin ahead: its bin, and 0..63 within it.  Smaller logits never have a
@@ -354,9 +362,24 @@ struct Row {
     if (!STAGED) tidy<2>(f);
     return make_float2(f[0], f[1]);
   }
-  GBF_DEVICE void get(int v, float f[N]) const {
-    Elem<T>::widen(STAGED ? stage()[v - v0] : load(v), f);
+  GBF_DEVICE uint4 raw(int v) const { return STAGED ? stage()[v - v0] : load(v); }
+  static GBF_DEVICE void widen(uint4 v, float f[N]) {
+    Elem<T>::widen(v, f);
     if (!STAGED) tidy<N>(f);
+  }
+  GBF_DEVICE void get(int v, float f[N]) const { widen(raw(v), f); }
+  // f(v, elements) for v = from, from + step, ... below end; each vector is loaded a turn ahead
+  template <typename F>
+  GBF_DEVICE void each(int from, int end, int step, F f) const {
+    if (from >= end) return;
+    uint4 next = raw(from);
+#pragma unroll 1
+    for (int v = from; v < end; v += step) {
+      float x[N];
+      widen(next, x);
+      if (v + step < end) next = raw(v + step);
+      f(v, x);
+    }
   }
   GBF_DEVICE float2 pair_or_none(int j, int end) const {
     return j < end ? pair(j) : make_float2(-INFINITY, -INFINITY);
@@ -928,6 +951,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.turn = 0;
   const int tid = s.tid = threadIdx.x, lane = s.lane = tid & 31, warp = s.warp = tid >> 5;
   if (tid < 64) mem()->pow[tid] = kPow[tid];
+  if (tid < 16) {
+    const u64 p = kPow[4 * tid];
+    const float hi = __ull2float_rn(p);
+    // (the low part of 1 is not 0, which has no exponent to add to)
+    const float lo = tid ? __ll2float_rn(static_cast<long long>(p - __float2ull_rn(hi))) : 0x1p-17f;
+    mem()->sixteenth[tid] = make_float2(hi * 0x1p-43f, lo * 0x1p-43f);
+  }
   s.clear();
   pdl_wait();
   pdl_launch_dependents();
@@ -1011,6 +1041,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   const float floor_k = group > 0 && low > 0 ? of_key(low) : -FLT_MAX;
   s.scale.top = of_key(top);
+  const float quick_top = __fmul_rn(s.scale.top, s.scale.c_hi);
+  s.scale.cut = s.scale.top - 41.5f * heat;
+  s.scale.n_top = (__float_as_int(__fadd_rn(quick_top, kMagic)) >> 4) + 1;
 
   const bool bad = !(temp >= 0.0f && temp < INFINITY) || !(p == p) || !(mp <= 1.0f) || !(u >= 0.0f && u < 1.0f);
   if (bad || top == 0) {
@@ -1073,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     u64 mass;
     if (s.rank == 0 && s.draw_of_lists(k, by_p, p, least, u, &token, &l, &mass)) {
       a.tokens[b] = static_cast<int32_t>(token);
-      if (a.logprob) a.logprob[b] = log_share(s.scale, l, heat, mass);
+      if (a.logprob) a.logprob[b] = log_share(s.scale, l, heat, mass, 1ull << kFix);
     }
     return true;
   };
@@ -1088,17 +1121,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     int p1 = 64 * kBins;
     bool listed = !counted;
     if (counted && (by_k || by_p)) {
-#pragma unroll 1
-      for (int i = v0 + tid; i < v1; i += kThreads) {
-        float f[N];
-        s.row.get(i, f);
+      s.row.each(v0 + tid, v1, kThreads, [&](int, const float(&f)[N]) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
           if (f[e] >= floor_k) {
             const int at = s.place(f[e]);
             atomicAdd(&mem()->hist[at >> 6], by_k ? 1u : (1u << 20) + (at & 63));
           }
-      }
+      });
       // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
       s.find_bins(
           [&](int j) {
@@ -1145,7 +1175,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const float border_l = border ? of_key(static_cast<unsigned>(border >> 32)) : -FLT_MAX;
   const float from_l = by_p ? border_l : fmaxf(border_l, floor_l);
   // float32 first: where there is much to weigh (top-k leaves little), and no two criteria meet in one sum
-  bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || s.scale.top == INFINITY;
+  bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || !(fabsf(quick_top) < kQuickRange) ||
+               heat > kQuickHeat;
+
+  // min-p's bound in the float32 pass's weights
+  const Pair2 w_top = quick_weights(mem()->sixteenth, s.scale, two(s.scale.top));
+  const float mp_w = mp * (w_top.hi.x + w_top.lo.x);
 
   for (;; exact = true) {
     // The kept mass of each run.  With top-p, also the mass in all and above the border's bins; what lies in them
@@ -1167,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (exact) {
         s.weigh(two(l), &w0, &w1);
       } else {
-        const Pair2 w = quick_weights(s.scale, two(l));
+        const Pair2 w = quick_weights(mem()->sixteenth, s.scale, two(l));
         w0 = fixed_of(w.hi.x, w.lo.x);
       }
       return w0;
@@ -1186,15 +1221,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     };
     if (!exact) {
       Sum2 sum{}, sum_above{};
-      const float mp_lo = mp * (1.0f - 0x1p-21f), mp_hi = mp * (1.0f + 0x1p-21f);
-#pragma unroll 1
-      for (int i = u0 + lane; i < u1; i += 32) {
-        float f[N];
-        s.row.get(i, f);
+      // (weights as float32 numbers here: 2^-23 of each other)
+      const float mp_lo = mp_w * (1.0f - 0x1p-21f), mp_hi = mp_w * (1.0f + 0x1p-21f);
+      s.row.each(u0 + lane, u1, 32, [&](int i, const float(&f)[N]) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
           const float2 l = make_float2(f[e], f[e + 1]);
-          Pair2 w = quick_weights(s.scale, l);
+          Pair2 w = quick_weights(mem()->sixteenth, s.scale, l);
           if (by_p) {
             sum.add(w.hi, w.lo);
             const bool a0 = l.x > above_l, a1 = l.y > above_l;
@@ -1209,16 +1242,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             }
           } else {
             if (mp > 0.0f) {
-              if ((w.hi.x > mp_lo && w.hi.x < mp_hi && w.hi.x != 1.0f) ||
-                  (w.hi.y > mp_lo && w.hi.y < mp_hi && w.hi.y != 1.0f))
+              const float2 h = __fadd2_rn(w.hi, w.lo);
+              if ((h.x > mp_lo && h.x < mp_hi && l.x != s.scale.top) || (h.y > mp_lo && h.y < mp_hi && l.y != s.scale.top))
                 mem()->doubt = 1;
-              if (w.hi.x < mp) w.hi.x = w.lo.x = 0.0f;
-              if (w.hi.y < mp) w.hi.y = w.lo.y = 0.0f;
+              if (h.x < mp_w) w.hi.x = w.lo.x = 0.0f;
+              if (h.y < mp_w) w.hi.y = w.lo.y = 0.0f;
             }
             sum.add(w.hi, w.lo);
           }
         }
-      }
+      });
       if (by_p) {
         all = sum.fixed();
         above += sum_above.fixed();
@@ -1362,13 +1395,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (exact) {
             s.weigh(f, &w[0], &w[1]);
           } else {
-            const Pair2 q = quick_weights(s.scale, f);
-            w[0] = q.hi.x >= mp ? fixed_of(q.hi.x, q.lo.x) : 0;
-            w[1] = q.hi.y >= mp ? fixed_of(q.hi.y, q.lo.y) : 0;
+            const Pair2 q = quick_weights(mem()->sixteenth, s.scale, f);
+            w[0] = q.hi.x + q.lo.x >= mp_w ? fixed_of(q.hi.x, q.lo.x) : 0;
+            w[1] = q.hi.y + q.lo.y >= mp_w ? fixed_of(q.hi.y, q.lo.y) : 0;
           }
           const unsigned i = 2 * j - s.row.shift;
-          if (f.x == -INFINITY || rank_of(key_of(f.x), i) < border || w[0] < least) w[0] = 0;
-          if (f.y == -INFINITY || rank_of(key_of(f.y), i + 1) < border || w[1] < least) w[1] = 0;
+          if (f.x == -INFINITY || rank_of(key_of(f.x), i) < border || (exact && w[0] < least)) w[0] = 0;
+          if (f.y == -INFINITY || rank_of(key_of(f.y), i + 1) < border || (exact && w[1] < least)) w[1] = 0;
         }
         u64 incl = warp_scan64(w[0] + w[1], lane);
         __syncthreads();
@@ -1398,7 +1431,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (token >= 0) {
       a.tokens[b] = token;
-      if (a.logprob) a.logprob[b] = log_share(s.scale, token_l, heat, total);
+      if (a.logprob)
+        a.logprob[b] = log_share(s.scale, token_l, heat, total, exact ? 1ull << kFix : fixed_of(w_top.hi.x, w_top.lo.x));
     }
     return;
   }
@@ -1430,12 +1464,15 @@ template <typename T>
 cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
   constexpr int N = Elem<T>::N;
   const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
-  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (61 rows of 50257: 21 us with four,
-  // 25 with eight); a batch that takes several waves has rows cut less, because a CTA spends some 20 us beside its
-  // elements (256 rows of 128000 float32: 225 us with four, 267 with eight, 303 with one).
+  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (nucleus of 64 rows of 128000 bf16: 60
+  // us with four, 82 with eight), or of one per SM where slices then are short, because two on one SM cost each other
+  // more than half a short slice is worth (64 rows of 32000: 28.3 us with two, 29.3 with four; 32 rows of 151936: 39.7
+  // with eight, 45.7 with four).  Long rows are cut in two at least (256 rows of 128000 float32: 194 us, 244 with one, 210
+  // with four; 256 rows of 50257: 91.7, 91.2 with one), and very long ones in four, so that a bin's count holds.
   int ranks = 8;
   while (ranks > 1 && a.batch * ranks > 2 * kSms) ranks /= 2;
-  const int least = a.vocab > 96 * 1024 ? 4 : a.vocab > 48 * 1024 ? 2 : 1;
+  if (ranks > 1 && a.batch * ranks > kSms && 2 * (a.vocab / ranks) <= 32 * 1024) ranks /= 2;
+  const int least = a.vocab > 256 * 1024 ? 4 : a.vocab > 64 * 1024 ? 2 : 1;
   if (ranks < least) ranks = least;
   const int64_t slice = (vectors + ranks - 1) / ranks * 16;
   if (slice <= kStageBytes) return launch<T, true>(a, ranks, sizeof(Shared) + static_cast<size_t>(slice), stream);

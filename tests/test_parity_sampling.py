@@ -264,3 +264,20 @@ def test_repeats_graph_and_streams(gbf):
     gbf.sample_tokens(l, u, outs[0], top_p=p)
     torch.cuda.synchronize()
     assert torch.equal(outs[3], outs[0])
+
+
+def test_min_p_of_one_keeps_the_largest_alone(gbf):
+    """Logits one float32 step below the largest, hot enough that their weights round to the same float32 number."""
+    rng = np.random.default_rng(12)
+    batch, vocab = 4, 70000
+    top = np.float32(10.0)
+    l = np.full((batch, vocab), np.nextafter(top, np.float32(0)), np.float32)
+    u = np.array([0.0, 0.25, 0.6, 1 - 2.0 ** -24], np.float32)
+    tops = [np.sort(rng.choice(vocab, 1000, replace=False)) for _ in range(batch)]
+    for b in range(batch):
+        l[b, tops[b]] = top
+    tokens, lps = run(gbf, l, u, True, temperature=np.full(batch, 100.0), min_p=np.ones(batch))
+    want = [tops[b][int(np.float64(u[b]) * 1000)] for b in range(batch)]
+    assert tokens.tolist() == want
+    # log(1 / 1000): a float32 logarithm (2 ulp) of a sum that is right to 2^-23
+    assert np.all(np.abs(lps + np.log(1000.0)) <= 3 * 2.0 ** -23 * np.log(1000.0))
