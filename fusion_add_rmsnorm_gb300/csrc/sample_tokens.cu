@@ -59,6 +59,7 @@
 
 #include "common.cuh"
 #include "decode.h"
+#include "tma.cuh"
 
 namespace gbf {
 namespace {
@@ -83,7 +84,6 @@ constexpr int kNear = 2048;                 // this rank's elements in the bins 
 constexpr int kFilterVectors = 512;         // slices of more 16-byte vectors are first done in float32
 constexpr int kSpans = 32;                  // parts that the bins that may hold top-p's border are cut into
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
-constexpr int kQuickFix = 42;               // 2^42: the unit of the float32 pass's sums
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
 constexpr float kLeastTemperature = 1e-30f;
 constexpr int kSms = 152;
@@ -107,7 +107,7 @@ __device__ const u64 kPow[64] = {
 struct __align__(16) Shared {
   unsigned hist[kBins];
   u64 pow[64];
-  float2 sixteenth[16];        // 2^(j / 16) in two parts
+  float2 sixteenth[16];        // 2^(j / 16) in float32, and the rest of it relative to that
   u64 list[kList];             // candidates of every rank, as (key, ~index)
   union {
     struct {
@@ -150,7 +150,7 @@ struct RowScale {
   float c_place;           // places (64ths of a bin) per unit of logit, and about its inverse
   float c_inverse;
   float cut;               // 60 octaves below the top
-  int n_top;               // see quick_weights
+  unsigned n_top;          // exponent field of 2^N, see quick_weight
 };
 
 GBF_DEVICE float2 two(float x) { return make_float2(x, x); }
@@ -158,10 +158,10 @@ GBF_DEVICE float2 two(float x) { return make_float2(x, x); }
 GBF_DEVICE float2 sub2(float2 b, float2 a) { return __ffma2_rn(a, two(-1.0f), b); }
 
 // From the table index ji, and the fraction's parts in the mantissas of qa and qb: the weight.
-constexpr float kUa = 12582912.0f / 536870912.0f, kUb = 12582912.0f / 274877906944.0f;   // 1.5 * 2^23 units
+constexpr float kWa = 12582912.0f / 536870912.0f, kWb = 12582912.0f / 274877906944.0f;   // 1.5 * 2^23 units
 GBF_DEVICE u64 assemble(const u64* pow, float nt, float q, float qa, float qb) {
   const int ji = __float_as_int(q) - 0x4b400000;
-  const int i = (__float_as_int(qa) - __float_as_int(kUa)) * 512 + (__float_as_int(qb) - __float_as_int(kUb));
+  const int i = (__float_as_int(qa) - __float_as_int(kWa)) * 512 + (__float_as_int(qb) - __float_as_int(kWb));
   const u64 p = pow[ji & 63];
   const long long part = static_cast<long long>(i) * static_cast<int>(p >> 13);
   const u64 w = p * 2 + static_cast<u64>(part >> 24);               // twice the weight, before the octave
@@ -196,79 +196,69 @@ GBF_DEVICE void weights(const u64* pow, const RowScale& s, float2 l, u64* w0, u6
   b = __ffma2_rn(__fmul2_rn(x, x), series, b);
   // a + b in units of 2^-38, read off the mantissas after adding 1.5 * 2^23 units (which holds up to 2^22 of
   // them): a (below 2^-7) to 2^-29, then the rest (below 0.97 * 2^-16) to 2^-38
-  const float2 qa = sub2(two(kUa), na);
-  const float2 rest = sub2(b, __fadd2_rn(na, __ffma2_rn(two(-kUa), one, qa)));
-  const float2 qb = __fadd2_rn(rest, two(kUb));
+  const float2 qa = sub2(two(kWa), na);
+  const float2 rest = sub2(b, __fadd2_rn(na, __ffma2_rn(two(-kWa), one, qa)));
+  const float2 qb = __fadd2_rn(rest, two(kWb));
   *w0 = assemble(pow, nt.x, q.x, qa.x, qb.x);
   *w1 = assemble(pow, nt.y, q.y, qa.y, qb.y);
 }
 
-// The float32 pass's weights: exp(l / T) of two logits over 2^N, in float32 hi + lo within 2^-32 (2^-33.7 seen over 10^7
-// logits), N as for the largest logit (scale.n_top), whose weight lies in [1/2, 1.02).  The argument l / T log2(e) =
-// m + x + xl with m a multiple of 1/16, which a rounding addition leaves in the low bits of q; |x| <= 2^-5, exactly;
-// 2^m from the table and an exponent, 2^(x + xl) - 1 = a + b: the linear term in two parts, the rest by a polynomial
-// (minimax, 2^-36).  Logits more than 60 octaves below the top are taken as those there: 2^-60 each is lost in any sum.
-// For rows with |top| / T log2(e) < 2^14 (xl's own rounding: 2^-34).
+// The float32 pass's weight: exp(l / T) over 2^N, in float32 hi + lo within 2^-32 (2^-33 seen over 10^7 logits), N as for
+// the largest logit (scale.n_top), whose weight lies in [1/2, 1.03).  The argument l / T log2(e) = m + x + xl with m a
+// multiple of 1/16, which a rounding addition leaves in the low bits of q; |x| <= 2^-5, exactly; 2^m from the table and an
+// exponent, 2^(x + xl) - 1 = y + yl by a polynomial (minimax, 2^-36).  Logits more than 60 octaves below the top, -inf and
+// NaN are taken as those there: 2^-60 each is lost in any sum.  For rows with |top| / T log2(e) < 2^14 (xl's own rounding:
+// 2^-34).  Scalar instructions, whose constants and signs cost nothing: in pairs, half of what was issued were moves.
 constexpr float kMagic = 786432.0f;         // 1.5 * 2^19: a float of 1/16 ulp
 constexpr float kQuickRange = 16384.0f, kQuickHeat = 1e30f;
-struct Pair2 {
-  float2 hi, lo;
+struct Quick {
+  float w, lo;
 };
-GBF_DEVICE Pair2 quick_weights(const float2* sixteenth, const RowScale& s, float2 l) {
-  l = make_float2(fmaxf(l.x, s.cut), fmaxf(l.y, s.cut));
-  const float2 np = __fmul2_rn(l, two(-s.c_hi));                    // (negative parts where an instruction needs them)
-  const float2 q = sub2(two(kMagic), np);
-  const float2 nx = __fadd2_rn(__fadd2_rn(q, two(-kMagic)), np);    // exact
-  float2 xl = __ffma2_rn(l, two(s.c_hi), np);                       // what the product lacks
-  xl = __ffma2_rn(l, two(s.c_lo), xl);
-  const float2 x = sub2(xl, nx);
-  xl = sub2(xl, __fadd2_rn(x, nx));
-  constexpr float kL = 0.693147180559945309f;
-  constexpr float kLl = static_cast<float>(0.693147180559945309417 - static_cast<double>(kL));
-  const float2 a = __fmul2_rn(x, two(kL)), na = __fmul2_rn(x, two(-kL));
-  float2 b = __ffma2_rn(x, two(kL), na);
-  b = __ffma2_rn(x, two(kLl), b);
-  b = __ffma2_rn(xl, two(kL), b);
-  float2 r = __ffma2_rn(x, two(0.00961828f), two(0.05550509f));
-  r = __ffma2_rn(x, r, two(0.2402265f));
-  b = __ffma2_rn(__fmul2_rn(x, x), r, b);
-  const int q0 = __float_as_int(q.x), q1 = __float_as_int(q.y);
-  const float2 t0 = sixteenth[q0 & 15], t1 = sixteenth[q1 & 15];    // 2^(j / 16), hi and lo
-  const unsigned e0 = static_cast<unsigned>((q0 >> 4) - s.n_top) << 23, e1 = static_cast<unsigned>((q1 >> 4) - s.n_top) << 23;
-  const float2 hi = make_float2(__uint_as_float(__float_as_uint(t0.x) + e0), __uint_as_float(__float_as_uint(t1.x) + e1));
-  const float2 lo = make_float2(__uint_as_float(__float_as_uint(t0.y) + e0), __uint_as_float(__float_as_uint(t1.y) + e1));
-  const float2 nz = __fmul2_rn(hi, na);
-  float2 rest = __ffma2_rn(hi, a, nz);
-  rest = __ffma2_rn(hi, b, rest);
-  rest = __ffma2_rn(lo, a, rest);
-  rest = __fadd2_rn(rest, lo);
-  const float2 w = sub2(hi, nz);
-  return {w, sub2(rest, __fadd2_rn(nz, sub2(w, hi)))};
+GBF_DEVICE Quick quick_weight(unsigned table, const RowScale& s, float l) {
+  l = fmaxf(l, s.cut);
+  const float p = __fmul_rn(l, s.c_hi), q = __fadd_rn(p, kMagic);
+  const float x0 = __fsub_rn(p, __fsub_rn(q, kMagic));              // exact
+  float xl = __fmaf_rn(l, s.c_lo, __fmaf_rn(l, s.c_hi, -p));
+  const float x = __fadd_rn(x0, xl);
+  xl = __fsub_rn(xl, __fsub_rn(x, x0));
+  constexpr float kL = 0.693147180559945309f;                       // ln 2 to 2^-28, times x: 2^-33
+  const float r = __fmaf_rn(x, __fmaf_rn(x, 0.00961828f, 0.05550509f), 0.2402265f);
+  const float b = __fmaf_rn(__fmul_rn(x, x), r, __fmul_rn(xl, kL));
+  const float y = __fmaf_rn(x, kL, b);
+  float yl = __fadd_rn(__fmaf_rn(x, kL, -y), b);
+  float hi, rel;                                                    // 2^(j / 16), and what that lacks of itself
+  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(hi), "=f"(rel) : "r"(table + ((__float_as_uint(q) & 15u) << 3)));
+  hi = __uint_as_float(__float_as_uint(hi) + ((__float_as_uint(q) << 19) & 0xff800000u) - s.n_top);
+  yl = __fmaf_rn(rel, y, __fadd_rn(yl, rel));
+  const float w = __fmaf_rn(hi, y, hi);
+  return {w, __fmaf_rn(hi, yl, __fmaf_rn(hi, y, __fsub_rn(hi, w)))};
 }
 
-// A sum of weights that loses nothing: what each addition rounds off is added up beside it, with the weights' low
-// parts.
-struct Sum2 {
-  float2 s, c;
-  GBF_DEVICE void add(float2 w, float2 lo) {
-    const float2 t = __fadd2_rn(s, w), b = sub2(t, s);
-    c = __fadd2_rn(c, __fadd2_rn(__fadd2_rn(sub2(s, sub2(t, b)), sub2(w, b)), lo));
-    s = t;
+// Sums of such weights in integers: what 2 + w holds of w, in units of 2^-22, and the rest with lo to 2^-45.3, in units
+// of 2^-44 (at most 2^21.9 of them a weight, and 520 weights a thread: a slice has at most 2^18 elements).
+constexpr float kUa = 2.0f, kUb = 12582912.0f / 17592186044416.0f;  // 1.5 * 2^23 units
+struct Sum {
+  unsigned a;
+  int b;
+  GBF_DEVICE void add(const Sum& o) {
+    a += o.a;
+    b += o.b;
   }
-  GBF_DEVICE u64 fixed() const {
-    constexpr float k = static_cast<float>(1ull << kQuickFix);
-    return __float2ull_rn(s.x * k) + __float2ull_rn(s.y * k) +
-           static_cast<u64>(__float2ll_rn(c.x * k) + __float2ll_rn(c.y * k));
+  GBF_DEVICE u64 fixed() const {                                    // in units of 2^-kFix
+    static_assert(kFix == 43, "");
+    return (static_cast<u64>(a) << 21) + static_cast<u64>(static_cast<long long>(b >> 1));
   }
 };
-GBF_DEVICE u64 fixed_of(float hi, float lo) {
-  constexpr float k = static_cast<float>(1ull << kQuickFix);
-  return __float2ull_rn(hi * k) + static_cast<u64>(__float2ll_rn(lo * k));
+GBF_DEVICE Sum parts_of(const Quick& q) {
+  const float a = __fadd_rn(q.w, kUa);
+  const float b = __fadd_rn(__fadd_rn(__fsub_rn(q.w, __fsub_rn(a, kUa)), q.lo), kUb);
+  return {__float_as_uint(a) - __float_as_uint(kUa), __float_as_int(b) - __float_as_int(kUb)};
 }
-// What a float32 sum of masses and a share of another may be apart by: twice 2^-32 of them and as much again for the sums'
-// own roundings; and of the conversions to integers one unit for each thread's sums (twice 8 * 512) and each element near
-// the border (8 * kNear).
-GBF_DEVICE u64 slack_of(u64 total) { return (total >> 30) + 32768; }
+
+// What a float32 sum of masses and a share of another may be apart by: twice 2^-32 of them; the weights' last places
+// (0.4 units of 2^-43 each, twice); one unit for each thread's sums (twice 8 * 512) and each element near the border
+// (8 * kNear).
+GBF_DEVICE u64 slack_of(u64 total, int vocab) { return (total >> 31) + vocab + 32768; }
 
 // ln(w / total) = (l - top) / T - ln(total / the top's weight), both terms of one sign.
 GBF_DEVICE float log_share(const RowScale& s, float l, float heat, u64 total, u64 of_top) {
@@ -327,10 +317,11 @@ struct Row {
   const char* base;        // 16-byte aligned
   int shift, vocab;
   int v0;
+  int full0, full;         // the vectors that lie within the row: the first, and how many
 
   GBF_DEVICE uint4 load(int v) const {
     const int e0 = v * N - shift;
-    if (e0 >= 0 && e0 + N <= vocab) return ld_stream(base + static_cast<int64_t>(v) * 16);
+    if (static_cast<unsigned>(v - full0) < static_cast<unsigned>(full)) return ld_stream(base + static_cast<unsigned>(v) * 16u);
     unsigned w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -363,12 +354,12 @@ struct Row {
     return make_float2(f[0], f[1]);
   }
   GBF_DEVICE uint4 raw(int v) const { return STAGED ? stage()[v - v0] : load(v); }
-  static GBF_DEVICE void widen(uint4 v, float f[N]) {
-    Elem<T>::widen(v, f);
+  GBF_DEVICE void get(int v, float f[N]) const {
+    Elem<T>::widen(raw(v), f);
     if (!STAGED) tidy<N>(f);
   }
-  GBF_DEVICE void get(int v, float f[N]) const { widen(raw(v), f); }
-  // f(v, elements) for v = from, from + step, ... below end; each vector is loaded a turn ahead
+  // f(v, elements) for v = from, from + step, ... below end; each vector is loaded a turn ahead.  The elements as they
+  // are (NaN, -0).
   template <typename F>
   GBF_DEVICE void each(int from, int end, int step, F f) const {
     if (from >= end) return;
@@ -376,13 +367,10 @@ struct Row {
 #pragma unroll 1
     for (int v = from; v < end; v += step) {
       float x[N];
-      widen(next, x);
+      Elem<T>::widen(next, x);
       if (v + step < end) next = raw(v + step);
       f(v, x);
     }
-  }
-  GBF_DEVICE float2 pair_or_none(int j, int end) const {
-    return j < end ? pair(j) : make_float2(-INFINITY, -INFINITY);
   }
 };
 
@@ -954,9 +942,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (tid < 16) {
     const u64 p = kPow[4 * tid];
     const float hi = __ull2float_rn(p);
-    // (the low part of 1 is not 0, which has no exponent to add to)
-    const float lo = tid ? __ll2float_rn(static_cast<long long>(p - __float2ull_rn(hi))) : 0x1p-17f;
-    mem()->sixteenth[tid] = make_float2(hi * 0x1p-43f, lo * 0x1p-43f);
+    mem()->sixteenth[tid] =
+        make_float2(hi * 0x1p-43f, __ll2float_rn(static_cast<long long>(p - __float2ull_rn(hi))) / hi);
   }
   s.clear();
   pdl_wait();
@@ -969,6 +956,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.row.shift = off / static_cast<int>(sizeof(T));
   s.row.vocab = a.vocab;
   const int vectors = (s.row.shift + a.vocab + N - 1) / N;
+  s.row.full0 = s.row.shift ? 1 : 0;
+  s.row.full = max((s.row.shift + a.vocab) / N - s.row.full0, 0);
   const int per = (vectors + s.ranks - 1) / s.ranks;
   const int v0 = s.v0 = s.row.v0 = min(static_cast<int>(s.rank) * per, vectors);
   const int v1 = s.v1 = min(v0 + per, vectors);
@@ -1043,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.scale.top = of_key(top);
   const float quick_top = __fmul_rn(s.scale.top, s.scale.c_hi);
   s.scale.cut = s.scale.top - 41.5f * heat;
-  s.scale.n_top = (__float_as_int(__fadd_rn(quick_top, kMagic)) >> 4) + 1;
+  s.scale.n_top = ((__float_as_uint(__fadd_rn(quick_top, kMagic)) << 19) & 0xff800000u) + 0x800000u;
 
   const bool bad = !(temp >= 0.0f && temp < INFINITY) || !(p == p) || !(mp <= 1.0f) || !(u >= 0.0f && u < 1.0f);
   if (bad || top == 0) {
@@ -1110,6 +1099,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     return true;
   };
+  // (shared addresses that stay in registers: the compiler would derive them again at each use)
+  unsigned hist_at, sixteenth;
+  asm volatile("mov.u32 %0, %1;" : "=r"(hist_at) : "r"(smem_u32(mem()->hist)));
+  asm volatile("mov.u32 %0, %1;" : "=r"(sixteenth) : "r"(smem_u32(mem()->sixteenth)));
   u64 border = 0;                                        // ranks below it are cut off
   int b0 = 0, b1 = kBins - 1;                            // bins the border of top-p lies in
   typename Sampler<T, STAGED>::Hit hit[2];
@@ -1121,14 +1114,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     int p1 = 64 * kBins;
     bool listed = !counted;
     if (counted && (by_k || by_p)) {
-      s.row.each(v0 + tid, v1, kThreads, [&](int, const float(&f)[N]) {
+      const unsigned one = by_k ? 1u : 1u << 20, offset = by_k ? 0u : 63u;
+      auto count = [&](float l, int at) {                  // (without a branch for each element)
+        asm volatile("{ .reg .pred p; setp.ge.f32 p, %0, %1; @p red.shared.add.u32 [%2], %3; }" ::"f"(l), "f"(floor_k),
+                     "r"(hist_at + ((static_cast<unsigned>(at) >> 6) << 2)), "r"(one + (at & offset))
+                     : "memory");
+      };
+      if (s.scale.top == INFINITY)
+        s.row.each(v0 + tid, v1, kThreads, [&](int, const float(&f)[N]) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (f[e] >= floor_k) {
-            const int at = s.place(f[e]);
-            atomicAdd(&mem()->hist[at >> 6], by_k ? 1u : (1u << 20) + (at & 63));
-          }
-      });
+          for (int e = 0; e < N; ++e) count(f[e], s.place(f[e]));
+        });
+      else
+        s.row.each(v0 + tid, v1, kThreads, [&](int, const float(&f)[N]) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) count(f[e], place_of(s.scale, f[e]));
+        });
       // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
       s.find_bins(
           [&](int j) {
@@ -1179,17 +1180,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                heat > kQuickHeat;
 
   // min-p's bound in the float32 pass's weights
-  const Pair2 w_top = quick_weights(mem()->sixteenth, s.scale, two(s.scale.top));
-  const float mp_w = mp * (w_top.hi.x + w_top.lo.x);
+  const Quick w_top = quick_weight(sixteenth, s.scale, s.scale.top);
+  const float mp_w = mp > 0.0f ? mp * w_top.w : 0.0f;
 
   for (;; exact = true) {
     // The kept mass of each run.  With top-p, also the mass in all and above the border's bins; what lies in them
     // goes to a list, and its mass to the span of bins.
     // (a logit above above_l lies in a bin before b0, one below below_l behind b1)
     float above_l = INFINITY, below_l = -FLT_MAX;
+    // (by two places, which are rounded by half of one and are as far from (top - l) c_place by 2^-4 at most)
     if (by_p && s.scale.top != INFINITY) {
-      if (b0 > 0) above_l = s.scale.top - 64 * (b0 - 1) * s.scale.c_inverse;
-      if (b1 < kBins - 1) below_l = fmaxf(s.scale.top - 64 * (b1 + 2) * s.scale.c_inverse, -FLT_MAX);
+      if (b0 > 0) above_l = __fadd_ru(s.scale.top, -(64 * b0 - 34) * s.scale.c_inverse);
+      if (b1 < kBins - 1) below_l = fmaxf(__fadd_rd(s.scale.top, -(64 * b1 + 33) * s.scale.c_inverse), -FLT_MAX);
     }
     const int p0 = 64 * b0, p1 = 64 * b1 + 63;           // the bins' places, in spans of 2^coarse
     const int coarse = max(0, 32 - __clz(p1 - p0) - 5);
@@ -1202,8 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (exact) {
         s.weigh(two(l), &w0, &w1);
       } else {
-        const Pair2 w = quick_weights(mem()->sixteenth, s.scale, two(l));
-        w0 = fixed_of(w.hi.x, w.lo.x);
+        w0 = parts_of(quick_weight(sixteenth, s.scale, l)).fixed();
       }
       return w0;
     };
@@ -1220,43 +1221,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       return true;
     };
     if (!exact) {
-      Sum2 sum{}, sum_above{};
-      // (weights as float32 numbers here: 2^-23 of each other)
-      const float mp_lo = mp_w * (1.0f - 0x1p-21f), mp_hi = mp_w * (1.0f + 0x1p-21f);
-      s.row.each(u0 + lane, u1, 32, [&](int i, const float(&f)[N]) {
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 l = make_float2(f[e], f[e + 1]);
-          Pair2 w = quick_weights(mem()->sixteenth, s.scale, l);
-          if (by_p) {
-            sum.add(w.hi, w.lo);
-            const bool a0 = l.x > above_l, a1 = l.y > above_l;
-            sum_above.add(make_float2(a0 ? w.hi.x : 0.0f, a1 ? w.hi.y : 0.0f),
-                          make_float2(a0 ? w.lo.x : 0.0f, a1 ? w.lo.y : 0.0f));
-            const bool n0 = !a0 && l.x >= below_l, n1 = !a1 && l.y >= below_l;
-            if (n0 || n1) {
-              const unsigned at = static_cast<unsigned>(i * N + e - s.row.shift);
-              const u64 w0 = fixed_of(w.hi.x, w.lo.x), w1 = fixed_of(w.hi.y, w.lo.y);
-              if (n0 && !near(l.x, at, w0)) above += w0;
-              if (n1 && !near(l.y, at + 1, w1)) above += w1;
-            }
-          } else {
-            if (mp > 0.0f) {
-              const float2 h = __fadd2_rn(w.hi, w.lo);
-              if ((h.x > mp_lo && h.x < mp_hi && l.x != s.scale.top) || (h.y > mp_lo && h.y < mp_hi && l.y != s.scale.top))
-                mem()->doubt = 1;
-              if (h.x < mp_w) w.hi.x = w.lo.x = 0.0f;
-              if (h.y < mp_w) w.hi.y = w.lo.y = 0.0f;
-            }
-            sum.add(w.hi, w.lo);
-          }
-        }
-      });
+      Sum sum{};
       if (by_p) {
+        Sum sum_above{};
+        s.row.each(u0 + lane, u1, 32, [&](int i, const float(&f)[N]) {
+          bool any = false;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const Sum w = parts_of(quick_weight(sixteenth, s.scale, f[e]));
+            sum.add(w);
+            asm("{ .reg .pred p; setp.gt.f32 p, %2, %3; @p add.u32 %0, %0, %4; @p add.s32 %1, %1, %5; }"
+                : "+r"(sum_above.a), "+r"(sum_above.b) : "f"(f[e]), "f"(above_l), "r"(w.a), "r"(w.b));
+            any = any | (f[e] <= above_l & f[e] >= below_l);
+          }
+          if (any)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const float l = f[e] + 0.0f;                 // (-0 as 0)
+              if (l > above_l || !(l >= below_l)) continue;
+              const u64 w = weight_of(l);
+              if (!near(l, static_cast<unsigned>(i * N + e - s.row.shift), w)) above += w;
+            }
+        });
         all = sum.fixed();
-        above += sum_above.fixed();
-        kept = above;
+        kept = above += sum_above.fixed();
+      } else if (mp > 0.0f) {
+        // (weights as float32 numbers: 2^-23 of each other)
+        const float mp_lo = mp_w * (1.0f - 0x1p-21f), mp_hi = mp_w * (1.0f + 0x1p-21f);
+        s.row.each(u0 + lane, u1, 32, [&](int, const float(&f)[N]) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const Quick w = quick_weight(sixteenth, s.scale, f[e]);
+            if (w.w > mp_lo && w.w < mp_hi && f[e] != s.scale.top) mem()->doubt = 1;
+            if (!(w.w < mp_w)) sum.add(parts_of(w));
+          }
+        });
+        kept = sum.fixed();
       } else {
+        s.row.each(u0 + lane, u1, 32, [&](int, const float(&f)[N]) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) sum.add(parts_of(quick_weight(sixteenth, s.scale, f[e])));
+        });
         kept = sum.fixed();
       }
     } else {
@@ -1326,7 +1331,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         many = !s.close_lists();
       }
       if (!many) {
-        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target), weight_of);
+        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target, a.vocab), weight_of);
         if (!exact && !found.sure) continue;
         border = found.rank;
       } else {
@@ -1384,7 +1389,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int of_run = __ffs(__ballot_sync(0xffffffffu, before + incl_runs > target)) - 1;
       before += __shfl_sync(0xffffffffu, incl_runs - mine, of_run);
       const int r0 = s.j0 + of_run * run, r1 = min(r0 + run, s.j1);
-      const u64 slack = exact ? 0 : slack_of(total);
+      const u64 slack = exact ? 0 : slack_of(total, a.vocab);
 #pragma unroll 1
       for (int i0 = r0; i0 < r1; i0 += kThreads) {       // the whole CTA walks that run
         const int j = i0 + tid;
@@ -1395,9 +1400,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (exact) {
             s.weigh(f, &w[0], &w[1]);
           } else {
-            const Pair2 q = quick_weights(mem()->sixteenth, s.scale, f);
-            w[0] = q.hi.x + q.lo.x >= mp_w ? fixed_of(q.hi.x, q.lo.x) : 0;
-            w[1] = q.hi.y + q.lo.y >= mp_w ? fixed_of(q.hi.y, q.lo.y) : 0;
+            const Quick q0 = quick_weight(sixteenth, s.scale, f.x), q1 = quick_weight(sixteenth, s.scale, f.y);
+            w[0] = q0.w < mp_w ? 0 : parts_of(q0).fixed();
+            w[1] = q1.w < mp_w ? 0 : parts_of(q1).fixed();
           }
           const unsigned i = 2 * j - s.row.shift;
           if (f.x == -INFINITY || rank_of(key_of(f.x), i) < border || (exact && w[0] < least)) w[0] = 0;
@@ -1432,7 +1437,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (token >= 0) {
       a.tokens[b] = token;
       if (a.logprob)
-        a.logprob[b] = log_share(s.scale, token_l, heat, total, exact ? 1ull << kFix : fixed_of(w_top.hi.x, w_top.lo.x));
+        a.logprob[b] = log_share(s.scale, token_l, heat, total, exact ? 1ull << kFix : parts_of(w_top).fixed());
     }
     return;
   }
