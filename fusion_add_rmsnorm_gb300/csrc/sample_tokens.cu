@@ -45,11 +45,20 @@
 // groups it leaves about n ln n elements, in whatever order the logits come.
 //
 // The exact weight is the dear part (some 45 integer instructions, which run at
-// half rate), so a long slice is first done in float32 with an error bound: the
-// weight to 2^-32 in pairs of float32, compensated sums, and every decision
-// checked against twice that bound.  A row in which all decisions clear it is
-// done; the others (one in some thousands with nuclei of 10^5 tokens) are done
-// again exactly.
+// half rate), so a row is first done in float32 with an error bound: the weight
+// to 2^-32 in two float32 parts, summed as integers, and every decision checked
+// against twice that bound.  A row in which all decisions clear it is done; the
+// others (one in some thousands with nuclei of 10^5 tokens) are done again
+// exactly.
+//
+// What bounds it: instructions and barriers, not HBM.  A nucleus row issues about
+// 100 instructions per 32 elements (8 for pass 1, 12 for the histogram, 60 for the
+// weights) at 2.5 a cycle and SM, and a cluster passes some seven barriers with
+// an exchange behind each, 1 to 2 us apiece.  Measured (device time, back to
+// back): one row of 32000 bf16, nucleus, 18.9 us (temperature alone 8.4);
+// 32 rows of 151936, mixed requests, 37.9 us (10 MB: 0.26 TB/s); 61 rows of 50257,
+// temperature alone, 14.7 us; 256 rows of 128000 float32, nucleus, 181 us (131 MB:
+// 0.72 TB/s).
 //
 // Ranks hand each other totals by remote stores into boxes (read locally behind
 // the next barrier).
@@ -81,7 +90,6 @@ constexpr int kList = 1024;                 // candidates that are sorted, an eq
 constexpr int kGroup = 64;                  // bins per group (and groups): the two steps of a search over the bins
 constexpr int kFew = 128;                   // up to this many are compared with each other
 constexpr int kNear = 2048;                 // this rank's elements in the bins that may hold top-p's border
-constexpr int kFilterVectors = 512;         // slices of more 16-byte vectors are first done in float32
 constexpr int kSpans = 32;                  // parts that the bins that may hold top-p's border are cut into
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
@@ -1175,8 +1183,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const u64 k_border = border;
   const float border_l = border ? of_key(static_cast<unsigned>(border >> 32)) : -FLT_MAX;
   const float from_l = by_p ? border_l : fmaxf(border_l, floor_l);
-  // float32 first: where there is much to weigh (top-k leaves little), and no two criteria meet in one sum
-  bool exact = per <= kFilterVectors || by_k || (by_p && mp > 0.0f) || !(fabsf(quick_top) < kQuickRange) ||
+  // float32 first, unless two criteria meet in one sum or top-k leaves little (even on the shortest slices: one row of
+  // 1000 bf16 8.0 us, 8.6 exactly; 256 rows of 4000 21.8 and 22.6)
+  bool exact = by_k || (by_p && mp > 0.0f) || !(fabsf(quick_top) < kQuickRange) ||
                heat > kQuickHeat;
 
   // min-p's bound in the float32 pass's weights
@@ -1469,11 +1478,12 @@ template <typename T>
 cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
   constexpr int N = Elem<T>::N;
   const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
-  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (nucleus of 64 rows of 128000 bf16: 60
-  // us with four, 82 with eight), or of one per SM where slices then are short, because two on one SM cost each other
-  // more than half a short slice is worth (64 rows of 32000: 28.3 us with two, 29.3 with four; 32 rows of 151936: 39.7
-  // with eight, 45.7 with four).  Long rows are cut in two at least (256 rows of 128000 float32: 194 us, 244 with one, 210
-  // with four; 256 rows of 50257: 91.7, 91.2 with one), and very long ones in four, so that a bin's count holds.
+  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (nucleus of 64 rows of 128000 bf16: 55
+  // us with four, 77 with eight), or of one per SM where slices then are short, because two on one SM cost each other
+  // more than half a short slice is worth (64 rows of 32000, temperature alone: 11.8 us with two, 12.7 with four; 32 rows
+  // of 151936: 23.7 with eight, 33.2 with four).  Long rows are cut in two at least (nucleus of 256 rows of 128000 bf16:
+  // 163 us, 198 with one, 185 with four; 256 rows of 50257: 85.7, 85.0 with one), and very long ones in four, so that a
+  // bin's count and a thread's sums hold.
   int ranks = 8;
   while (ranks > 1 && a.batch * ranks > 2 * kSms) ranks /= 2;
   if (ranks > 1 && a.batch * ranks > kSms && 2 * (a.vocab / ranks) <= 32 * 1024) ranks /= 2;
