@@ -125,6 +125,12 @@ GBF_DEVICE Request request_of(const PagedAttnArgs& a, int b) {
   return r;
 }
 
+// a / b of values >= 0, b > 0, as a 32-bit division where they fit
+GBF_DEVICE int64_t quotient(int64_t a, int64_t b) {
+  if ((a | b) >> 31) return a / b;
+  return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // Where unit c * share lies: request, and units into that request.
 struct Place {
   int64_t units;          // of the whole batch
@@ -168,7 +174,7 @@ GBF_DEVICE Place locate(const PagedAttnArgs& a, int64_t c, bool report) {
     units += warp_sum[w];
   }
   base += incl - mine;
-  int64_t share = (units + a.ctas - 1) / a.ctas;
+  int64_t share = quotient(units + a.ctas - 1, a.ctas);
   if (share < a.min_units) share = a.min_units;
   const int64_t u = c * share;
   if (u >= base && u < base + mine) {       // exactly one thread, unless u is past the end
@@ -210,7 +216,7 @@ struct Cursor {
     b = p.b;
     r = request_of(a, b);
     const int64_t n = r.tiles + kOwn;
-    item = static_cast<int>(p.rest / n);
+    item = static_cast<int>(quotient(p.rest, n));
     left = units;
     turn = solo_turn = 0;
     most_solo = p.share * a.batch * a.hkv * a.chunks >= 2 * p.units ? kSoloTwo : kSoloOne;
@@ -327,36 +333,40 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
   work = load;
   load.settle(a, warp);
 
-  // Block-table entry of lane's token (lanes 0..15) of the load cursor's tile,
-  // requested one tile before its rows are.
-  int entry = -1, offset = 0;
-  bool inside = false;
+  // Block-table entry of lane's token (lanes 0..15) of the load cursor's tile, requested one tile before its rows are,
+  // and the cursor's step to the next tile.
+  struct Fetch {
+    int entry, offset, head;
+    bool inside, on;
+  };
   auto fetch_entry = [&]() {
-    inside = false;
-    if (load.done) return;
+    Fetch f{-1, 0, 0, false, !load.done};
+    if (load.done) return f;
+    f.head = load.item / a.chunks;
     const int tok = load.r.lo + load.t * kTile + (lane & 15);
     if (tok < load.r.len) {
       int blk;
       if (a.block_shift >= 0) {
         blk = tok >> a.block_shift;
-        offset = tok & (a.block_size - 1);
+        f.offset = tok & (a.block_size - 1);
       } else {
         blk = tok / a.block_size;
-        offset = tok - blk * a.block_size;
+        f.offset = tok - blk * a.block_size;
       }
-      inside = true;
-      entry = a.table[static_cast<int64_t>(load.b) * a.table_stride + blk];
+      f.inside = true;
+      f.entry = a.table[static_cast<int64_t>(load.b) * a.table_stride + blk];
     }
+    load.advance(a, warp);
+    return f;
   };
-  auto issue = [&](int stage) {
-    if (!load.done) {
-      const bool ok = inside && entry >= 0 && entry < a.num_blocks;
-      if (inside && !ok) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
-      const uint32_t row = ok ? static_cast<uint32_t>(entry * a.block_size + offset) : 0u;
+  auto issue = [&](int stage, const Fetch& f) {
+    if (f.on) {
+      const bool ok = f.inside && f.entry >= 0 && f.entry < a.num_blocks;
+      if (f.inside && !ok) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
+      const uint32_t row = ok ? static_cast<uint32_t>(f.entry * a.block_size + f.offset) : 0u;
       const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       if (lane == 0) sm_valid[warp][stage] = valid;
-      const int head = load.item / a.chunks;
-      const int64_t col = static_cast<int64_t>(head) * a.d * 2 + chunk_col * 16;
+      const int64_t col = static_cast<int64_t>(f.head) * a.d * 2 + chunk_col * 16;
       const char* kp = static_cast<const char*>(a.k) + col;
       const char* vp = static_cast<const char*>(a.v) + col;
       const uint32_t dst = stages_u + stage * stage_bytes<DP>() + chunk_row * (DP * 2);
@@ -371,16 +381,18 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
           cp_async16(at + kTile * DP * 2, vp + off, n);
         }
       }
-      load.advance(a, warp);
     }
     cp_async_commit();
   };
 
-  fetch_entry();
+  Fetch next;
+  {
+    Fetch first[NS - 1];                         // their entries are on their way together
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s) {
-    issue(s);
-    fetch_entry();
+    for (int s = 0; s < NS - 1; ++s) first[s] = fetch_entry();
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) issue(s, first[s]);
+    next = fetch_entry();
   }
 
   // ldmatrix rows of this lane: K (tokens 0..7 | 0..7 | 8..15 | 8..15, columns 0 | 8 | 0 | 8 of the k step),
@@ -434,8 +446,8 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
       __syncwarp();
       const uint32_t valid = sm_valid[warp][stage];
       const uint32_t base = stage * stage_bytes<DP>();
-      issue(stage == 0 ? NS - 1 : stage - 1);    // into the stage the previous tile has left
-      fetch_entry();
+      issue(stage == 0 ? NS - 1 : stage - 1, next);    // into the stage the previous tile has left
+      next = fetch_entry();
 
       float s[2][4];
 #pragma unroll
@@ -627,10 +639,10 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAt
   int item = 0, c0 = 0, c1 = 0;
   if (on) {
     const Request r = request_of(a, p.b);
-    item = static_cast<int>(p.rest / (r.tiles + kOwn));
+    item = static_cast<int>(quotient(p.rest, r.tiles + kOwn));
     const int64_t u = p.rest - static_cast<int64_t>(item) * (r.tiles + kOwn), begin = c * p.share - u;
-    c0 = static_cast<int>((begin + kOwn) / p.share);        // CTAs of the item's first and last tile
-    c1 = static_cast<int>((begin + kOwn + r.tiles - 1) / p.share);
+    c0 = static_cast<int>(quotient(begin + kOwn, p.share));        // CTAs of the item's first and last tile
+    c1 = static_cast<int>(quotient(begin + kOwn + r.tiles - 1, p.share));
     on = u > kOwn && c == c0 + 1;
   }
   const int head = item / a.chunks, row0 = (item - head * a.chunks) * 16, row = blockIdx.y;
