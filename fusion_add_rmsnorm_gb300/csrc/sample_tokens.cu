@@ -63,6 +63,7 @@
 // Ranks hand each other totals by remote stores into boxes (read locally behind
 // the next barrier).
 #include <cfloat>
+#include <mutex>
 
 #include <cooperative_groups.h>
 
@@ -94,7 +95,6 @@ constexpr int kSpans = 32;                  // parts that the bins that may hold
 constexpr int kFix = 43;                    // 2^43: the weight of the largest logit
 constexpr int kStageBytes = 66 * 1024;      // largest slice kept in shared memory
 constexpr float kLeastTemperature = 1e-30f;
-constexpr int kSms = 152;
 
 // 2^43 * 2^(j / 64)
 __device__ const u64 kPow[64] = {
@@ -1452,46 +1452,95 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 }
 
+// Dynamic shared memory of a CTA that is to have an SM for itself.
+constexpr int kAloneBytes = 120 * 1024;
+static_assert(sizeof(Shared) + kStageBytes < kAloneBytes && 2 * kAloneBytes > 228 * 1024, "");
+
+// The launch of `batch` clusters of `ranks` CTAs.
 template <typename T, bool STAGED>
-cudaError_t launch(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<sample_kernel<T, STAGED>>(static_cast<int>(sizeof(Shared)) +
-                                                             (STAGED ? kStageBytes : 0));
-  if (e != cudaSuccess) return e;
+struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ranks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a);
+
+  Launch(int64_t batch, int ranks, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned>(batch * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+  static cudaError_t allow() { return allow_smem<sample_kernel<T, STAGED>>(kAloneBytes); }
+  cudaError_t go(const SampleArgs& a) { return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a); }
+};
+
+// How many clusters of 1, 2, 4 and 8 CTAs the device holds at once, with an SM for each CTA and with two CTAs on one
+// (the SMs of a GPC are not a multiple of 8: 15 and 36 clusters of eight here, not 19 and 38).  Asked once per device.
+struct Fits {
+  int alone[4], shared[4];
+};
+cudaError_t fits(Fits* out) {
+  static std::mutex lock;
+  static Fits known[64];
+  static uint64_t done = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> hold(lock);
+  Fits& f = known[dev & 63];
+  if (!(done >> (dev & 63) & 1)) {
+    typedef Launch<__nv_bfloat16, true> L;
+    e = L::allow();
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+      L one(1, 1 << i, kAloneBytes, nullptr), two(1, 1 << i, sizeof(Shared) + kStageBytes, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&f.alone[i], sample_kernel<__nv_bfloat16, true>, &one.cfg);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&f.shared[i], sample_kernel<__nv_bfloat16, true>, &two.cfg);
+    }
+    if (e != cudaSuccess) return e;
+    done |= 1ull << (dev & 63);
+  }
+  *out = f;
+  return cudaSuccess;
+}
+
+template <typename T, bool STAGED>
+cudaError_t launch(const SampleArgs& a, int ranks, bool alone, size_t smem, cudaStream_t stream) {
+  const cudaError_t e = Launch<T, STAGED>::allow();
+  if (e != cudaSuccess) return e;
+  return Launch<T, STAGED>(a.batch, ranks, alone ? kAloneBytes : smem, stream).go(a);
 }
 
 template <typename T>
 cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
   constexpr int N = Elem<T>::N;
   const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
-  // CTAs per row: as many as leave the whole batch in one wave of two CTAs per SM (nucleus of 64 rows of 128000 bf16: 55
-  // us with four, 77 with eight), or of one per SM where slices then are short, because two on one SM cost each other
-  // more than half a short slice is worth (64 rows of 32000, temperature alone: 11.8 us with two, 12.7 with four; 32 rows
-  // of 151936: 23.7 with eight, 33.2 with four).  Long rows are cut in two at least (nucleus of 256 rows of 128000 bf16:
-  // 163 us, 198 with one, 185 with four; 256 rows of 50257: 85.7, 85.0 with one), and very long ones in four, so that a
-  // bin's count and a thread's sums hold.
-  int ranks = 8;
-  while (ranks > 1 && a.batch * ranks > 2 * kSms) ranks /= 2;
-  if (ranks > 1 && a.batch * ranks > kSms && 2 * (a.vocab / ranks) <= 32 * 1024) ranks /= 2;
-  const int least = a.vocab > 256 * 1024 ? 4 : a.vocab > 64 * 1024 ? 2 : 1;
-  if (ranks < least) ranks = least;
-  const int64_t slice = (vectors + ranks - 1) / ranks * 16;
-  if (slice <= kStageBytes) return launch<T, true>(a, ranks, sizeof(Shared) + static_cast<size_t>(slice), stream);
-  return launch<T, false>(a, ranks, sizeof(Shared), stream);
+  auto slice = [&](int ranks) { return (vectors + ranks - 1) / ranks * 16; };
+  Fits f;
+  const cudaError_t e = fits(&f);
+  if (e != cudaSuccess) return e;
+  // CTAs per row: as many as leave an SM to each CTA, because two on one SM cost each other more than half a slice is
+  // worth (64 rows of 32000, nucleus: 27 us with two, 28 with four; 16 rows: 21.6 with four, 23.5 with eight) ...
+  int i = 3;
+  while (i > 0 && a.batch > f.alone[i]) --i;
+  // ... and twice that, two on one SM, where a slice would not fit in shared memory (32 rows of 151936, nucleus: 51 us
+  // with eight, 60 with four; 200 rows of 50257: 73 with two, 82 with one; 256 of 32000, which fit: 62 with one, 69 with
+  // two)
+  if (i < 3 && slice(1 << i) > kStageBytes && (i == 0 || a.batch <= f.shared[i + 1])) ++i;
+  // very long rows: so that a bin's count and a thread's sums hold
+  if (a.vocab > 256 * 1024 && i < 2) i = 2;
+  // Where they fit, CTAs are kept from sharing an SM (by the shared memory they ask for): in a run of calls, the second
+  // call's would otherwise settle in pairs beside the first one's (61 rows of 50257: 14.9 us, or 21.8 in half of the
+  // processes; 152 rows of 30000: 16.5 and 24).
+  const bool alone = a.batch <= f.alone[i];
+  const int64_t bytes = slice(1 << i);
+  if (bytes <= kStageBytes) return launch<T, true>(a, 1 << i, alone, sizeof(Shared) + static_cast<size_t>(bytes), stream);
+  return launch<T, false>(a, 1 << i, alone, sizeof(Shared), stream);
 }
 
 }  // namespace
