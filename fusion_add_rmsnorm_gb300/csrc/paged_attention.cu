@@ -29,6 +29,12 @@
 // the tokens as columns; the score accumulators are then, element for
 // element, the A operand of the product with V.
 //
+// What bounds it: HBM, from the first tile's arrival to the last one's.  In front of that lie the reads that follow one
+// from another (lengths, table, rows: 3.5 us of the 36 to 50 us of a batch), behind it the join.  Device time, back to
+// back: 32 requests up to 4096, 32 heads on 8 of 128, 49 us (277 MB: 5.6 TB/s); 256 such requests 326 us (2.16 GB: 6.6
+// TB/s); two documents of 131072 on 8 KV heads 126 us (806 MB: 6.4 TB/s); 48 requests on one KV head of 256, window 4096,
+// 35.8 us (158 MB: 4.4 TB/s); one request of 700 tokens 7.4 us (two launches, and reads that wait for one another).
+//
 // Rounding: scores, maxima, sums and outputs are float32.  P enters the second
 // product as a pair of bf16 (value and remainder, 2^-17 together), because one
 // bf16 alone would add an error as large as the final bf16 rounding.  For
@@ -42,18 +48,26 @@ namespace {
 
 constexpr int kTile = 16;              // tokens per tile
 // An item is one warp's alone (joining the warps costs about as much as four tiles) when it has at most 4 tiles, 8
-// where a CTA has two items on average, and up to 16 as long as that is a 16th of the CTA's units.
+// where a CTA has two items on average, and up to 16 as long as that is a 16th of the CTA's units.  192 requests up to
+// 2048, 8 KV heads of 64: 80.1 us, 84.8 with 4 throughout; 48 on one KV head of 256, window 4096: 36.0, 45.7 with 16
+// throughout; 64 requests up to 1024, 12 KV heads of 64: 28.9, 33.3 with none.
 constexpr int kSoloOne = 4, kSoloTwo = 8, kSoloMost = 16;
-constexpr int kOwn = 4;                // units an item counts beside its tiles
+// Units an item counts beside its tiles, for its queries, its start and its join: 24 requests of 32 KV heads take 48.8 us
+// with 8 or 4, 60.8 with 0; window 4096 on one KV head 35.8 with 8, 37.2 with 4, 35.3 with 12, and 256 requests up to 512
+// 52.3, 51.8 and 54.3.
+constexpr int kOwn = 8;
 constexpr int kSms = 152;
 constexpr float kLn2 = 0.693147180559945f;
 
-// Layout per padded head width: warps per CTA, ring depth, CTAs per SM.
+// Layout per padded head width: warps per CTA, ring depth, CTAs per SM.  Two stages ahead of the one in use keep 130 to
+// 210 KB of an SM on their way, more than the bandwidth needs: at 64 three stages take 27.2 us on 64 requests of 12 heads
+// and six 29.0 (a longer start), three CTAs per SM 95 us where two take 79; at 128 one CTA with six stages 58 us where two
+// with three take 48.5, and two stages 48.8; at 256 two stages 57 us, three 54.5.
 template <int DP>
 struct Plan;
 template <>
 struct Plan<64> {
-  static constexpr int kWarps = 4, kStages = 6, kPerSm = 2;
+  static constexpr int kWarps = 4, kStages = 3, kPerSm = 2;
 };
 template <>
 struct Plan<128> {
