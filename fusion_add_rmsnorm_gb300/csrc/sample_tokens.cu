@@ -48,12 +48,12 @@
 // half rate), so a row is first done in float32 with an error bound: the weight
 // to 2^-32 in two float32 parts, summed as integers, and every decision checked
 // against twice that bound.  A row in which all decisions clear it is done; the
-// others (one in some thousands with nuclei of 10^5 tokens) are done again
-// exactly.
+// others (one in 500 of 128000 candidates with top_p up to 0.99, one in 4000 of
+// 50257 without) are done again exactly.
 //
-// What bounds it: instructions and barriers, not HBM.  A nucleus row issues about
-// 100 instructions per 32 elements (8 for pass 1, 12 for the histogram, 60 for the
-// weights) at 2.5 a cycle and SM, and a cluster passes some seven barriers with
+// What bounds it: instructions and barriers, not HBM.  A nucleus row issues 107
+// instructions per 32 elements (9 for pass 1, some 12 for the histogram, 55 for the
+// weights, the rest for the border and the draw) at 2.5 a cycle and SM, and a cluster passes some seven barriers with
 // an exchange behind each, 1 to 2 us apiece.  Measured (device time, back to
 // back): one row of 32000 bf16, nucleus, 18.9 us (temperature alone 8.4);
 // 32 rows of 151936, mixed requests, 37.9 us (10 MB: 0.26 TB/s); 61 rows of 50257,
@@ -242,7 +242,7 @@ GBF_DEVICE Quick quick_weight(unsigned table, const RowScale& s, float l) {
   return {w, __fmaf_rn(hi, yl, __fmaf_rn(hi, y, __fsub_rn(hi, w)))};
 }
 
-// Sums of such weights in integers: what 2 + w holds of w, in units of 2^-22, and the rest with lo to 2^-45.3, in units
+// Sums of such weights in integers: what 2 + w holds of w, in units of 2^-22, and the rest with lo to 2^-44.6, in units
 // of 2^-44 (at most 2^21.9 of them a weight, and 520 weights a thread: a slice has at most 2^18 elements).
 constexpr float kUa = 2.0f, kUb = 12582912.0f / 17592186044416.0f;  // 1.5 * 2^23 units
 struct Sum {
@@ -264,9 +264,11 @@ GBF_DEVICE Sum parts_of(const Quick& q) {
 }
 
 // What a float32 sum of masses and a share of another may be apart by: twice 2^-32 of them; the weights' last places
-// (0.4 units of 2^-43 each, twice); one unit for each thread's sums (twice 8 * 512) and each element near the border
-// (8 * kNear).
-GBF_DEVICE u64 slack_of(u64 total, int vocab) { return (total >> 31) + vocab + 32768; }
+// (2^-45 and a quarter of it each, which is 0.32 units of 2^-43, in both); one unit for each thread's two sums and each
+// element near the border.
+GBF_DEVICE u64 slack_of(u64 total, int vocab, unsigned ranks) {
+  return (total >> 31) + (vocab - (vocab >> 3)) + ranks * (2 * kThreads + kNear);
+}
 
 // ln(w / total) = (l - top) / T - ln(total / the top's weight), both terms of one sign.
 GBF_DEVICE float log_share(const RowScale& s, float l, float heat, u64 total, u64 of_top) {
@@ -1340,7 +1342,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         many = !s.close_lists();
       }
       if (!many) {
-        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target, a.vocab), weight_of);
+        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target, a.vocab, s.ranks), weight_of);
         if (!exact && !found.sure) continue;
         border = found.rank;
       } else {
@@ -1398,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int of_run = __ffs(__ballot_sync(0xffffffffu, before + incl_runs > target)) - 1;
       before += __shfl_sync(0xffffffffu, incl_runs - mine, of_run);
       const int r0 = s.j0 + of_run * run, r1 = min(r0 + run, s.j1);
-      const u64 slack = exact ? 0 : slack_of(total, a.vocab);
+      const u64 slack = exact ? 0 : slack_of(total, a.vocab, s.ranks);
 #pragma unroll 1
       for (int i0 = r0; i0 < r1; i0 += kThreads) {       // the whole CTA walks that run
         const int j = i0 + tid;

@@ -5,6 +5,10 @@ into the cache, attention over it with E4M3 codes out, the E4M3 Linear, logits,
 the next token, which feeds the next step), a request ends and another takes its
 place and its blocks.  Every operator is compared with the oracle on the inputs
 it was given, so that one operator's rounding is not another's error."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -170,3 +174,29 @@ def test_a_server_decodes(gbf):
     torch.cuda.synchronize()
     check_step(s, before)
     assert gbf.device_status()[0] == gbf.OK
+
+
+FIRST = """
+import torch, fusion_add_rmsnorm_gb300 as gbf
+z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")
+bf = torch.bfloat16
+lens, new, table, free = z(2), torch.ones(2, dtype=torch.int32, device="cuda"), z(2, 4), torch.arange(8, device="cuda").int()
+ring, seq, ring_out, slots, pos = torch.tensor([0, 8], device="cuda").int(), z(2), z(2), z(2), z(2)
+q, k, out, ws = z(2, 4, 64, t=bf) + 1, z(128, 2, 64, t=bf) + 1, z(2, 4, 64, t=bf), z(1 << 22, t=torch.uint8)
+logits, u, tokens = z(2, 1000, t=bf), z(2, t=torch.float32) + 0.5, z(2)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gbf.paged_slots(lens, new, table, free, ring, 16, seq, ring_out, slots, pos)
+    gbf.paged_attention(q, k, k, table, seq, 16, out, ws)
+    gbf.sample_tokens(logits, u, tokens)
+g.replay()
+torch.cuda.synchronize()
+assert slots.tolist() == [0, 16] and tokens.tolist() == [500, 500] and (out == 1).all() and gbf.device_status()[0] == gbf.OK
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """What a call sets up once per device is set up while a stream is being captured too."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
