@@ -527,15 +527,17 @@ struct Sampler {
   }
   // The bins in which the running sum over bins 0, 1, ... and all ranks reaches
   // two targets: by groups of 64 bins, then the bins of the groups they lie
-  // in.  value(j): this rank's of bin j.  Float32 sums: exact for counts (at
-  // most 2^20), and 2^-19 for masses that are known to 0.3 %.  Two barriers.
+  // in, read from every rank's histogram.  value(h, j): of bin j that holds h.
+  // Float32 sums: exact for counts (at most 2^20), and 2^-19 for masses that are
+  // known to 0.3 %.  One cluster barrier, and another has to pass before a rank
+  // writes to its histogram again or ends.
   template <typename Value, typename Targets>
   GBF_DEVICE void find_bins(Value value, Targets targets, Hit out[2]) {
     static_assert(kBins == 8 * kThreads && kGroup * kGroup == kBins && kThreads == 8 * kGroup, "");
     __syncthreads();                                     // this rank's histogram is complete
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += value(tid * 8 + i);
+    for (int i = 0; i < 8; ++i) sum += value(mem()->hist[tid * 8 + i], tid * 8 + i);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((tid & 7) < ranks) of(tid & 7)->search.group[rank][tid >> 3] = sum;
@@ -547,10 +549,10 @@ struct Sampler {
     for (int k = 0; k < 2; ++k) {
       out[k] = hit64(groups, t[k]);
       const unsigned r = tid >> 6;
-      if (out[k].at >= 0 && r < ranks)
-        of(r)->search.bin[k][rank][tid & 63] = value(out[k].at * kGroup + (tid & 63));
+      const int j = out[k].at * kGroup + (tid & 63);
+      if (out[k].at >= 0 && r < ranks) mem()->search.bin[k][r][tid & 63] = value(of(r)->hist[j], j);
     }
-    cluster.sync();
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (out[k].at >= 0) {
@@ -632,6 +634,19 @@ struct Sampler {
     }
     return n;
   }
+  // Those of the lists' candidates that keep(c) is true for, in any order (mine_n is 0 before); how many.
+  template <typename Keep>
+  GBF_DEVICE unsigned pack_some(u64* order, Keep keep) {
+    const unsigned share = kList / ranks;
+#pragma unroll
+    for (unsigned j = tid; j < kList; j += kThreads)
+      if (j % share < mem()->list_n[j / share]) {
+        const u64 c = mem()->list[j];
+        if (keep(c)) order[atomicAdd(&mem()->mine_n, 1u)] = c;
+      }
+    __syncthreads();
+    return mem()->mine_n;
+  }
   // Sorts n <= kList values, larger first: bitonic, a warp's 64 values in its lanes
   // as long as the steps stay within them.  Zeros go behind, up to a power of two.
   // They stand `from` values into the histogram's memory.
@@ -693,15 +708,14 @@ struct Sampler {
     __syncthreads();
   }
 
-  // Ranks the lists' candidates, the same in every rank, in the histogram's memory
+  // Ranks n candidates, the same in every rank, packed in the histogram's memory
   // (a few by comparison with each other, more by a bitonic sort, larger first):
   // the last of them before which less than `target` lies, `before` lying before
   // all.  value(l): what a candidate counts for.
   template <typename Value>
-  GBF_DEVICE Border border_of_lists(u64 before, u64 target, u64 slack, Value value) {
+  GBF_DEVICE Border border_of(unsigned n, u64 before, u64 target, u64 slack, Value value) {
     static_assert(2 * kList * sizeof(u64) <= sizeof(unsigned) * kBins && kFew <= kThreads, "");
     u64* order = reinterpret_cast<u64*>(mem()->hist);
-    const unsigned n = pack(order);
     u64 last = ~0ull;
     bool sure = false;
     auto decide = [&](u64 k, u64 at, u64 w) {
@@ -919,7 +933,7 @@ struct Sampler {
         while (((hi - lo) >> s) >= kCells) ++s;
       }
     }
-    return border_of_lists(before, target, 0, [&](float l) {
+    return border_of(pack(reinterpret_cast<u64*>(mem()->hist)), before, target, 0, [&](float l) {
              u64 w0 = 1, w1;
              if (by_mass) weigh(two(l), &w0, &w1);
              return w0;
@@ -1142,8 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         });
       // counts, or with top-p alone the bins' masses: middle weight times (count - ln 2 / 128 * sum of offsets)
       s.find_bins(
-          [&](int j) {
-            const unsigned h = mem()->hist[j];
+          [&](unsigned h, int j) {
             if (by_k) return static_cast<float>(h);
             const float c = static_cast<float>(h >> 20), places = static_cast<float>(h & 0xfffffu);
             return (c - 0.00541521235f / 64.0f * (places - 32.0f * c)) * exp2_approx(-j / kBinsPerOctave);
@@ -1194,7 +1207,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const Quick w_top = quick_weight(sixteenth, s.scale, s.scale.top);
   const float mp_w = mp > 0.0f ? mp * w_top.w : 0.0f;
 
-  for (;; exact = true) {
+  // With top-p alone the lists are free at first: the candidates near the border go to all ranks with the totals.
+  bool direct = by_p && !by_k;
+
+  for (;; exact = true, direct = false) {
     // The kept mass of each run.  With top-p, also the mass in all and above the border's bins; what lies in them
     // goes to a list, and its mass to the span of bins.
     // (a logit above above_l lies in a bin before b0, one below below_l behind b1)
@@ -1309,6 +1325,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (by_p) {
       s.block_sum(&above, &all);
+      const unsigned share = kList / s.ranks;
+      if (direct) {
+        const unsigned n = mem()->near_n;
+        if (n <= share)
+          for (unsigned i = tid; i < n * s.ranks; i += kThreads)
+            s.of(i % s.ranks)->list[s.rank * share + i / s.ranks] = mem()->near[i / s.ranks];
+        if (tid < s.ranks) s.of(tid)->list_n[s.rank] = n;
+      }
       // spans and whether the list holds them all to all ranks with the totals
       if (tid < kSpans * 8 && (tid >> 5) < s.ranks)
         s.of(tid >> 5)->span[s.rank][lane] = mass_of(mem()->span_lo[lane], mem()->span_hi[lane]);
@@ -1333,17 +1357,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       const int hit = max(__ffs(reached) - 1, 0);
       const u64 before = __shfl_sync(0xffffffffu, incl - mass, hit);
-      if (!many) {                                       // the span's elements, from the list
-        for (unsigned i = tid; i < mem()->near_n; i += kThreads) {
-          const u64 c = mem()->near[i];
-          if (((s.place(of_key(static_cast<unsigned>(c >> 32))) - p0) >> coarse) == hit) s.offer(c, s.ranks);
-        }
+      u64* order = reinterpret_cast<u64*>(mem()->hist);
+      auto in_span = [&](u64 c) { return ((s.place(of_key(static_cast<unsigned>(c >> 32))) - p0) >> coarse) == hit; };
+      unsigned n = 0;                                    // the span's elements
+      if (direct) {
+        for (unsigned r = 0; r < s.ranks; ++r) direct = direct && mem()->list_n[r] <= share;
+        if (direct) n = s.pack_some(order, in_span);
+        else s.cluster.sync();                           // every rank has read the lists' sizes
+      }
+      if (!direct && !many) {                            // from this rank's list to all
+        for (unsigned i = tid; i < mem()->near_n; i += kThreads)
+          if (in_span(mem()->near[i])) s.offer(mem()->near[i], s.ranks);
         __syncthreads();
         many = !s.close_lists();
+        if (!many) n = s.pack(order);
       }
       if (!many) {
-        const auto found = s.border_of_lists(before, target, exact ? 0 : slack_of(target, a.vocab, s.ranks), weight_of);
-        if (!exact && !found.sure) continue;
+        const auto found = s.border_of(n, before, target, exact ? 0 : slack_of(target, a.vocab, s.ranks), weight_of);
+        if (!exact && !found.sure) {
+          if (direct) s.cluster.sync();                  // every rank has read its spans and lists
+          continue;
+        }
         border = found.rank;
       } else {
         s.cluster.sync();                                // every rank has read the lists' sizes

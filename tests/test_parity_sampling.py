@@ -281,3 +281,23 @@ def test_min_p_of_one_keeps_the_largest_alone(gbf):
     assert tokens.tolist() == want
     # log(1 / 1000): a float32 logarithm (2 ulp) of a sum that is right to 2^-23
     assert np.all(np.abs(lps + np.log(1000.0)) <= 3 * 2.0 ** -23 * np.log(1000.0))
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("batch,vocab", [(2, 60000), (30, 60001), (60, 50000), (160, 40000), (4, 300000)])
+def test_borders_that_fall_on_an_element(gbf, batch, vocab, f32):
+    """n equal logits and nothing else of weight: a top_p of 1 / 2 ends exactly at an element, and so does a u of 1 / 2
+    or 0 (or a u with no top_p).  The float32 pass may not decide those; all sums are exact, and logprob = -log(kept)
+    is a float32 logarithm (2 ulp) of a ratio that is right to half of one."""
+    rng = np.random.default_rng(batch)
+    counts = np.array([64, 4, 16, 2])[np.arange(batch) % 4]
+    l = np.full((batch, vocab), -200.0, np.float32)
+    at = [np.sort(rng.choice(vocab, n, replace=False)) for n in counts]
+    for b in range(batch):
+        l[b, at[b]] = 1.5
+    u = np.where(np.arange(batch) % 3 == 0, 0.0, 0.5).astype(np.float32)
+    for top_p in (np.full(batch, 0.5), np.where(np.arange(batch) % 2, 0.5, 0.25), None):
+        tokens, lps = run(gbf, l, u, f32, top_p=top_p)
+        kept = counts if top_p is None else (counts * np.maximum(top_p, 1.0 / counts)).astype(int)
+        assert tokens.tolist() == [at[b][int(kept[b] * u[b])] for b in range(batch)]
+        assert np.all(np.abs(lps + np.log(kept)) <= 3 * 2.0 ** -23 * np.log(kept))
