@@ -27,6 +27,37 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// How many clusters of 2^log_ranks CTAs (1 to 8) of `Kernel` the current device holds at once; asked once per device.
+// (Fewer than SMs would hold: those of a GPC are not a multiple of 8.)
+template <auto Kernel>
+cudaError_t resident_clusters(int log_ranks, int threads, int smem, int* out) {
+  static std::atomic<int> known[64][4];              // how many, and one; 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>& k = known[dev & 63][log_ranks];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    e = allow_smem<Kernel>(smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << log_ranks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1u << log_ranks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    k.store(++n, std::memory_order_relaxed);
+  }
+  *out = n - 1;
+  return cudaSuccess;
+}
+
 // Further bits of the device error word (bits 0..2 are common.cuh's).
 enum : unsigned int {
   DEV_ERR_BLOCK_RANGE = 1u << 3,   // a block id outside the cache, or a length outside its block-table row
@@ -59,6 +90,7 @@ struct PagedAttnArgs {
   int group, chunks;        // query heads per KV head; row tiles they are cut into
   int min_units;            // least token tiles per CTA
   int ctas;
+  int log_ranks;            // CTAs of an item's cluster, where items are clusters
 };
 
 int64_t paged_attention_workspace(int hq, int hkv, int d);

@@ -19,6 +19,11 @@
 // workspace, and a second small kernel joins the partials in CTA order, so
 // results do not depend on timing.
 //
+// A call whose lengths cannot be long (by the block table's width, or the
+// window) and whose items all find room at once takes the other split: an item
+// is a cluster of 1 to 8 CTAs, joined through distributed shared memory, with no
+// scan, no workspace and no second launch.
+//
 // Inside a CTA the warps take a range's tiles in turn and never wait for one
 // another within an item: each has its own ring of stages (16 K rows and 16 V
 // rows) filled by 16-byte cp.async, its own running maximum and sum, and its
@@ -33,18 +38,23 @@
 // from another (lengths, table, rows: 3.5 us of the 36 to 50 us of a batch), behind it the join.  Device time, back to
 // back: 32 requests up to 4096, 32 heads on 8 of 128, 49 us (277 MB: 5.6 TB/s); 256 such requests 326 us (2.16 GB: 6.6
 // TB/s); two documents of 131072 on 8 KV heads 126 us (806 MB: 6.4 TB/s); 48 requests on one KV head of 256, window 4096,
-// 35.8 us (158 MB: 4.4 TB/s); one request of 700 tokens 7.4 us (two launches, and reads that wait for one another).
+// 35.8 us (158 MB: 4.4 TB/s); one request of 700 tokens 5.1 us (a launch,
+// and reads that wait for one another).
 //
 // Rounding: scores, maxima, sums and outputs are float32.  P enters the second
 // product as a pair of bf16 (value and remainder, 2^-17 together), because one
 // bf16 alone would add an error as large as the final bf16 rounding.  For
 // groups of up to 8 heads the remainder rides in the rows 8..15 that the heads
 // leave empty, at no further instruction.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "decode.h"
 
 namespace gbf {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kTile = 16;              // tokens per tile
 // An item is one warp's alone (joining the warps costs about as much as four tiles) when it has at most 4 tiles, 8
@@ -57,6 +67,12 @@ constexpr int kSoloOne = 4, kSoloTwo = 8, kSoloMost = 16;
 // 52.3, 51.8 and 54.3.
 constexpr int kOwn = 8;
 constexpr int kSms = 152;
+constexpr int kTogether = 8;           // most CTAs of a cluster that share an item
+// What each of them takes at least where a smaller cluster would do, and at most (in tokens).  One request, 8 KV heads, 256
+// tokens: 5.0 us with four CTAs of 64, 5.4 with eight, 6.9 split over the GPU; 4096 tokens 10.3 with eight of 512, 13.5 over
+// the GPU, 8192 tokens 14.8 and 15.0; 8 requests of 2048 11.6 with four of 512 and 13.0, of 4096 21.7 and 20.5; 24 of 256
+// 7.7 with one CTA each and 10.6, of 1024 18.8 and 15.6.
+constexpr int kTogetherLeast = 64, kTogetherMost = 512;
 constexpr float kLn2 = 0.693147180559945f;
 
 // Layout per padded head width: warps per CTA, ring depth, CTAs per SM.  Two stages ahead of the one in use keep 130 to
@@ -238,6 +254,22 @@ struct Cursor {
     done = false;
     enter(static_cast<int>(p.rest - item * n), warp);
   }
+  // TOGETHER: an equal share of one item's tiles, and nothing else
+  GBF_DEVICE void share_of_item(const PagedAttnArgs& a, int cta, int warp) {
+    const int items = a.hkv * a.chunks, index = cta >> a.log_ranks;
+    const int64_t rank = cta - (index << a.log_ranks);
+    b = index / items;
+    item = index - b * items;
+    r = request_of(a, b);
+    left = 0;
+    turn = solo_turn = most_solo = 0;
+    t0 = static_cast<int>(r.tiles * rank >> a.log_ranks);
+    t1 = static_cast<int>(r.tiles * (rank + 1) >> a.log_ranks);
+    whole = solo = done = false;
+    mine = true;
+    t = t0 + warp;
+    step = NW;
+  }
   // the segment that begins at unit u of the item
   GBF_DEVICE void enter(int u, int warp) {
     const int64_t rest = r.tiles + kOwn - u, n = rest < left ? rest : left;
@@ -308,7 +340,9 @@ GBF_DEVICE void store_out2(const PagedAttnArgs& a, int64_t at, float2 o) {
 
 // DP: head width padded to 64, 128 or 256.  WIDE: 9..16 heads per row tile
 // (else up to 8, with the remainders of P in rows 8..15).
-template <int DP, bool WIDE>
+// TOGETHER: the split into clusters: an equal share of an item's tiles is each
+// CTA's, and each joins a part of the columns.
+template <int DP, bool WIDE, bool TOGETHER>
 __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
     paged_attention_kernel(const PagedAttnArgs a) {
   constexpr int NW = Plan<DP>::kWarps, NS = Plan<DP>::kStages, NT = NW * 32;
@@ -319,14 +353,23 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[2][NW][16], sm_l[2][NW][16];
   __shared__ uint32_t sm_valid[NW][NS];
+  __shared__ float cta_m[16], cta_l[16];         // TOGETHER: this CTA's maxima and sums
 
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Place place = locate<NT>(a, blockIdx.x, blockIdx.x == 0);
-  if (place.b < 0) return;
-  const int64_t first_unit = static_cast<int64_t>(blockIdx.x) * place.share;
-  const int64_t units = place.units - first_unit < place.share ? place.units - first_unit : place.share;
+  Cursor<NW> load, work;
+  if (TOGETHER) {
+    work.share_of_item(a, blockIdx.x, warp);
+    const int len = a.lens[work.b];
+    if (tid == 0 && (len < 0 || len > a.room)) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
+  } else {
+    const Place place = locate<NT>(a, blockIdx.x, blockIdx.x == 0);
+    if (place.b < 0) return;
+    const int64_t first_unit = static_cast<int64_t>(blockIdx.x) * place.share;
+    const int64_t units = place.units - first_unit < place.share ? place.units - first_unit : place.share;
+    work.start(a, place, units, warp);
+  }
 
   unsigned char* stages = smem + warp * (NS * stage_bytes<DP>());
   const uint32_t stages_u = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
@@ -342,9 +385,7 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
   const int chunk_row = lane / CPR;
   const bool col_on = chunk_col * 8 < a.d;
 
-  Cursor<NW> load, work;
-  load.start(a, place, units, warp);
-  work = load;
+  load = work;
   load.settle(a, warp);
 
   // Block-table entry of lane's token (lanes 0..15) of the load cursor's tile, requested one tile before its rows are,
@@ -578,6 +619,7 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
       }
     const bool whole = work.whole;
     float* part = a.ws + (2 * static_cast<int64_t>(blockIdx.x) + (work.t0 == 0 ? 1 : 0)) * partial_floats<DP, WIDE>();
+    float* cta_o = reinterpret_cast<float*>(smem);         // TOGETHER: [rows][DP], where the stages were
 #pragma unroll
     for (int pass = 0; pass < 2 * HALVES; ++pass) {
       const int h = pass >> 1, half = pass & 1;
@@ -613,7 +655,13 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
           acc.w += v.w;
           if (big != -INFINITY) total += sm_l[parity][w][row] * exp2_approx(sm_m[parity][w][row] - big);
         }
-        if (whole) {
+        if (TOGETHER) {
+          *reinterpret_cast<float4*>(cta_o + row * DP + c) = acc;
+          if (c == 0) {
+            cta_m[row] = big;
+            cta_l[row] = total;
+          }
+        } else if (whole) {
           const float inv = total == 0.0f ? 0.0f : 1.0f / total;
           acc.x *= inv;
           acc.y *= inv;
@@ -629,6 +677,48 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
           }
         }
       }
+    }
+    if (TOGETHER) {
+      cg::cluster_group cluster = cg::this_cluster();
+      const int ranks = 1 << a.log_ranks;
+      cluster.sync();
+      for (int i = static_cast<int>(cluster.block_rank()) * NT + tid; i < rows * (DP / 4); i += ranks * NT) {
+        const int row = i / (DP / 4), c = (i - row * (DP / 4)) * 4;
+        if (c >= a.d) continue;
+        float m_of[kTogether], l_of[kTogether], top = -INFINITY, total = 0.0f;
+        float4 o_of[kTogether], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          m_of[k] = -INFINITY;
+          l_of[k] = 0.0f;
+          o_of[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k < ranks) {
+            m_of[k] = *cluster.map_shared_rank(cta_m + row, k);
+            l_of[k] = *cluster.map_shared_rank(cta_l + row, k);
+            o_of[k] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(cta_o + row * DP + c, k));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) top = fmaxf(top, m_of[k]);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          const float f = m_of[k] == -INFINITY ? 0.0f : exp2_approx(m_of[k] - top);
+          total += l_of[k] * f;
+          acc.x += o_of[k].x * f;
+          acc.y += o_of[k].y * f;
+          acc.z += o_of[k].z * f;
+          acc.w += o_of[k].w * f;
+        }
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        store_out4(a, (q_row0 + row) * a.d + c, acc);
+        if (c == 0 && a.lse) a.lse[q_row0 + row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+      }
+      cluster.sync();                            // the others have read this CTA's results
+      break;
     }
     parity ^= 1;
     if (!work.next_segment(a, warp)) break;
@@ -721,18 +811,56 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAt
 }
 
 template <int DP, bool WIDE>
+cudaError_t launch_together(const PagedAttnArgs& a, int items, cudaStream_t stream) {
+  const cudaError_t e = allow_smem<paged_attention_kernel<DP, WIDE, true>>(smem_bytes<DP>());
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items << a.log_ranks);
+  cfg.blockDim = dim3(Plan<DP>::kWarps * 32);
+  cfg.dynamicSmemBytes = smem_bytes<DP>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1 << a.log_ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_attention_kernel<DP, WIDE, true>, a);
+}
+
+template <int DP, bool WIDE>
 cudaError_t launch(PagedAttnArgs a, cudaStream_t stream) {
   constexpr int NW = Plan<DP>::kWarps;
-  cudaError_t e = allow_smem<paged_attention_kernel<DP, WIDE>>(smem_bytes<DP>());
-  if (e != cudaSuccess) return e;
   a.min_units = NW;
   const int64_t seen = a.window > 0 && a.window < a.room ? a.window : a.room;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.hkv * a.chunks;
+  cudaError_t e = cudaSuccess;
+  if (seen <= kTogether * kTogetherMost) {
+    int i = 0, n = 0;
+    while (1 << i < kTogether && seen > kTogetherLeast << i) ++i;
+    auto fit = [&] { return resident_clusters<paged_attention_kernel<DP, WIDE, true>>(i, NW * 32, smem_bytes<DP>(), &n); };
+    e = fit();
+    while (e == cudaSuccess && i > 0 && items > n) {
+      --i;
+      e = fit();
+    }
+    if (e != cudaSuccess) return e;
+    if (items <= n && seen <= kTogetherMost << i) {
+      a.log_ranks = i;
+      return launch_together<DP, WIDE>(a, static_cast<int>(items), stream);
+    }
+  }
+  e = allow_smem<paged_attention_kernel<DP, WIDE, false>>(smem_bytes<DP>());
+  if (e != cudaSuccess) return e;
   const int64_t tiles = (seen + kTile - 1) / kTile;
-  const int64_t units = (tiles + kOwn) * a.batch * a.hkv * a.chunks;
+  const int64_t units = (tiles + kOwn) * items;
   int64_t ctas = (units + NW - 1) / NW;
   if (ctas > kSms * Plan<DP>::kPerSm) ctas = kSms * Plan<DP>::kPerSm;
   a.ctas = static_cast<int>(ctas);
-  e = launch_pdl(paged_attention_kernel<DP, WIDE>, dim3(a.ctas), dim3(NW * 32), smem_bytes<DP>(), stream, a);
+  e = launch_pdl(paged_attention_kernel<DP, WIDE, false>, dim3(a.ctas), dim3(NW * 32), smem_bytes<DP>(), stream, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
   const int rows = a.group < 16 ? a.group : 16;
   return launch_pdl(paged_attention_join_kernel<DP, WIDE>, dim3(a.ctas - 1, rows), dim3(128), 0, stream, a);

@@ -53,9 +53,9 @@
 //
 // What bounds it: instructions and barriers, not HBM.  A nucleus row issues 107
 // instructions per 32 elements (9 for pass 1, some 12 for the histogram, 55 for the
-// weights, the rest for the border and the draw) at 2.5 a cycle and SM, and a cluster passes five barriers with an
-// exchange behind each, 1 to 2 us apiece.  Measured (device time, back to
-// back): one row of 32000 bf16, nucleus, 17.6 us (temperature alone 8.4);
+// weights, the rest for the border and the draw) at 2.5 a cycle and SM, and a
+// cluster passes five barriers with an exchange behind each, 1 to 2 us apiece.
+// Measured (device time, back to back): one row of 32000 bf16, nucleus, 17.6 us (temperature alone 8.4);
 // 32 rows of 151936, mixed requests, 36.7 us (10 MB: 0.26 TB/s); 61 rows of 50257,
 // temperature alone, 15.1 us; 256 rows of 128000 float32, nucleus, 182 us (131 MB:
 // 0.72 TB/s).
@@ -63,7 +63,6 @@
 // Ranks hand each other totals by remote stores into boxes (read locally behind
 // the next barrier).
 #include <cfloat>
-#include <mutex>
 
 #include <cooperative_groups.h>
 
@@ -1488,68 +1487,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs that are there at once with two CTAs on an SM (a bound for a choice, not for correctness).
+constexpr int kShared[4] = {304, 152, 74, 36};
 // Dynamic shared memory of a CTA that is to have an SM for itself.
 constexpr int kAloneBytes = 120 * 1024;
 static_assert(sizeof(Shared) + kStageBytes < kAloneBytes && 2 * kAloneBytes > 228 * 1024, "");
 
-// The launch of `batch` clusters of `ranks` CTAs.
 template <typename T, bool STAGED>
-struct Launch {
+cudaError_t launch(const SampleArgs& a, int ranks, size_t smem, cudaStream_t stream) {
+  const cudaError_t e = allow_smem<sample_kernel<T, STAGED>>(kAloneBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-
-  Launch(int64_t batch, int ranks, size_t smem, cudaStream_t stream) {
-    cfg.gridDim = dim3(static_cast<unsigned>(batch * ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-  }
-  static cudaError_t allow() { return allow_smem<sample_kernel<T, STAGED>>(kAloneBytes); }
-  cudaError_t go(const SampleArgs& a) { return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a); }
-};
-
-// How many clusters of 1, 2, 4 and 8 CTAs the device holds at once, with an SM for each CTA and with two CTAs on one
-// (the SMs of a GPC are not a multiple of 8: 15 and 36 clusters of eight here, not 19 and 38).  Asked once per device.
-struct Fits {
-  int alone[4], shared[4];
-};
-cudaError_t fits(Fits* out) {
-  static std::mutex lock;
-  static Fits known[64];
-  static uint64_t done = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> hold(lock);
-  Fits& f = known[dev & 63];
-  if (!(done >> (dev & 63) & 1)) {
-    typedef Launch<__nv_bfloat16, true> L;
-    e = L::allow();
-    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
-      L one(1, 1 << i, kAloneBytes, nullptr), two(1, 1 << i, sizeof(Shared) + kStageBytes, nullptr);
-      e = cudaOccupancyMaxActiveClusters(&f.alone[i], sample_kernel<__nv_bfloat16, true>, &one.cfg);
-      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&f.shared[i], sample_kernel<__nv_bfloat16, true>, &two.cfg);
-    }
-    if (e != cudaSuccess) return e;
-    done |= 1ull << (dev & 63);
-  }
-  *out = f;
-  return cudaSuccess;
-}
-
-template <typename T, bool STAGED>
-cudaError_t launch(const SampleArgs& a, int ranks, bool alone, size_t smem, cudaStream_t stream) {
-  const cudaError_t e = Launch<T, STAGED>::allow();
-  if (e != cudaSuccess) return e;
-  return Launch<T, STAGED>(a.batch, ranks, alone ? kAloneBytes : smem, stream).go(a);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a);
 }
 
 template <typename T>
@@ -1557,26 +1519,33 @@ cudaError_t plan(const SampleArgs& a, cudaStream_t stream) {
   constexpr int N = Elem<T>::N;
   const int64_t vectors = (static_cast<int64_t>(a.vocab) + N - 1) / N + 1;
   auto slice = [&](int ranks) { return (vectors + ranks - 1) / ranks * 16; };
-  Fits f;
-  const cudaError_t e = fits(&f);
-  if (e != cudaSuccess) return e;
+  // (of the kernel with an SM for each CTA)
+  auto alone_at = [](int i, int* n) { return resident_clusters<sample_kernel<T, true>>(i, kThreads, kAloneBytes, n); };
   // CTAs per row: as many as leave an SM to each CTA, because two on one SM cost each other more than half a slice is
   // worth (64 rows of 32000, nucleus: 27 us with two, 28 with four; 16 rows: 21.6 with four, 23.5 with eight) ...
-  int i = 3;
-  while (i > 0 && a.batch > f.alone[i]) --i;
+  int i = 3, n = 0;
+  cudaError_t e = alone_at(i, &n);
+  while (e == cudaSuccess && i > 0 && a.batch > n) e = alone_at(--i, &n);
+  if (e != cudaSuccess) return e;
+  bool alone = a.batch <= n;
   // ... and twice that, two on one SM, where a slice would not fit in shared memory (32 rows of 151936, nucleus: 51 us
   // with eight, 60 with four; 200 rows of 50257: 73 with two, 82 with one; 256 of 32000, which fit: 62 with one, 69 with
-  // two)
-  if (i < 3 && slice(1 << i) > kStageBytes && (i == 0 || a.batch <= f.shared[i + 1])) ++i;
+  // two) and they are all there at once (76 rows of 128000: 66 with two, 74 with four)
+  if (i < 3 && slice(1 << i) > kStageBytes && (i == 0 || a.batch <= kShared[i + 1])) {
+    ++i;
+    alone = false;
+  }
   // very long rows: so that a bin's count and a thread's sums hold
-  if (a.vocab > 256 * 1024 && i < 2) i = 2;
+  if (a.vocab > 256 * 1024 && i < 2) {
+    i = 2;
+    alone = false;
+  }
   // Where they fit, CTAs are kept from sharing an SM (by the shared memory they ask for): in a run of calls, the second
   // call's would otherwise settle in pairs beside the first one's (61 rows of 50257: 14.9 us, or 21.8 in half of the
   // processes; 152 rows of 30000: 16.5 and 24).
-  const bool alone = a.batch <= f.alone[i];
-  const int64_t bytes = slice(1 << i);
-  if (bytes <= kStageBytes) return launch<T, true>(a, 1 << i, alone, sizeof(Shared) + static_cast<size_t>(bytes), stream);
-  return launch<T, false>(a, 1 << i, alone, sizeof(Shared), stream);
+  const size_t bytes = static_cast<size_t>(slice(1 << i));
+  if (bytes <= kStageBytes) return launch<T, true>(a, 1 << i, alone ? kAloneBytes : sizeof(Shared) + bytes, stream);
+  return launch<T, false>(a, 1 << i, alone ? kAloneBytes : sizeof(Shared), stream);
 }
 
 }  // namespace

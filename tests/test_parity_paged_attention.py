@@ -267,3 +267,63 @@ def test_empty_batch(gbf):
     gbf.paged_attention(z, kc, kc.clone(), i.view(0, 4), i, 16, torch.empty_like(z),
                         torch.empty(1 << 23, dtype=torch.uint8, device="cuda"))
     assert gbf.device_status()[0] == gbf.OK
+
+
+# Which of the two splits a call takes depends on the block table's width and on how many items there are: the cases above
+# have tables as narrow as their lengths; these have room for more tokens than clusters take, or more items.
+
+WIDE = 600      # blocks of 16: 9600 tokens
+
+
+@pytest.mark.parametrize("d", [16, 64, 80, 128, 176, 256])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2), (5, 5), (12, 1), (24, 2)])
+def test_wide_tables(gbf, d, hq, hkv):
+    c = case(RAGGED, hq, hkv, d, 16, seed=d + hq, width=WIDE)
+    check(c, *run(gbf, c))
+
+
+@pytest.mark.parametrize("group", [1, 7, 8, 9, 16, 17, 33])
+@pytest.mark.parametrize("out_scale", [None, 0.01])
+def test_wide_tables_groups_and_codes(gbf, group, out_scale):
+    c = case([3, 40, 0, 129, 700], 2 * group, 2, 64, 16, seed=group, width=WIDE)
+    check(c, *run(gbf, c, out_scale=out_scale), out_scale=out_scale)
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [5000], [4097, 1, 1, 1], [0, 0, 2049, 0], [16] * 70, [1000] * 9])
+@pytest.mark.parametrize("window", [0, 4500])
+def test_wide_tables_splits(gbf, lens, window):
+    c = case(lens, 8, 2, 128, 16, seed=sum(lens), width=WIDE)
+    check(c, *run(gbf, c, window=window), window=window)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 2), (128, 24, 2), (256, 16, 2)])
+@pytest.mark.parametrize("batch,longest", [(1, 50), (1, 300), (3, 4000), (8, 500), (16, 900), (30, 130), (60, 260), (150, 60),
+                                           (170, 60)])
+def test_few_items_by_their_number_and_length(gbf, d, hq, hkv, batch, longest):
+    """Clusters of 1 to 8 CTAs, and more items than find room as such."""
+    rng = np.random.default_rng(batch * longest)
+    lens = rng.integers(0, longest + 1, batch)
+    lens[0] = longest
+    c = case(lens, hq, hkv, d, 16, seed=batch)
+    check(c, *run(gbf, c))
+
+
+@pytest.mark.parametrize("width", [4, WIDE])
+def test_bad_ids_and_lengths_in_either_split(gbf, width):
+    """The GPU skips what it cannot look up, reports it, and the other requests come out as ever."""
+    c = case([40, 33, 64, 20], 8, 2, 128, 16, seed=9, width=width)
+    table, lens = c["table"].copy(), c["lens"].copy()
+    bad = dict(c, table=table, lens=lens)
+    bad["table"] = table.copy()
+    bad["table"][1, 1] = 1 << 20                       # tokens 16..31 of request 1 lie nowhere
+    bad["lens"] = lens.copy()
+    bad["lens"][3] = -5                                # request 3 has no length
+    out, lse = run(gbf, bad)
+    s, msg = gbf.device_status()
+    assert s == gbf.EDEVICE and "block id or length" in msg
+    good, good_lse = run(gbf, c)
+    assert gbf.device_status()[0] == gbf.OK
+    for b in (0, 2):
+        assert np.array_equal(out[b], good[b]) and np.array_equal(lse[b], good_lse[b])
+    y = formats.bf16_decode(out)
+    assert np.isfinite(y).all() and (y[3] == 0).all() and np.isneginf(lse[3]).all() and np.isfinite(lse[1]).all()
