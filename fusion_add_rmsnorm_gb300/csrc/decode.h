@@ -90,7 +90,7 @@ struct PagedAttnArgs {
   int group, chunks;        // query heads per KV head; row tiles they are cut into
   int min_units;            // least token tiles per CTA
   int ctas;
-  int log_ranks;            // CTAs of an item's cluster, where items are clusters
+  int log_ranks;            // CTAs of an item's cluster, where items are clusters; -1: items are warps
 };
 
 int64_t paged_attention_workspace(int hq, int hkv, int d);

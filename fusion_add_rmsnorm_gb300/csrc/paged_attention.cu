@@ -20,9 +20,9 @@
 // results do not depend on timing.
 //
 // A call whose lengths cannot be long (by the block table's width, or the
-// window) and whose items all find room at once takes the other split: an item
-// is a cluster of 1 to 8 CTAs, joined through distributed shared memory, with no
-// scan, no workspace and no second launch.
+// window) takes another split: an item is one warp's, or, where all items find
+// room at once, a cluster's of 1 to 8 CTAs, joined through distributed shared
+// memory; with no scan, no workspace and no second launch.
 //
 // Inside a CTA the warps take a range's tiles in turn and never wait for one
 // another within an item: each has its own ring of stages (16 K rows and 16 V
@@ -73,6 +73,10 @@ constexpr int kTogether = 8;           // most CTAs of a cluster that share an i
 // the GPU, 8192 tokens 14.8 and 15.0; 8 requests of 2048 11.6 with four of 512 and 13.0, of 4096 21.7 and 20.5; 24 of 256
 // 7.7 with one CTA each and 10.6, of 1024 18.8 and 15.6.
 constexpr int kTogetherLeast = 64, kTogetherMost = 512;
+// One warp takes an item alone, with no join at all, where it has at most four tiles (896 items of up to 64 tokens: 6.3
+// us, 12.1 over the GPU; 160 items: 5.3, 5.5 with a CTA each, 10.1 over the GPU), or 16 where the items are too many for a
+// CTA each (896 of 256 tokens: 16.8 us, 21.0 over the GPU, 23.1 with a CTA each; of 512 tokens 29.8, 29.9 and 32.4).
+constexpr int kWarpTokens = 64, kWarpTokensMany = 256;
 constexpr float kLn2 = 0.693147180559945f;
 
 // Layout per padded head width: warps per CTA, ring depth, CTAs per SM.  Two stages ahead of the one in use keep 130 to
@@ -254,21 +258,30 @@ struct Cursor {
     done = false;
     enter(static_cast<int>(p.rest - item * n), warp);
   }
-  // TOGETHER: an equal share of one item's tiles, and nothing else
-  GBF_DEVICE void share_of_item(const PagedAttnArgs& a, int cta, int warp) {
-    const int items = a.hkv * a.chunks, index = cta >> a.log_ranks;
-    const int64_t rank = cta - (index << a.log_ranks);
+  // TOGETHER: an equal share of one item's tiles, or a whole item, and nothing else; false: there is none
+  GBF_DEVICE bool share_of_item(const PagedAttnArgs& a, int cta, int warp) {
+    solo = a.log_ranks < 0;
+    const int items = a.hkv * a.chunks, index = solo ? cta * NW + warp : cta >> a.log_ranks;
+    if (index >= a.batch * items) return false;
     b = index / items;
     item = index - b * items;
     r = request_of(a, b);
     left = 0;
     turn = solo_turn = most_solo = 0;
-    t0 = static_cast<int>(r.tiles * rank >> a.log_ranks);
-    t1 = static_cast<int>(r.tiles * (rank + 1) >> a.log_ranks);
-    whole = solo = done = false;
+    whole = done = false;
     mine = true;
-    t = t0 + warp;
-    step = NW;
+    if (solo) {
+      t = t0 = 0;
+      t1 = r.tiles;
+      step = 1;
+    } else {
+      const int64_t rank = cta - (index << a.log_ranks);
+      t0 = static_cast<int>(r.tiles * rank >> a.log_ranks);
+      t1 = static_cast<int>(r.tiles * (rank + 1) >> a.log_ranks);
+      t = t0 + warp;
+      step = NW;
+    }
+    return true;
   }
   // the segment that begins at unit u of the item
   GBF_DEVICE void enter(int u, int warp) {
@@ -340,8 +353,8 @@ GBF_DEVICE void store_out2(const PagedAttnArgs& a, int64_t at, float2 o) {
 
 // DP: head width padded to 64, 128 or 256.  WIDE: 9..16 heads per row tile
 // (else up to 8, with the remainders of P in rows 8..15).
-// TOGETHER: the split into clusters: an equal share of an item's tiles is each
-// CTA's, and each joins a part of the columns.
+// TOGETHER: the split into clusters (an equal share of an item's tiles is each
+// CTA's, and each joins a part of the columns) or warps.
 template <int DP, bool WIDE, bool TOGETHER>
 __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
     paged_attention_kernel(const PagedAttnArgs a) {
@@ -360,9 +373,9 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Cursor<NW> load, work;
   if (TOGETHER) {
-    work.share_of_item(a, blockIdx.x, warp);
+    if (!work.share_of_item(a, blockIdx.x, warp)) return;  // (a warp without an item: nobody waits for it)
     const int len = a.lens[work.b];
-    if (tid == 0 && (len < 0 || len > a.room)) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
+    if (lane == 0 && (len < 0 || len > a.room)) raise_error(a.err, DEV_ERR_BLOCK_RANGE);
   } else {
     const Place place = locate<NT>(a, blockIdx.x, blockIdx.x == 0);
     if (place.b < 0) return;
@@ -815,7 +828,7 @@ cudaError_t launch_together(const PagedAttnArgs& a, int items, cudaStream_t stre
   const cudaError_t e = allow_smem<paged_attention_kernel<DP, WIDE, true>>(smem_bytes<DP>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(items << a.log_ranks);
+  cfg.gridDim = dim3(a.log_ranks < 0 ? (items + Plan<DP>::kWarps - 1) / Plan<DP>::kWarps : items << a.log_ranks);
   cfg.blockDim = dim3(Plan<DP>::kWarps * 32);
   cfg.dynamicSmemBytes = smem_bytes<DP>();
   cfg.stream = stream;
@@ -823,7 +836,7 @@ cudaError_t launch_together(const PagedAttnArgs& a, int items, cudaStream_t stre
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1 << a.log_ranks;
+  attr[1].val.clusterDim.x = a.log_ranks < 0 ? 1 : 1 << a.log_ranks;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -838,7 +851,9 @@ cudaError_t launch(PagedAttnArgs a, cudaStream_t stream) {
   const int64_t seen = a.window > 0 && a.window < a.room ? a.window : a.room;
   const int64_t items = static_cast<int64_t>(a.batch) * a.hkv * a.chunks;
   cudaError_t e = cudaSuccess;
-  if (seen <= kTogether * kTogetherMost) {
+  a.log_ranks = -1;                              // a warp per item
+  bool together = seen <= kWarpTokens;
+  if (!together && seen <= kTogether * kTogetherMost) {
     int i = 0, n = 0;
     while (1 << i < kTogether && seen > kTogetherLeast << i) ++i;
     auto fit = [&] { return resident_clusters<paged_attention_kernel<DP, WIDE, true>>(i, NW * 32, smem_bytes<DP>(), &n); };
@@ -848,11 +863,14 @@ cudaError_t launch(PagedAttnArgs a, cudaStream_t stream) {
       e = fit();
     }
     if (e != cudaSuccess) return e;
-    if (items <= n && seen <= kTogetherMost << i) {
+    if (items <= n) {
+      together = seen <= kTogetherMost << i;
       a.log_ranks = i;
-      return launch_together<DP, WIDE>(a, static_cast<int>(items), stream);
+    } else {
+      together = seen <= kWarpTokensMany;
     }
   }
+  if (together && items <= 1 << 28) return launch_together<DP, WIDE>(a, static_cast<int>(items), stream);
   e = allow_smem<paged_attention_kernel<DP, WIDE, false>>(smem_bytes<DP>());
   if (e != cudaSuccess) return e;
   const int64_t tiles = (seen + kTile - 1) / kTile;

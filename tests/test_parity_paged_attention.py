@@ -298,9 +298,9 @@ def test_wide_tables_splits(gbf, lens, window):
 
 @pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 2), (128, 24, 2), (256, 16, 2)])
 @pytest.mark.parametrize("batch,longest", [(1, 50), (1, 300), (3, 4000), (8, 500), (16, 900), (30, 130), (60, 260), (150, 60),
-                                           (170, 60)])
+                                           (170, 60), (200, 250), (300, 5)])
 def test_few_items_by_their_number_and_length(gbf, d, hq, hkv, batch, longest):
-    """Clusters of 1 to 8 CTAs, and more items than find room as such."""
+    """Clusters of 1 to 8 CTAs, items of one warp each, and more items than find room as such."""
     rng = np.random.default_rng(batch * longest)
     lens = rng.integers(0, longest + 1, batch)
     lens[0] = longest
