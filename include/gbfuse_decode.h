@@ -90,6 +90,8 @@ GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, i
  * Requires head_dim % 16 == 0, head_dim <= 256, n_q_heads % n_kv_heads == 0,
  * cache_rows < 2^31, 16-byte aligned q, k_cache, v_cache, out, workspace; scale
  * > 0 and finite.  batch == 0 enqueues nothing.  out and lse may not overlap each other or an input.
+ * How the work is split follows from batch, heads, window and max_blocks * block_size, not from the lengths, which only
+ * the device knows: for few or short requests, a max_blocks (or a window) no wider than they need saves 2 to 8 us.
  */
 GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void* v_cache, int64_t cache_rows,
                                  const int32_t* block_table, int64_t table_stride, int64_t max_blocks,
