@@ -1225,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (tid == 0) mem()->near_n = mem()->mine_n = mem()->doubt = 0;
     __syncthreads();
     u64 kept = 0, above = 0, all = 0;
-    auto weight_of = [&](float l) {                      // the weight that this round's sums are made of
+    auto weight_of = [&](float l) {                      // the weight that this turn's sums are made of
       u64 w0, w1;
       if (exact) {
         s.weigh(two(l), &w0, &w1);

@@ -175,3 +175,11 @@ def test_graph_follows_the_lengths(gbf):
         want = {**want, "ctx": seq, "table": p.table, "free": p.free_ring, "ring": [p.head, p.count]}
     assert np.array_equal(ctx.cpu().numpy(), want["ctx"]) and ring.cpu().numpy().tolist() == want["ring"]
     assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("batch,prompts,ended", [(512, 0, 3), (513, 0, 3), (900, 2, 20), (2040, 0, 0), (2300, 1, 60)])
+def test_large_batches_of_decode_rows(gbf, batch, prompts, ended, in_place):
+    """Batches scanned by 256 and by 1024 threads, with up to two tokens for each thread and with more."""
+    c = case(np.random.default_rng(batch), batch, 16, 40, prompts, ended)
+    check(c, run(gbf, c, in_place=in_place))
