@@ -960,6 +960,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   s.rank = s.cluster.block_rank();
   s.ranks = s.cluster.num_blocks();
   s.turn = 0;
+  // Shared memory of another CTA may be touched only once that CTA runs: every rank says so here, and the first exchange
+  // waits for all of them (behind the row's read, where that costs nothing).
+  s.cluster.barrier_arrive();
   const int tid = s.tid = threadIdx.x, lane = s.lane = tid & 31, warp = s.warp = tid >> 5;
   if (tid < 64) mem()->pow[tid] = kPow[tid];
   if (tid < 16) {
@@ -1044,6 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   __syncthreads();
   top = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_a[lane]) : 0u);
   low = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(mem()->warp_b[lane]) : 0xffffffffu);
+  s.cluster.barrier_wait();                              // all ranks have started
   {
     const u64(*box)[8] = s.exchange(top, low);
     for (unsigned r = 0; r < s.ranks; ++r) {

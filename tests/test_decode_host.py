@@ -179,3 +179,13 @@ def test_compiled_wrappers_arguments(gbf):
         raises("out_scale", gbf.paged_attention, **{**attn, "out": u8(2, 8, 64), "out_scale": bad})
     with pytest.raises(TypeError, match="out"):
         gbf.paged_attention(**{**attn, "out_scale": 1.0})
+
+
+def test_clusters_have_started_before_they_write_to_each_other():
+    """Shared memory of another CTA may be touched only once that CTA is known to run, which nothing shows from
+    outside: in the sampling kernel all ranks arrive at its start, and wait before the first exchange."""
+    text = open(os.path.join(ROOT, "fusion_add_rmsnorm_gb300", "csrc", "sample_tokens.cu")).read()
+    kernel = text[text.index("sample_kernel(const SampleArgs a) {"):]
+    arrive, wait = kernel.find("cluster.barrier_arrive();"), kernel.find("cluster.barrier_wait();")
+    first = min(kernel.index(f"s.{f}(") for f in ("exchange", "offer", "of", "find_bins", "close_lists"))
+    assert 0 <= arrive < kernel.index("pdl_wait();") < wait < first

@@ -301,3 +301,32 @@ def test_borders_that_fall_on_an_element(gbf, batch, vocab, f32):
         kept = counts if top_p is None else (counts * np.maximum(top_p, 1.0 / counts)).astype(int)
         assert tokens.tolist() == [at[b][int(kept[b] * u[b])] for b in range(batch)]
         assert np.all(np.abs(lps + np.log(kept)) <= 3 * 2.0 ** -23 * np.log(kept))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("batch", [1, 5, 18, 40])
+def test_short_rows_on_clusters(gbf, batch, f32):
+    """Rows shorter than a vector per CTA, whose CTAs have next to nothing to do before they first write to one
+    another, in long runs of calls behind one another and beside a kernel that keeps part of the SMs busy."""
+    rng = np.random.default_rng(batch)
+    busy = torch.zeros(64 << 20, device="cuda")
+    other = torch.cuda.Stream()
+    for vocab in (1, 2, 7, 9, 63):
+        l, u = logits(rng, batch, vocab, f32), rng.random(batch).astype(np.float32)
+        p = params(rng, batch)
+        t = torch.from_numpy(l).cuda() if f32 else torch.from_numpy(l).to(torch.bfloat16).cuda()
+        args = {k: torch.from_numpy(v).cuda() for k, v in p.items()}
+        uniform = torch.from_numpy(u).cuda()
+        tokens = torch.full((60, batch), -7, dtype=torch.int32, device="cuda")
+        lp = torch.full((60, batch), 9.0, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(60):
+            if i % 10 == 0:
+                with torch.cuda.stream(other):
+                    busy.add_(1.0)
+            gbf.sample_tokens(t, uniform, tokens[i], logprob=lp[i], **args)
+        torch.cuda.synchronize()
+        tokens, lp = tokens.cpu().numpy(), lp.cpu().numpy()
+        check(l, u, (tokens[0], lp[0]), **p)
+        assert (tokens == tokens[0]).all() and (lp.view(np.int32) == lp[0].view(np.int32)).all()
+    assert gbf.device_status()[0] == gbf.OK
