@@ -200,10 +200,9 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
     a.ring_out[1] = count - taken + given;
   }
   for (int64_t b = worker; b < n; b += workers) {
-    const int c = ctx[b];
-    const int tokens = first_tok[b + 1] - first_tok[b];
-    const bool ended = c >= 0 && first_old[b + 1] != first_old[b];
-    a.seq[b] = c < 0 ? ~c : ended ? 0 : c + tokens;
+    // (by its own new tokens: the prefix sums stop at 2^31 - 1, which a refused request's new length may reach)
+    const int c = ctx[b], more = a.add[b];
+    a.seq[b] = c < 0 ? ~c : more < 0 ? 0 : c + more;
     if (a.start) a.start[b] = first_tok[b];
   }
   if (worker == 0 && a.start) a.start[n] = first_tok[n];

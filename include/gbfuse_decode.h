@@ -38,7 +38,7 @@ extern "C" {
  *   - token i of request b, the packed token start[b] + i, gets
  *     pos = ctx + i and slot = block_table[b, pos / bs] * bs + pos % bs.
  * seq_lens[b] = ctx + new (0 when it has ended); start[b] = tokens of the
- * requests before b (start[batch] = all).  The slots and positions are what
+ * requests before b (start[batch] = all; sums past 2^31 - 1 stay there).  The slots and positions are what
  * gbf_qkv_split_norm_rope takes, seq_lens and block_table what
  * gbfd_paged_attention takes.
  *

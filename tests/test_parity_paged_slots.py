@@ -183,3 +183,26 @@ def test_large_batches_of_decode_rows(gbf, batch, prompts, ended, in_place):
     """Batches scanned by 256 and by 1024 threads, with up to two tokens for each thread and with more."""
     c = case(np.random.default_rng(batch), batch, 16, 40, prompts, ended)
     check(c, run(gbf, c, in_place=in_place))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("tokens", [3, 3000])
+@pytest.mark.parametrize("batch", [5, 700])
+def test_a_length_that_fills_the_sums(gbf, batch, tokens, in_place):
+    """A request whose new length is 2^31 - 1 is refused; the ones behind it take their block and their length all the
+    same, although their packed tokens lie past the end."""
+    c = case(np.random.default_rng(batch), batch, 4, 40, ended=1, spare=2 * batch)
+    c["ctx"][1:4], c["new"][0:4] = [0, 4, 6], [1, 2 ** 31 - 1, 1, 1]
+    c["table"][2, 0], c["table"][3, :2] = c["free"][c["ring"][0]], c["free"][c["ring"][0]]     # (any block)
+    got = run(gbf, c, tokens=tokens, pad=0, in_place=in_place)
+    # (a new length that only just does not fit is refused alike, and can be counted out one by one)
+    room = c["table"].shape[1] * 4
+    p, seq, slots, pos, _, refused = decode.paged_slots(c["ctx"], np.where(c["new"] > room, room + 1, c["new"]), c["table"],
+                                                        c["free"], c["ring"], 4)
+    assert refused[1] and not refused[2] and not refused[3] and seq[2] == 5 and seq[3] == 7
+    assert np.array_equal(got["seq"], seq) and np.array_equal(got["table"], p.table)
+    assert np.array_equal(got["free"], p.free_ring) and got["ring"].tolist() == [p.head, p.count]
+    assert got["slots"][0] == slots[0] and (got["slots"][1:] == -1).all()
+    assert np.array_equal(got["pos"], np.concatenate([pos[:1], np.arange(tokens - 1)]))
+    assert got["start"][:2].tolist() == [0, 1] and (got["start"][3:] == 2 ** 31 - 1).all()
+    assert gbf.device_status()[0] == gbf.EDEVICE
