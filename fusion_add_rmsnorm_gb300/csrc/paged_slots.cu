@@ -75,11 +75,10 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = a.block_size;
   const int64_t room = static_cast<int64_t>(a.max_blocks) * bs;
-  int head = a.ring[0], count = a.ring[1];
-  if (head < 0 || head >= a.num_blocks || count < 0 || count > a.num_blocks) {
-    if (tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
-    head = count = 0;
-  }
+  const int32_t ring0 = a.ring[0], ring1 = a.ring[1];
+  const bool ring_ok = ring0 >= 0 && ring0 < a.num_blocks && ring1 >= 0 && ring1 <= a.num_blocks;
+  if (!ring_ok && tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
+  const int head = ring_ok ? ring0 : 0, count = ring_ok ? ring1 : 0;     // (a bad ring has nothing to take)
   if (tid == 0) s_taken = 0;
 
   // this thread's requests, a contiguous run of them
@@ -183,8 +182,10 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   }
   taken = s_taken;
   int given = first_old[n];
-  if (static_cast<int64_t>(count) + given > a.num_blocks) {     // more blocks than there are: nothing goes back
-    if (tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
+  // more blocks than there are, or a bad ring: nothing goes back, and the ended requests keep their blocks and lengths
+  const bool returns = ring_ok && static_cast<int64_t>(count) + given <= a.num_blocks;
+  if (!returns) {
+    if (given > 0 && tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
     given = 0;
   }
   const int64_t worker = static_cast<int64_t>(rank) * kSlotThreads + tid;
@@ -195,14 +196,14 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   };
 
   if (worker == 0) {
-    const int64_t h = ring_at(taken);
-    a.ring_out[0] = static_cast<int32_t>(h);
-    a.ring_out[1] = count - taken + given;
+    // (a bad ring stays as it is, so that the next call reports it again)
+    a.ring_out[0] = ring_ok ? static_cast<int32_t>(ring_at(taken)) : ring0;
+    a.ring_out[1] = ring_ok ? count - taken + given : ring1;
   }
   for (int64_t b = worker; b < n; b += workers) {
     // (by its own new tokens: the prefix sums stop at 2^31 - 1, which a refused request's new length may reach)
     const int c = ctx[b], more = a.add[b];
-    a.seq[b] = c < 0 ? ~c : more < 0 ? 0 : c + more;
+    a.seq[b] = c < 0 ? ~c : more >= 0 ? c + more : returns ? 0 : c;
     if (a.start) a.start[b] = first_tok[b];
   }
   if (worker == 0 && a.start) a.start[n] = first_tok[n];

@@ -56,9 +56,11 @@ extern "C" {
  * takes no block, the device error word is set -- when its length is negative
  * or does not fit its table row, or when the free blocks run out before it
  * (all later requests that need a block are then refused too).  A block id
- * outside [0, num_blocks) sets the error word and gives slot -1.  More packed
- * tokens than `tokens`, a ring state out of range or one that would hold more
- * than num_blocks sets it too; the excess is not written.
+ * outside [0, num_blocks) sets the error word and gives slot -1.  A ring state
+ * out of range sets it, is passed on to ring_out as it is, and has no free block;
+ * with one, or where the ring would come to hold more than num_blocks, nothing is
+ * given back: ended requests that hold blocks are refused.  More packed tokens than `tokens`
+ * set the error word too; the excess is not written.
  * Requires batch <= 8192, block_size >= 1, num_blocks * block_size < 2^31.
  * batch == 0 enqueues nothing and writes nothing.
  */

@@ -17,16 +17,21 @@ class Pool:
 
 def paged_slots(ctx, new, table, free_ring, ring, block_size):
     """One step: every request in turn takes the blocks its new tokens need from
-    the front of the ring; then the ended ones' blocks go behind its end.
+    the front of the ring; then the ended ones' blocks go behind its end.  A ring
+    state out of range stays as it is, nothing taken and nothing given back; where
+    more would go back than there are blocks, nothing does.
     Returns (pool, seq_lens, slots, pos, start, refused)."""
     p = Pool(table, free_ring, ring)
     n, width = p.free_ring.size, p.table.shape[1]
     seq, slots, pos, start, refused = [], [], [], [0], []
-    left, taken, dry = p.count, 0, False
+    ring_ok = 0 <= p.head < n and 0 <= p.count <= n
+    back = sum(-(-int(h) // block_size) for h, m in zip(ctx, new) if m < 0 and 0 <= h <= width * block_size)
+    returns = ring_ok and p.count + back <= n
+    left, taken, dry = p.count if ring_ok else 0, 0, False
     for b, (have, more) in enumerate(zip(ctx, new)):
         have, more = int(have), int(more)
         need = -(-(have + max(more, 0)) // block_size) - -(-have // block_size)
-        bad = have < 0 or have + max(more, 0) > width * block_size
+        bad = have < 0 or have + max(more, 0) > width * block_size or (more < 0 < have and not returns)
         if not bad and need > 0 and (dry or need > left):
             bad = dry = True
         refused.append(bad)
@@ -47,7 +52,8 @@ def paged_slots(ctx, new, table, free_ring, ring, block_size):
             for j in range(-(-int(have) // block_size)):
                 p.free_ring[tail % n] = p.table[b, j]
                 tail += 1
-    p.head, p.count = (p.head + taken) % n, tail - p.head - taken
+    if ring_ok:
+        p.head, p.count = (p.head + taken) % n, tail - p.head - taken
     return p, np.array(seq), np.array(slots, int), np.array(pos, int), np.array(start), np.array(refused)
 
 

@@ -26,6 +26,19 @@ def test_slots_pool_runs_out_in_request_order():
     assert (slots[8:] == -1).all() and (p.head, p.count) == (2, 1)
 
 
+def test_slots_of_a_bad_ring_or_too_many_blocks():
+    """Nothing is taken or given back; who needs neither goes on."""
+    table = np.array([[0, 1], [2, -1], [3, -1]])
+    for ring in ([-1, 2], [6, 1], [0, -1], [0, 7], [0, 5]):
+        p, seq, slots, _, _, refused = decode.paged_slots([5, 4, 1], [-1, 1, 1], table, [4, 5, 0, 0, 0, 0], ring, 4)
+        dry = ring != [0, 5]                               # five are free, and two more would go back to a ring of six
+        assert refused.tolist() == [True, dry, False] and seq.tolist() == [5, 4 if dry else 5, 2]
+        assert slots.tolist() == [-1 if dry else 16, 13] and p.free_ring.tolist() == [4, 5, 0, 0, 0, 0]
+        assert [p.head, p.count] == (ring if dry else [1, 4])
+    p, seq, _, _, _, refused = decode.paged_slots([5, 4, 1], [-1, 0, 1], table, [4, 5, 0, 0, 0, 0], [0, 4], 4)
+    assert seq.tolist() == [0, 4, 2] and not refused.any() and (p.head, p.count) == (0, 6)
+
+
 def test_attention_closed_forms():
     rng = np.random.default_rng(0)
     k, v = rng.normal(size=(12, 2, 8)), rng.normal(size=(12, 2, 8))

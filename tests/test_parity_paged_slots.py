@@ -206,3 +206,28 @@ def test_a_length_that_fills_the_sums(gbf, batch, tokens, in_place):
     assert np.array_equal(got["pos"], np.concatenate([pos[:1], np.arange(tokens - 1)]))
     assert got["start"][:2].tolist() == [0, 1] and (got["start"][3:] == 2 ** 31 - 1).all()
     assert gbf.device_status()[0] == gbf.EDEVICE
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("prompts", [0, 20])
+@pytest.mark.parametrize("state", ["head -1", "head n", "count -2", "count n + 1", "too many"])
+def test_a_bad_ring_stays_as_it_is(gbf, state, prompts, in_place):
+    """Nothing is taken from it or given back to it: the free ids are all there, ended requests keep their blocks and
+    lengths, and a later call reports it again.  So too where more would go back than there are blocks."""
+    c = case(np.random.default_rng(9), 40, 16, 200, prompts=prompts, ended=5)
+    n = c["free"].size
+    c["ring"][:] = {"head -1": [-1, 2], "head n": [n, 2], "count -2": [0, -2], "count n + 1": [0, n + 1],
+                    "too many": [3, n]}[state]
+    c["free"][:] = np.arange(n)
+    ended = c["new"] < 0
+    assert (c["ctx"][ended] > 0).any()
+    for _ in range(2):
+        got = run(gbf, c, in_place=in_place)
+        refused = check(c, got)
+        assert refused[ended & (c["ctx"] > 0)].all() and np.array_equal(got["free"], c["free"])
+        assert np.array_equal(got["seq"][ended], c["ctx"][ended])
+        if state != "too many":
+            assert got["ring"].tolist() == c["ring"].tolist()
+        s, msg = gbf.device_status()
+        assert s == gbf.EDEVICE and "pool" in msg
+        c = {**c, "ring": got["ring"].copy() if state != "too many" else c["ring"]}
