@@ -75,11 +75,24 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = a.block_size;
   const int64_t room = static_cast<int64_t>(a.max_blocks) * bs;
-  const int32_t ring0 = a.ring[0], ring1 = a.ring[1];
-  const bool ring_ok = ring0 >= 0 && ring0 < a.num_blocks && ring1 >= 0 && ring1 <= a.num_blocks;
-  if (!ring_ok && tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
-  const int head = ring_ok ? ring0 : 0, count = ring_ok ? ring1 : 0;     // (a bad ring has nothing to take)
+  int head = a.ring[0], count = a.ring[1];
+  if (head < 0 || head >= a.num_blocks || count < 0 || count > a.num_blocks) {
+    if (tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
+    head = 0;
+    count = -1;                                  // a bad ring: nothing to take
+  }
   if (tid == 0) s_taken = 0;
+
+  unsigned rank = 0, ranks = 1;                  // (the cluster is the whole grid)
+  if (SHARE != kAlone) {
+    rank = blockIdx.x;
+    ranks = gridDim.x;
+  }
+  const int64_t worker = static_cast<int64_t>(rank) * kSlotThreads + tid;
+  const int64_t workers = static_cast<int64_t>(ranks) * kSlotThreads;
+  // for seq: asked for here, so that its write does not wait for it (0.1 us of 4; with eight requests per thread the
+  // register costs as much)
+  int added = PER == 2 && worker < n ? a.add[worker] : 0;
 
   // this thread's requests, a contiguous run of them
   const int per = (n + kSlotThreads - 1) / kSlotThreads;
@@ -167,29 +180,16 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   }
   // every read of ctx, add and ring is done
   if (taken > 0) atomicMax(&s_taken, taken);
-  unsigned rank = 0, ranks = 1;
-  if (SHARE == kCluster) {
-    cg::cluster_group cluster = cg::this_cluster();
-    rank = cluster.block_rank();
-    ranks = cluster.num_blocks();
-    cluster.sync();
-  } else {
-    if (SHARE == kGrid) {
-      rank = blockIdx.x;
-      ranks = gridDim.x;
-    }
-    __syncthreads();
-  }
+  if (SHARE == kCluster) cg::this_cluster().sync();
+  else __syncthreads();
   taken = s_taken;
   int given = first_old[n];
   // more blocks than there are, or a bad ring: nothing goes back, and the ended requests keep their blocks and lengths
-  const bool returns = ring_ok && static_cast<int64_t>(count) + given <= a.num_blocks;
+  const bool returns = count >= 0 && static_cast<int64_t>(count) + given <= a.num_blocks;
   if (!returns) {
     if (given > 0 && tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
     given = 0;
   }
-  const int64_t worker = static_cast<int64_t>(rank) * kSlotThreads + tid;
-  const int64_t workers = static_cast<int64_t>(ranks) * kSlotThreads;
   auto ring_at = [&](int64_t i) {               // i < 2 * num_blocks
     const int64_t j = head + i;
     return j >= a.num_blocks ? (j - a.num_blocks >= a.num_blocks ? j - 2LL * a.num_blocks : j - a.num_blocks) : j;
@@ -197,13 +197,14 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
 
   if (worker == 0) {
     // (a bad ring stays as it is, so that the next call reports it again)
-    a.ring_out[0] = ring_ok ? static_cast<int32_t>(ring_at(taken)) : ring0;
-    a.ring_out[1] = ring_ok ? count - taken + given : ring1;
+    a.ring_out[0] = count < 0 ? a.ring[0] : static_cast<int32_t>(ring_at(taken));
+    a.ring_out[1] = count < 0 ? a.ring[1] : count - taken + given;
   }
   for (int64_t b = worker; b < n; b += workers) {
     // (by its own new tokens: the prefix sums stop at 2^31 - 1, which a refused request's new length may reach)
-    const int c = ctx[b], more = a.add[b];
-    a.seq[b] = c < 0 ? ~c : more >= 0 ? c + more : returns ? 0 : c;
+    const int c = ctx[b];
+    if (PER != 2 || b != worker) added = a.add[b];
+    a.seq[b] = c < 0 ? ~c : added >= 0 ? c + added : returns ? 0 : c;
     if (a.start) a.start[b] = first_tok[b];
   }
   if (worker == 0 && a.start) a.start[n] = first_tok[n];
