@@ -55,7 +55,8 @@ extern "C" {
  * A request is refused -- its slots are -1, its seq_lens entry stays ctx, it
  * takes no block, the device error word is set -- when its length is negative
  * or does not fit its table row, or when the free blocks run out before it
- * (all later requests that need a block are then refused too).  A block id
+ * (all later requests that need a block are then refused too).  A ctx that is itself
+ * out of range gives the nearest length that is not: 0, or max_blocks * block_size.  A block id
  * outside [0, num_blocks) sets the error word and gives slot -1.  A ring state
  * out of range sets it, is passed on to ring_out as it is, and has no free block;
  * with one, or where the ring would come to hold more than num_blocks, nothing is

@@ -231,3 +231,17 @@ def test_a_bad_ring_stays_as_it_is(gbf, state, prompts, in_place):
         s, msg = gbf.device_status()
         assert s == gbf.EDEVICE and "pool" in msg
         c = {**c, "ring": got["ring"].copy() if state != "too many" else c["ring"]}
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_cached_length_out_of_range_is_clamped(gbf, in_place):
+    """Below 0 it counts as 0, above its table row as all of the row; the request is refused, ended or not."""
+    c = case(np.random.default_rng(10), 12, 16, 100)
+    room = c["table"].shape[1] * 16
+    c["ctx"][[1, 4, 7, 9]], c["new"][[1, 4, 7, 9]] = [-1, -2 ** 31, room + 1, 2 ** 31 - 1], [1, -1, -1, 2]
+    c["tokens"] = int(np.maximum(c["new"], 0).sum())
+    got = run(gbf, c, in_place=in_place)
+    assert check(c, got)[[1, 4, 7, 9]].all()
+    assert got["seq"][[1, 4, 7, 9]].tolist() == [0, 0, room, room]
+    s, msg = gbf.device_status()
+    assert s == gbf.EDEVICE and "length" in msg
