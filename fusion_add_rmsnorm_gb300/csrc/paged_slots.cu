@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
     const int j = ceil_div(ctx[b], bs) + static_cast<int>(i) - first_new[b];
     a.table[b * a.table_stride + j] = a.free_ring[ring_at(i)];
   }
-  // blocks given back
+  // blocks given back (a bad id too: leaving it out would move all behind it, which CTAs that do not wait for one another
+  // cannot agree on; the tokens of whoever takes it get slot -1)
   for (int64_t i = worker; i < given; i += workers) {
     const int b = find_last(first_old, n, static_cast<int>(i));
     const int32_t id = a.table[b * a.table_stride + (i - first_old[b])];

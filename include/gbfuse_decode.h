@@ -57,7 +57,9 @@ extern "C" {
  * or does not fit its table row, or when the free blocks run out before it
  * (all later requests that need a block are then refused too).  A ctx that is itself
  * out of range gives the nearest length that is not: 0, or max_blocks * block_size.  A block id
- * outside [0, num_blocks) sets the error word and gives slot -1.  A ring state
+ * outside [0, num_blocks) sets the error word and gives slot -1; an ended request's goes
+ * back into the ring as it is, and sets the error word again, with slot -1, for whoever
+ * takes it from there (ids are looked at where they are used, not sought out).  A ring state
  * out of range sets it, is passed on to ring_out as it is, and has no free block;
  * with one, or where the ring would come to hold more than num_blocks, nothing is
  * given back: ended requests that hold blocks are refused.  More packed tokens than `tokens`

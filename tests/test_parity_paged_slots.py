@@ -245,3 +245,32 @@ def test_a_cached_length_out_of_range_is_clamped(gbf, in_place):
     assert got["seq"][[1, 4, 7, 9]].tolist() == [0, 0, room, room]
     s, msg = gbf.device_status()
     assert s == gbf.EDEVICE and "length" in msg
+
+
+@pytest.mark.parametrize("prompts", [0, 20])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+def test_a_bad_id_that_goes_back(gbf, bad, in_place, prompts):
+    """An ended request's bad id is reported and keeps its place in the ring; the request that takes it gets slot -1 for
+    its tokens there, reported again, and everyone else their blocks."""
+    c = case(np.random.default_rng(12), 30, 16, 100, prompts=prompts, ended=1, spare=0)
+    b = int(np.flatnonzero(c["new"] < 0)[0])
+    if c["ctx"][b] == 0:
+        c["ctx"][b] = 5
+    c["table"][b, 0] = bad
+    got = run(gbf, c, in_place=in_place)
+    check(c, got)
+    s, msg = gbf.device_status()
+    assert s == gbf.EDEVICE and "block id" in msg
+    head, count = got["ring"]
+    assert count == -(-int(c["ctx"][b]) // 16) and got["free"][head] == bad          # all others are taken
+    new = np.zeros(30, np.int32)
+    new[b] = 16 * count
+    again = {**c, "ctx": got["seq"], "new": new, "table": got["table"], "free": got["free"], "ring": got["ring"],
+             "tokens": int(new.sum())}
+    out = run(gbf, again, in_place=in_place)
+    assert gbf.device_status()[0] == gbf.EDEVICE
+    assert (out["slots"][:16] == -1).all() and (out["slots"][16:again["tokens"]] >= 0).all()
+    ids = got["free"][(head + 1 + np.arange(count - 1)) % got["free"].size]
+    assert np.array_equal(out["slots"][16:again["tokens"]], (ids[:, None] * 16 + np.arange(16)).ravel())
+    assert np.array_equal(out["seq"], got["seq"] + new) and out["ring"][1] == 0
