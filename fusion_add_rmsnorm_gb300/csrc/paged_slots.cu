@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
 #pragma unroll
     for (int i = 0; i < kRow; ++i) {
       slot[i] = pos[i] = -1;
-      const int t = static_cast<int>(t0) + i;
-      if (t >= tokens) continue;
+      if (t0 + i >= tokens) continue;
+      const int t = static_cast<int>(t0 + i);
       while (first_tok[b + 1] <= t) ++b;                 // (requests without tokens are passed over)
       const int c = ctx[b];
       const int64_t p = static_cast<int64_t>(c < 0 ? ~c : c) + (t - first_tok[b]);
@@ -270,7 +270,7 @@ cudaError_t launch(const PagedSlotsArgs& a, size_t smem, cudaStream_t stream) {
   constexpr int most = (4 * THREADS * PER + 3) * static_cast<int>(sizeof(int));
   const cudaError_t e = allow_smem<paged_slots_kernel<THREADS, PER, SHARE>>(most);
   if (e != cudaSuccess) return e;
-  const int fill = (a.tokens + 4 * THREADS - 1) / (4 * THREADS);
+  const int fill = static_cast<int>((static_cast<int64_t>(a.tokens) + 4 * THREADS - 1) / (4 * THREADS));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(SHARE == kAlone ? 1 : SHARE == kCluster ? kSlotsCluster : fill < kSlotsGrid ? fill : kSlotsGrid);
   cfg.blockDim = dim3(THREADS);

@@ -274,3 +274,28 @@ def test_a_bad_id_that_goes_back(gbf, bad, in_place, prompts):
     ids = got["free"][(head + 1 + np.arange(count - 1)) % got["free"].size]
     assert np.array_equal(out["slots"][16:again["tokens"]], (ids[:, None] * 16 + np.arange(16)).ravel())
     assert np.array_equal(out["seq"], got["seq"] + new) and out["ring"][1] == 0
+
+
+@pytest.mark.parametrize("more", [3, 1000])
+def test_rows_for_two_to_the_31_tokens(gbf, more):
+    """The longest slots and pos there may be (8.6 GB each), few of their entries used: the rest keep their values."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    slots, pos = (torch.full((2 ** 31 - 1,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    c = case(np.random.default_rng(more), 40, 16, 100)
+    c["new"][3] = more
+    c["table"] = np.pad(c["table"], ((0, 0), (0, 80)), constant_values=-3)
+    c["free"] = np.pad(c["free"], (0, 100), constant_values=-4)
+    held = np.unique(c["table"][c["table"] >= 0])
+    spare = np.setdiff1d(np.arange(c["free"].size), held).astype(np.int32)
+    c["free"][:spare.size], c["ring"][:] = spare, [0, spare.size]
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()      # noqa: E731
+    table, seq, ring_out = d(c["table"]), d(np.zeros_like(c["ctx"])), d(np.zeros_like(c["ring"]))
+    gbf.paged_slots(d(c["ctx"]), d(c["new"]), table, d(c["free"]), d(c["ring"]), 16, seq, ring_out, slots, pos)
+    torch.cuda.synchronize()
+    p, want, s, q, _, refused = decode.paged_slots(c["ctx"], c["new"], c["table"], c["free"], c["ring"], 16)
+    assert not refused.any() and np.array_equal(seq.cpu().numpy(), want) and np.array_equal(table.cpu().numpy(), p.table)
+    assert np.array_equal(slots[:s.size].cpu().numpy(), s) and np.array_equal(pos[:s.size].cpu().numpy(), q)
+    assert bool((slots[s.size:s.size + 4096] == -9).all()) and bool((slots[-4096:] == -9).all())
+    assert bool((pos[s.size:s.size + 4096] == -9).all()) and bool((pos[-4096:] == -9).all())
+    assert gbf.device_status()[0] == gbf.OK
