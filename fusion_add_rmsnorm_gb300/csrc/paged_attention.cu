@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < NW; ++w) top = fmaxf(top, sm_m[parity][w][g + 8 * h]);
-      const float f = top == -INFINITY ? 0.0f : exp2_approx(m[h] - top);
+      // (a NaN score is in the sums but not in the maximum, so that with no other score that is -inf still)
+      const float f = exp2_approx(m[h] - (top == -INFINITY ? 0.0f : top));
       float* dst = joined + (warp * 8 + g) * join_stride<DP>() + t4 * 2;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(Plan<DP>::kWarps * 32, Plan<DP>::kPerSm)
           acc.y += v.y;
           acc.z += v.z;
           acc.w += v.w;
-          if (big != -INFINITY) total += sm_l[parity][w][row] * exp2_approx(sm_m[parity][w][row] - big);
+          total += sm_l[parity][w][row] * exp2_approx(sm_m[parity][w][row] - (big == -INFINITY ? 0.0f : big));
         }
         if (TOGETHER) {
           *reinterpret_cast<float4*>(cta_o + row * DP + c) = acc;
@@ -801,26 +802,24 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAt
   for (int i = 0; i < PARTS; ++i) top = fmaxf(top, m_s[i]);
   float4 out = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
-  if (top != -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-      const float f = exp2_approx(m_s[i] - top);
-      const float4 v = acc_s[i][col];
-      total += l_s[i] * f;
-      out.x += v.x * f;
-      out.y += v.y * f;
-      out.z += v.z * f;
-      out.w += v.w * f;
-    }
-    const float inv = 1.0f / total;
-    out.x *= inv;
-    out.y *= inv;
-    out.z *= inv;
-    out.w *= inv;
+  for (int i = 0; i < PARTS; ++i) {
+    const float f = exp2_approx(m_s[i] - (top == -INFINITY ? 0.0f : top));
+    const float4 v = acc_s[i][col];
+    total += l_s[i] * f;
+    out.x += v.x * f;
+    out.y += v.y * f;
+    out.z += v.z * f;
+    out.w += v.w * f;
   }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  out.x *= inv;
+  out.y *= inv;
+  out.z *= inv;
+  out.w *= inv;
   const int64_t q_row = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(head) * a.group + row0 + row;
   store_out4(a, q_row * a.d + col * 4, out);
-  if (col == 0 && a.lse) a.lse[q_row] = top == -INFINITY ? -INFINITY : (top + log2f(total)) * kLn2;
+  if (col == 0 && a.lse) a.lse[q_row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 template <int DP, bool WIDE>

@@ -78,7 +78,9 @@ GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, i
  * lse = ln sum_j exp(s_j), for j in [0, len) or, with window > 0, the last
  * `window` of them (len counts the new token, whose K and V are in the cache).
  * Query head h reads KV head h / (n_q_heads / n_kv_heads).  A request of
- * length 0 gives out = 0 and lse = -inf.  Float32 scores, sums and outputs.
+ * length 0 gives out = 0 and lse = -inf, and so does one with no score above -inf; a
+ * score that is NaN or +inf gives out = lse = NaN, an infinite value in V an out that is
+ * not finite.  Float32 scores, sums and outputs.
  *
  * q: device bf16 [batch, n_q_heads, head_dim]; k_cache, v_cache: device bf16
  * [cache_rows, n_kv_heads, head_dim]; block_table: device int32, batch rows of

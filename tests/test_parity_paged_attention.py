@@ -327,3 +327,47 @@ def test_bad_ids_and_lengths_in_either_split(gbf, width):
         assert np.array_equal(out[b], good[b]) and np.array_equal(lse[b], good_lse[b])
     y = formats.bf16_decode(out)
     assert np.isfinite(y).all() and (y[3] == 0).all() and np.isneginf(lse[3]).all() and np.isfinite(lse[1]).all()
+
+
+# A score that is not a number shows in its head's output however the call is split; scores of -inf alone are no tokens.
+
+@pytest.mark.parametrize("lens,width", [([40, 5, 9], None), ([300, 900, 77], None), ([3000, 2500], None), ([60] * 200, None),
+                                        ([40, 5, 200, 700, 5000], WIDE), ([5000], WIDE)])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 24, 2), (256, 5, 1), (128, 40, 1)])
+@pytest.mark.parametrize("out_scale", [None, 0.01])
+def test_a_query_that_is_nan(gbf, lens, width, d, hq, hkv, out_scale):
+    c = case(lens, hq, hkv, d, 16, seed=len(lens), width=width)
+    good, good_lse = run(gbf, c, out_scale=out_scale)
+    gone = np.zeros((len(lens), hq), bool)
+    gone[::2, hq // 2], gone[-1, 0] = True, True
+    q = c["q"].copy()
+    q[gone, d // 3] = 0x7FC0
+    out, lse = run(gbf, dict(c, q=q), out_scale=out_scale)
+    assert (out[gone] & 0x7F == 0x7F).all() if out_scale else np.isnan(formats.bf16_decode(out[gone])).all()
+    assert np.isnan(lse[gone]).all()
+    assert np.array_equal(out[~gone], good[~gone]) and np.array_equal(lse[~gone], good_lse[~gone])
+    assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("lens,width", [([40, 5, 9], None), ([300, 900, 77], None), ([60] * 200, None),
+                                        ([40, 5, 200, 700, 5000], WIDE), ([5000, 3], WIDE)])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 24, 2), (256, 5, 1)])
+def test_keys_that_are_not_finite(gbf, lens, width, d, hq, hkv):
+    c = case(lens, hq, hkv, d, 16, seed=len(lens), width=width)
+    c["q"] &= 0x7FFF                                       # all above 0: a key of -inf gives a score of -inf
+    good, good_lse = run(gbf, c)
+    rows = lambda b, j: c["table"][b, j // 16] * 16 + j % 16                # noqa: E731
+    k, group = c["k"].copy(), hq // hkv
+    for b, n in enumerate(lens):
+        k[rows(b, np.arange(n)), 0, 1] = 0xFF80            # -inf throughout, in KV head 0
+    out, lse = run(gbf, dict(c, k=k))
+    y = formats.bf16_decode(out)
+    assert (y[:, :group] == 0).all() and np.isneginf(lse[:, :group]).all()
+    assert np.array_equal(out[:, group:], good[:, group:]) and np.array_equal(lse[:, group:], good_lse[:, group:])
+    k = c["k"].copy()
+    for b, n in enumerate(lens):
+        k[rows(b, np.array([n // 2])), hkv - 1, 1] = 0x7FC0                 # one NaN key, in the last KV head
+    out, lse = run(gbf, dict(c, k=k))
+    assert np.isnan(formats.bf16_decode(out[:, -group:])).all() and np.isnan(lse[:, -group:]).all()
+    assert np.array_equal(out[:, :-group], good[:, :-group]) and np.array_equal(lse[:, :-group], good_lse[:, :-group])
+    assert gbf.device_status()[0] == gbf.OK
