@@ -207,7 +207,9 @@ GBF_DEVICE void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_de
 // Launch `kernel` with programmatic stream serialisation: its CTAs may be
 // scheduled while the previous kernel in the stream is finishing, and they
 // wait for that kernel (completion and memory) in pdl_wait(), which every
-// kernel launched this way calls before its first global memory access.
+// kernel launched this way calls before its first global memory access, but
+// for paged_attention's join, which reads the request lengths ahead of it: the
+// reason why that is in order stands there.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args... args) {

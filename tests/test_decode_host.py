@@ -189,3 +189,17 @@ def test_clusters_have_started_before_they_write_to_each_other():
     arrive, wait = kernel.find("cluster.barrier_arrive();"), kernel.find("cluster.barrier_wait();")
     first = min(kernel.index(f"s.{f}(") for f in ("exchange", "offer", "of", "find_bins", "close_lists"))
     assert 0 <= arrive < kernel.index("pdl_wait();") < wait < first
+
+
+def test_the_join_starts_behind_the_lengths():
+    """paged_attention's join reads the lengths before its own wait.  That holds as long as every CTA of the kernel in
+    front waits first of all and lets the join begin only then, and the join reads them from L2."""
+    text = open(os.path.join(ROOT, "fusion_add_rmsnorm_gb300", "csrc", "paged_attention.cu")).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    main = text[text.index("    paged_attention_kernel(const PagedAttnArgs a) {"):]
+    wait, begin = main.index("pdl_wait();"), main.index("pdl_launch_dependents();")
+    assert wait < begin < min(main.index(s) for s in ("return", "a.lens", "a.table", "locate<"))
+    join = text[text.index("paged_attention_join_kernel(const PagedAttnArgs a) {"):]
+    early = join[:join.index("  pdl_wait();\n")]
+    assert "locate<128, true>(" in early and "request_of<true>(" in early
+    assert not re.search(r"a\.(lens|ws|table|q|k|v|out|lse)\b", early)

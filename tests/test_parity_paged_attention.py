@@ -371,3 +371,34 @@ def test_keys_that_are_not_finite(gbf, lens, width, d, hq, hkv):
     assert np.isnan(formats.bf16_decode(out[:, -group:])).all() and np.isnan(lse[:, -group:]).all()
     assert np.array_equal(out[:, :-group], good[:, :-group]) and np.array_equal(lse[:, :-group], good_lse[:, :-group])
     assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("batch,new", [(40, 1), (40, 150), (600, 3)])
+def test_lengths_written_by_the_call_before(gbf, batch, new):
+    """Step after step without a pause, lengths growing in place: the kernel, and the join behind it, see those of
+    their own step, whatever an SM held of the last one."""
+    steps, block = 12, 16
+    c = case([steps * new + 40] * batch, 8, 2, 128, block, seed=batch, width=WIDE)
+    start = torch.from_numpy(np.random.default_rng(new).integers(1, 40, batch).astype(np.int32)).cuda()
+    q, k, v, table = from_bits(c["q"]), from_bits(c["k"]), from_bits(c["v"]), dev(c["table"])
+    add = torch.full((batch,), new, dtype=torch.int32, device="cuda")
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")      # noqa: E731
+    lens, slots, pos, ws = start.clone(), i32(batch * new), i32(batch * new), workspace(gbf, c)
+    # the table has every block already: what paged_slots would enter goes to one of its own
+    spare, free, ring = i32(batch, WIDE), torch.arange(40000, dtype=torch.int32, device="cuda"), dev(np.array([0, 40000], np.int32))
+    outs = torch.zeros(steps, *q.shape, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(steps, *q.shape[:2], device="cuda")
+    torch.cuda.synchronize()
+    for i in range(steps):
+        gbf.paged_slots(lens, add, spare, free, ring, block, lens, ring, slots, pos)
+        gbf.paged_attention(q, k, v, table, lens, block, outs[i], ws, lse=lse[i])
+    torch.cuda.synchronize()
+    assert torch.equal(lens, start + steps * new)
+    out, l = torch.empty_like(q), torch.empty_like(lse[0])
+    for i in range(steps):
+        at = start + (i + 1) * new
+        torch.cuda.synchronize()
+        gbf.paged_attention(q, k, v, table, at, block, out, ws, lse=l)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), outs[i].view(torch.int16)) and torch.equal(l, lse[i]), i
+    assert gbf.device_status()[0] == gbf.OK
