@@ -496,7 +496,8 @@ GBF_API int gbfd_paged_attention(const void* q, const void* k_cache, const void*
   if (head_dim % 16 != 0 || head_dim > 256)
     return fail(GBF_EUNSUPPORTED, "%s: head_dim (%d) must be a multiple of 16 and <= 256", fn, head_dim);
   if (n_q_heads > 4096) return fail(GBF_EUNSUPPORTED, "%s: too many heads", fn);
-  if (cache_rows >= lim || max_blocks >= lim || batch * n_q_heads >= lim || batch >= lim)
+  if (batch > (1LL << 30)) return fail(GBF_EUNSUPPORTED, "%s: batch (%lld) > 2^30", fn, (long long)batch);
+  if (cache_rows >= lim || max_blocks >= lim || batch * n_q_heads >= lim)
     return fail(GBF_EUNSUPPORTED, "%s: cache_rows, max_blocks and batch * n_q_heads must be below 2^31", fn);
   if (batch == 0) return ok();
   if (!q || !seq_lens || !out || !workspace || (max_blocks && !block_table) || (cache_rows && (!k_cache || !v_cache)))

@@ -190,7 +190,7 @@ GBF_DEVICE Place locate(const PagedAttnArgs& a, int64_t c, bool report) {
   __shared__ Place place;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = a.hkv * a.chunks;
-  const int per = (a.batch + NT - 1) / NT;
+  const int per = (a.batch + NT - 1) / NT;       // (up to 2^30 requests: in 32 bits)
   const int b0 = tid * per < a.batch ? tid * per : a.batch;
   const int b1 = b0 + per < a.batch ? b0 + per : a.batch;
   int64_t mine = 0;

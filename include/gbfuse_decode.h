@@ -95,7 +95,7 @@ GBF_API int gbfd_paged_slots(const int32_t* ctx_lens, const int32_t* new_lens, i
  * whose block id lies outside the cache is left out; both set the device error
  * word.  Rows of the cache no position refers to are not read.
  * Requires head_dim % 16 == 0, head_dim <= 256, n_q_heads % n_kv_heads == 0,
- * cache_rows < 2^31, 16-byte aligned q, k_cache, v_cache, out, workspace; scale
+ * cache_rows < 2^31, batch <= 2^30, 16-byte aligned q, k_cache, v_cache, out, workspace; scale
  * > 0 and finite.  batch == 0 enqueues nothing.  out and lse may not overlap each other or an input.
  * How the work is split follows from batch, heads, window and max_blocks * block_size, not from the lengths, which only
  * the device knows: for few or short requests, a max_blocks (or a window) no wider than they need saves 2 to 8 us.

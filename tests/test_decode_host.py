@@ -203,3 +203,15 @@ def test_the_join_starts_behind_the_lengths():
     early = join[:join.index("  pdl_wait();\n")]
     assert "locate<128, true>(" in early and "request_of<true>(" in early
     assert not re.search(r"a\.(lens|ws|table|q|k|v|out|lse)\b", early)
+
+
+def test_paged_attention_batches_the_split_can_count(gbf):
+    """The scan over the lengths counts requests in 32 bits and steps past the end of them: 2^30 at most."""
+    names = lambda: [("q", A(0)), ("k", A(100)), ("v", A(200)), ("rows", 256), ("table", A(300)), ("stride", 1),   # noqa
+                     ("width", 1), ("bs", 16), ("lens", A(400)), ("batch", 4), ("hq", 1), ("hkv", 1), ("d", 16),
+                     ("scale", 0.1), ("window", 0), ("out", A(500)), ("out_scale", 0.0), ("lse", None), ("ws", A(600)),
+                     ("ws_bytes", 0), ("stream", None)]
+    f = lambda **k: call(gbf.raw().gbfd_paged_attention, names(), k)                              # noqa: E731
+    for batch in ((1 << 30) + 1, (1 << 31) - 1, 1 << 31, 1 << 62):
+        assert f(batch=batch) == gbf.EUNSUPPORTED and "2^30" in last(gbf), batch
+    assert f(batch=1 << 30) == gbf.EINVAL and "workspace" in last(gbf)
