@@ -5,7 +5,9 @@ Each CUDA translation unit under csrc/ is compiled to an object in parallel,
 then linked into fusion_add_rmsnorm_gb300/libgbfuse.so with the CUDA runtime
 linked statically (the library loads without a GPU driver; kernels need one).
 Objects go to fusion_add_rmsnorm_gb300/_build/ (git-ignored).  A source whose
-object is newer than the source and every header is not recompiled.
+object is newer than the source and every header is not recompiled.  The library
+needs neither torch nor Python's headers: it is linked before the binding is
+looked at, and `--no-binding` leaves the binding out.
 binding/decode_binding.cpp (the wrappers of the decode-step calls) becomes
 fusion_add_rmsnorm_gb300/decode_binding.so against the installed torch.
 """
@@ -49,7 +51,7 @@ def _stale(src, obj, hdr_mtime):
     return t < os.path.getmtime(src) or t < hdr_mtime
 
 
-def build(verbose=False, extra_flags=()):
+def build(verbose=False, extra_flags=(), binding=True):
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -67,11 +69,10 @@ def build(verbose=False, extra_flags=()):
         return r.stderr if verbose else None
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        binding = ex.submit(compile_binding, hdr_mtime)
+        binding_obj = ex.submit(compile_binding, hdr_mtime) if binding else None
         for out in ex.map(compile_one, zip(srcs, objs)):
             if out:
                 sys.stderr.write(out)
-        binding_obj = binding.result()
     if not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         tmp = LIB + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -79,13 +80,17 @@ def build(verbose=False, extra_flags=()):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    link_binding(binding_obj)
+    if binding:
+        link_binding(binding_obj.result())
     return LIB
 
 
 def _torch_dir():
     # found, not imported: the paths are all that is needed
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the binding needs torch (--no-binding builds the library alone)")
+    return os.path.dirname(spec.origin)
 
 
 def _run(cmd, what):
@@ -118,4 +123,4 @@ def link_binding(obj):
 if __name__ == "__main__":
     v = "-v" in sys.argv
     extra = ("-Xptxas", "-v") if v else ()
-    print(build(verbose=v, extra_flags=extra))
+    print(build(verbose=v, extra_flags=extra, binding="--no-binding" not in sys.argv))
