@@ -11,7 +11,8 @@ torch tensor of the element type the call reads, on the current device.
 There is no CPU path: importing this package fails when the compiled library
 is missing, and every call fails without a CUDA device.  The wrappers of the
 decode-step calls (paged_slots, paged_attention, sample_tokens) are compiled,
-because those calls are about as short as their checks would be in Python.
+because those calls are about as short as their checks would be in Python;
+where that extension is missing, they alone raise ImportError when called.
 
 Build the library with `python -c "import __graft_entry__ as g; g.build()"`
 (or `python fusion_add_rmsnorm_gb300/build.py`).
@@ -79,11 +80,21 @@ class GbfError(RuntimeError):
         self.status = status
 
 
-# the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
-from . import decode_binding as _decode     # noqa: E402
-from .decode_binding import paged_attention, paged_slots, sample_tokens     # noqa: E402, F401
+def _missing(name, why):
+    def call(*_, **__):
+        raise ImportError(f"{name}: the compiled wrappers cannot be used ({why}); run fusion_add_rmsnorm_gb300/build.py")
+    call.__name__ = call.__qualname__ = name
+    return call
 
-_decode.set_error(GbfError)
+
+# the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
+try:
+    from . import decode_binding as _decode     # noqa: E402
+    _decode.set_error(GbfError)
+    paged_slots, paged_attention, sample_tokens = _decode.paged_slots, _decode.paged_attention, _decode.sample_tokens
+except ImportError as _e:
+    paged_slots, paged_attention, sample_tokens = (_missing(_n, _e)
+                                                   for _n in ("paged_slots", "paged_attention", "sample_tokens"))
 
 
 def _check(status):

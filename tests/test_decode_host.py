@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -215,3 +216,44 @@ def test_paged_attention_batches_the_split_can_count(gbf):
     for batch in ((1 << 30) + 1, (1 << 31) - 1, 1 << 31, 1 << 62):
         assert f(batch=batch) == gbf.EUNSUPPORTED and "2^30" in last(gbf), batch
     assert f(batch=1 << 30) == gbf.EINVAL and "workspace" in last(gbf)
+
+
+def copy_of_the_package(tmp_path, *built):
+    here = tmp_path / "fusion_add_rmsnorm_gb300"
+    here.mkdir()
+    for name in ("__init__.py", "libgbfuse.so", *built):
+        (here / name).symlink_to(os.path.join(ROOT, "fusion_add_rmsnorm_gb300", name))
+    return str(tmp_path)
+
+
+WITHOUT = """
+import torch
+import fusion_add_rmsnorm_gb300 as gbf
+assert gbf.__file__.startswith({path!r}), gbf.__file__
+assert gbf.version() > 0 and gbf.paged_attention_workspace(8, 2, 64) > 0
+f = lambda *s: torch.zeros(*s)
+try:
+    gbf.bn_fold(f(4, 8), f(4), f(4), f(4), f(4), f(4), 1e-5, f(4, 8), f(4))
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise SystemExit("bn_fold ran on the CPU")
+for name in ("paged_slots", "paged_attention", "sample_tokens"):
+    try:
+        getattr(gbf, name)(1, stream=None)
+    except ImportError as e:
+        assert name in str(e) and "build.py" in str(e) and {why!r} in str(e), e
+    else:
+        raise SystemExit(name + " was there")
+"""
+
+
+def run_python(path, code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=path, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": path})
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_without_the_extension_the_other_operators_are_there(tmp_path):
+    path = copy_of_the_package(tmp_path)
+    run_python(path, WITHOUT.format(path=path, why="decode_binding"))
