@@ -12,7 +12,8 @@ There is no CPU path: importing this package fails when the compiled library
 is missing, and every call fails without a CUDA device.  The wrappers of the
 decode-step calls (paged_slots, paged_attention, sample_tokens) are compiled,
 because those calls are about as short as their checks would be in Python;
-where that extension is missing, they alone raise ImportError when called.
+where that extension is missing, or was built for another torch, they alone
+raise ImportError when called.
 
 Build the library with `python -c "import __graft_entry__ as g; g.build()"`
 (or `python fusion_add_rmsnorm_gb300/build.py`).
@@ -90,6 +91,8 @@ def _missing(name, why):
 # the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
 try:
     from . import decode_binding as _decode     # noqa: E402
+    if _decode.built_for_torch != torch.__version__:
+        raise ImportError(f"built for torch {_decode.built_for_torch}, this is torch {torch.__version__}")
     _decode.set_error(GbfError)
     paged_slots, paged_attention, sample_tokens = _decode.paged_slots, _decode.paged_attention, _decode.sample_tokens
 except ImportError as _e:

@@ -305,4 +305,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "decode_binding", "Decode-step entr
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_decode_binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit_decode_binding() {
+  PyObject* m = PyModule_Create(&module);
+  // torch's C++ interfaces change from version to version: the package looks at this before it uses anything here
+  if (m && PyModule_AddStringConstant(m, "built_for_torch", GBF_BUILT_FOR_TORCH) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -9,12 +9,14 @@ object is newer than the source and every header is not recompiled.  The library
 needs neither torch nor Python's headers: it is linked before the binding is
 looked at, and `--no-binding` leaves the binding out.
 binding/decode_binding.cpp (the wrappers of the decode-step calls) becomes
-fusion_add_rmsnorm_gb300/decode_binding.so against the installed torch.
+fusion_add_rmsnorm_gb300/decode_binding<tag of this Python>.so against the
+installed torch, whose version it carries; another Python or torch builds it anew.
 """
 import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -26,7 +28,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgbfuse.so")
 BINDING_SRC = os.path.join(HERE, "binding", "decode_binding.cpp")
-BINDING = os.path.join(HERE, "decode_binding.so")
+TAG = sysconfig.get_config_var("EXT_SUFFIX")              # .cpython-<version>-<platform>.so
+BINDING = os.path.join(HERE, "decode_binding" + TAG)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
@@ -99,14 +102,26 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _torch_version():
+    return runpy.run_path(os.path.join(_torch_dir(), "version.py"))["__version__"]
+
+
 def compile_binding(hdr_mtime):
-    obj = os.path.join(BUILD, "decode_binding.o")
-    torch_mtime = os.path.getmtime(os.path.join(_torch_dir(), "version.py"))     # another torch is another ABI
-    if _stale(BINDING_SRC, obj, max(hdr_mtime, torch_mtime)):
+    version = _torch_version()
+    obj = os.path.join(BUILD, "decode_binding" + os.path.splitext(TAG)[0] + ".o")
+    built_for = obj[:-2] + ".torch"                        # torch version of the object
+    if os.path.exists(built_for):
+        with open(built_for) as f:
+            same = f.read() == version
+    else:
+        same = False
+    if not same or _stale(BINDING_SRC, obj, hdr_mtime):
         cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
         inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(_torch_dir(), "include"), cuda]
-        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{p}" for p in inc], "-c", BINDING_SRC,
-              "-o", obj], "g++ on decode_binding.cpp")
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DGBF_BUILT_FOR_TORCH="{version}"',
+              *[f"-I{p}" for p in inc], "-c", BINDING_SRC, "-o", obj], "g++ on decode_binding.cpp")
+        with open(built_for, "w") as f:
+            f.write(version)
     return obj
 
 
@@ -118,6 +133,9 @@ def link_binding(obj):
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{lib}", "-ltorch_python", "-lc10", "-lc10_cuda", "-ltorch_cpu", f"-L{HERE}",
           "-l:libgbfuse.so", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"], "link of decode_binding.so")
     os.replace(tmp, BINDING)
+    untagged = os.path.join(os.path.dirname(BINDING), "decode_binding.so")   # as older builds left it, for any Python to import
+    if os.path.exists(untagged):
+        os.remove(untagged)
 
 
 if __name__ == "__main__":

@@ -45,3 +45,26 @@ def test_without_torch_the_binding_says_so(build, monkeypatch):
     with pytest.raises(RuntimeError, match="needs torch"):
         build.build()
     assert os.path.exists(build.LIB)
+
+
+def test_another_torch_builds_the_binding_anew(build, monkeypatch, tmp_path):
+    ran = []
+
+    def run(cmd, what):
+        ran.append((what, cmd))
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(build, "_run", run)
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    (tmp_path / "decode_binding.so").touch()               # an untagged one of an older build
+    open(build.LIB, "w").close()
+    version = build._torch_version()
+    for v, compiles in ((version, True), (version, False), ("9.9.9", True), ("9.9.9", False), (version, True)):
+        monkeypatch.setattr(build, "_torch_version", lambda: v)
+        ran.clear()
+        obj = build.compile_binding(0)
+        assert [w for w, _ in ran] == (["g++ on decode_binding.cpp"] if compiles else [])
+        assert not compiles or f'-DGBF_BUILT_FOR_TORCH="{v}"' in ran[0][1]
+    build.link_binding(obj)
+    assert not (tmp_path / "decode_binding.so").exists()
+    assert build.BINDING.endswith(build.TAG) and "cpython" in build.TAG

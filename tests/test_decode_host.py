@@ -257,3 +257,12 @@ def run_python(path, code):
 def test_without_the_extension_the_other_operators_are_there(tmp_path):
     path = copy_of_the_package(tmp_path)
     run_python(path, WITHOUT.format(path=path, why="decode_binding"))
+
+
+def test_the_extension_names_its_python_and_torch(gbf, tmp_path):
+    import sysconfig
+    name = "decode_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+    assert os.path.basename(gbf._decode.__file__) == name and gbf._decode.built_for_torch == torch.__version__
+    path = copy_of_the_package(tmp_path, name)
+    other = "import torch; torch.__version__ = '1.0.other'\n" + WITHOUT.format(path=path, why="this is torch 1.0.other")
+    run_python(path, other)
