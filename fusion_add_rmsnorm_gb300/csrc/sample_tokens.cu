@@ -82,9 +82,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 4096;
 constexpr float kBinsPerOctave = 128.0f;    // 32 octaves; what is smaller shares the last bin
 constexpr int kCells = kBins / 2;           // mass histogram in the same memory: low words, then high words
-// With top-p alone an element adds 2^20 and its place in the bin, so that a bin's mass is known to 2^(1/16384) + 4e-6
-// (46 ppm), as long as no more than 4095 elements of a CTA fall in it (otherwise the border turns out to lie outside the
-// bins searched, and all are).  Those of the last bin (weights below 2^-31.9) add vocab 2^-31.9 of the total at most.
+// With top-p alone an element adds 2^20 and its place in the bin, so that a bin's mass is known to 50 ppm: 42.3 for half a
+// place (2^(1/16384)), 3.7 for the weight taken as linear within the bin, 4 for the places' own rounding (3 2^-24 of up to
+// 2^18).  Behind that come the exponential (0.24 ppm), the products (0.24), 26 float32 additions on the way to a running
+// sum (1.6) and the target's products (0.2): 52.3 in all, taken as 60.  It holds as long as no more than 4095 elements of
+// a CTA fall in a bin (otherwise the border turns out to lie outside the bins searched, and all are).  Those of the last bin (weights below 2^-31.9) add vocab 2^-31.9 of the total at most.
 constexpr float kBinError = 60e-6f, kLastBinError = 2.6e-10f;
 constexpr int kList = 1024;                 // candidates that are sorted, an equal share of each rank's
 constexpr int kGroup = 64;                  // bins per group (and groups): the two steps of a search over the bins
@@ -527,8 +529,8 @@ struct Sampler {
   // The bins in which the running sum over bins 0, 1, ... and all ranks reaches
   // two targets: by groups of 64 bins, then the bins of the groups they lie
   // in, read from every rank's histogram.  value(h, j): of bin j that holds h.
-  // Float32 sums: exact for counts (at most 2^20), and 2^-19 for masses that are
-  // known to 0.3 %.  One cluster barrier, and another has to pass before a rank
+  // Float32 sums: exact for counts (at most 2^20), and good to 2^-19 for masses
+  // (a part of kBinError).  One cluster barrier, and another has to pass before a rank
   // writes to its histogram again or ends.
   template <typename Value, typename Targets>
   GBF_DEVICE void find_bins(Value value, Targets targets, Hit out[2]) {
