@@ -19,8 +19,8 @@
 // own; one cluster of eight, with a barrier between the last read of ctx and
 // ring and the first write, when one of them is updated in place.
 //
-// Measured (device time, back to back): 32 decode rows 3.9 us, of which a launch
-// alone is some 2; 300 rows beside 24 prompts, 50,000 tokens, 7.3 us (14.0 in
+// Measured (device time, back to back): 32 decode rows 3.7 us, of which a launch
+// alone is some 2; 300 rows beside 24 prompts, 50,000 tokens, 7.3 us (14.8 in
 // place, 202 on one CTA).
 #include "common.cuh"
 #include "decode.h"
@@ -90,9 +90,6 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   }
   const int64_t worker = static_cast<int64_t>(rank) * kSlotThreads + tid;
   const int64_t workers = static_cast<int64_t>(ranks) * kSlotThreads;
-  // for seq: asked for here, so that its write does not wait for it (0.1 us of 4; with eight requests per thread the
-  // register costs as much)
-  int added = PER == 2 && worker < n ? a.add[worker] : 0;
 
   // this thread's requests, a contiguous run of them
   const int per = (n + kSlotThreads - 1) / kSlotThreads;
@@ -200,11 +197,12 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
     a.ring_out[0] = count < 0 ? a.ring[0] : static_cast<int32_t>(ring_at(taken));
     a.ring_out[1] = count < 0 ? a.ring[1] : count - taken + given;
   }
-  for (int64_t b = worker; b < n; b += workers) {
+  // (by the workers that have the fewest tokens, which would wait for the read of add: 0.2 us of 3.8, 0.3 in place; of CTAs
+  // that do not wait for one another, by those that start first: 0.3 of 6.4)
+  for (int64_t b = SHARE == kGrid ? worker : workers - 1 - worker; b < n; b += workers) {
     // (by its own new tokens: the prefix sums stop at 2^31 - 1, which a refused request's new length may reach)
-    const int c = ctx[b];
-    if (PER != 2 || b != worker) added = a.add[b];
-    a.seq[b] = c < 0 ? ~c : added >= 0 ? c + added : returns ? 0 : c;
+    const int c = ctx[b], more = a.add[b];
+    a.seq[b] = c < 0 ? ~c : more >= 0 ? c + more : returns ? 0 : c;
     if (a.start) a.start[b] = first_tok[b];
   }
   if (worker == 0 && a.start) a.start[n] = first_tok[n];
