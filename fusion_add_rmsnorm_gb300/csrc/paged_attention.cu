@@ -4,9 +4,11 @@
 //   s_j = scale q . k_j  for the cached positions j in [max(0, len - window), len)
 //   out = sum_j softmax(s)_j v_j,   lse = ln sum_j exp(s_j)
 //
-// The query heads of one KV head (a group) share its K and V, so each is read
-// once: per token and KV head 4 d bytes for 4 d group flops, which leaves HBM
-// as the bound for any group of up to some hundred heads.
+// The query heads of one KV head (a group) share its K and V, so up to 16 of them
+// read each once: per token and KV head 4 d bytes for 4 d group flops, far on HBM's
+// side.  A larger group is cut into row tiles of 16 heads, items of their own, each
+// of which reads K and V again, from L2 at best: 32 requests of 4096 on one KV head
+// of 128 (67 MB) take 12.1 us with 8 heads, 14.2 with 16, 28.7 with 32 and 42.3 with 64.
 //
 // Work split: the unit is a tile of 16 cached tokens of one (request, KV head)
 // item, and kOwn units per item for what an item costs by itself.  All
@@ -38,8 +40,9 @@
 // from another (lengths, table, rows: 3.5 us of the 36 to 50 us of a batch), behind it the join.  Device time, back to
 // back: 32 requests up to 4096, 32 heads on 8 of 128, 49 us (277 MB: 5.6 TB/s); 256 such requests 326 us (2.16 GB: 6.6
 // TB/s); two documents of 131072 on 8 KV heads 126 us (806 MB: 6.4 TB/s); 48 requests on one KV head of 256, window 4096,
-// 35.8 us (158 MB: 4.4 TB/s); one request of 700 tokens 5.1 us (a launch,
-// and reads that wait for one another).
+// 35.8 us (158 MB: 4.4 TB/s; at that width the loop takes 255 registers and spills 184 bytes, with one warp per scheduler);
+// one request of 700 tokens 5.5 us (a launch, and reads that wait for one another) behind a table of up to 4096 tokens, 8.1
+// behind a wider one, which is split over the GPU.
 //
 // Rounding: scores, maxima, sums and outputs are float32.  P enters the second
 // product as a pair of bf16 (value and remainder, 2^-17 together), because one

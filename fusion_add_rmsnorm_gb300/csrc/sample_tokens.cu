@@ -55,10 +55,10 @@
 // instructions per 32 elements (9 for pass 1, some 12 for the histogram, 55 for the
 // weights, the rest for the border and the draw) at 2.5 a cycle and SM, and a
 // cluster passes five barriers with an exchange behind each, 1 to 2 us apiece.
-// Measured (device time, back to back): one row of 32000 bf16, nucleus, 17.6 us (temperature alone 8.4);
-// 32 rows of 151936, mixed requests, 36.7 us (10 MB: 0.26 TB/s); 61 rows of 50257,
-// temperature alone, 15.1 us; 256 rows of 128000 float32, nucleus, 182 us (131 MB:
-// 0.72 TB/s).
+// Measured (device time, back to back): one row of 32000 bf16, nucleus, 17.7 us (temperature alone 8.0);
+// 32 rows of 151936, mixed requests, 36.6 us (10 MB: 0.26 TB/s); 61 rows of 50257,
+// temperature alone, 15.1 us; 256 rows of 128000 float32, nucleus, 177 us (131 MB:
+// 0.74 TB/s).
 //
 // Ranks hand each other totals by remote stores into boxes (read locally behind
 // the next barrier).
