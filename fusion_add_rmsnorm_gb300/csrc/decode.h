@@ -114,7 +114,9 @@ struct PagedSlotsArgs {
   int64_t table_stride;
   int32_t num_blocks, tokens;
   int batch, max_blocks, block_size;
-  int wide;                 // slots and pos are 16-byte aligned (set by the launcher)
+  // set by the launcher
+  int wide;                 // slots and pos are 16-byte aligned
+  int room;                 // longest length of a table row: few and large blocks may hold more tokens than an int32 can say
 };
 
 cudaError_t launch_paged_slots(PagedSlotsArgs a, cudaStream_t stream);

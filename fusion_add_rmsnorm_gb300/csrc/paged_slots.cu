@@ -40,7 +40,7 @@ constexpr int kSlotsSmall = 512;
 // shared, 8.1 alone; 32 rows 3.9 alone, 5.3 shared.
 constexpr int kAlonePerThread = 2;
 
-GBF_DEVICE int clamp31(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : static_cast<int>(v); }
+__host__ GBF_DEVICE int clamp31(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : static_cast<int>(v); }
 
 // The last index i in [0, n) with first[i] <= x, for a non-decreasing `first`.
 GBF_DEVICE int find_last(const int* first, int n, int x) {
@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = a.block_size;
-  const int64_t room = static_cast<int64_t>(a.max_blocks) * bs;
   int head = a.ring[0], count = a.ring[1];
   if (head < 0 || head >= a.num_blocks || count < 0 || count > a.num_blocks) {
     if (tid == 0) raise_error(a.err, DEV_ERR_BLOCK_POOL);
@@ -104,13 +103,13 @@ __global__ void __launch_bounds__(THREADS) paged_slots_kernel(const PagedSlotsAr
     int len = a.ctx[b];
     const int more = a.add[b];
     bool refuse = false;
-    if (len < 0 || len > room) {
+    if (len < 0 || len > a.room) {
       raise_error(a.err, DEV_ERR_BLOCK_RANGE);
-      len = len < 0 ? 0 : static_cast<int>(room);
+      len = len < 0 ? 0 : a.room;
       refuse = true;
     }
     fresh[i] = more > 0 ? more : 0;
-    if (static_cast<int64_t>(len) + fresh[i] > room) {
+    if (fresh[i] > a.room - len) {
       raise_error(a.err, DEV_ERR_BLOCK_RANGE);
       refuse = true;
     }
@@ -290,6 +289,7 @@ cudaError_t launch(const PagedSlotsArgs& a, size_t smem, cudaStream_t stream) {
 
 cudaError_t launch_paged_slots(PagedSlotsArgs a, cudaStream_t stream) {
   const size_t smem = (4 * static_cast<size_t>(a.batch) + 3) * sizeof(int);
+  a.room = clamp31(static_cast<int64_t>(a.max_blocks) * a.block_size);
   a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
   const bool in_place = a.seq == a.ctx || a.ring_out == a.ring, small = a.batch <= kSlotsSmall;
   if (a.tokens <= kAlonePerThread * (small ? 256 : 1024))

@@ -54,7 +54,7 @@ extern "C" {
  *
  * A request is refused -- its slots are -1, its seq_lens entry stays ctx, it
  * takes no block, the device error word is set -- when its length is negative
- * or does not fit its table row, or when the free blocks run out before it
+ * or does not fit its table row (or int32), or when the free blocks run out before it
  * (all later requests that need a block are then refused too).  A ctx that is itself
  * out of range gives the nearest length that is not: 0, or max_blocks * block_size.  A block id
  * outside [0, num_blocks) sets the error word and gives slot -1; an ended request's goes

@@ -23,19 +23,20 @@ def paged_slots(ctx, new, table, free_ring, ring, block_size):
     Returns (pool, seq_lens, slots, pos, start, refused)."""
     p = Pool(table, free_ring, ring)
     n, width = p.free_ring.size, p.table.shape[1]
+    room = min(width * block_size, 2 ** 31 - 1)            # lengths are int32
     seq, slots, pos, start, refused = [], [], [], [0], []
     ring_ok = 0 <= p.head < n and 0 <= p.count <= n
-    back = sum(-(-int(h) // block_size) for h, m in zip(ctx, new) if m < 0 and 0 <= h <= width * block_size)
+    back = sum(-(-int(h) // block_size) for h, m in zip(ctx, new) if m < 0 and 0 <= h <= room)
     returns = ring_ok and p.count + back <= n
     left, taken, dry = p.count if ring_ok else 0, 0, False
     for b, (have, more) in enumerate(zip(ctx, new)):
         have, more = int(have), int(more)
         need = -(-(have + max(more, 0)) // block_size) - -(-have // block_size)
-        bad = have < 0 or have + max(more, 0) > width * block_size or (more < 0 < have and not returns)
+        bad = have < 0 or have + max(more, 0) > room or (more < 0 < have and not returns)
         if not bad and need > 0 and (dry or need > left):
             bad = dry = True
         refused.append(bad)
-        have = min(max(have, 0), width * block_size)
+        have = min(max(have, 0), room)
         if not bad:
             for j in range(need):
                 p.table[b, -(-have // block_size) + j] = p.free_ring[(p.head + taken) % n]

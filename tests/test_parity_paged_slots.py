@@ -299,3 +299,16 @@ def test_rows_for_two_to_the_31_tokens(gbf, more):
     assert bool((slots[s.size:s.size + 4096] == -9).all()) and bool((slots[-4096:] == -9).all())
     assert bool((pos[s.size:s.size + 4096] == -9).all()) and bool((pos[-4096:] == -9).all())
     assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_lengths_at_the_end_of_int32(gbf, in_place):
+    """Blocks so large that a table row has room for more tokens than a length can say."""
+    top = 2 ** 31 - 1
+    c = dict(ctx=np.array([top, top - 1, top - 5, 0, top], np.int32), new=np.array([1, 1, 6, 2, -1], np.int32),
+             table=np.zeros((5, 3), np.int32), free=np.zeros(1, np.int32), ring=np.array([0, 1], np.int32), block=1 << 30,
+             tokens=10)
+    got = run(gbf, c, in_place=in_place)
+    refused = check(c, got)
+    assert refused.tolist() == [True, False, True, False, True] and got["seq"].tolist() == [top, top, top - 5, 2, top]
+    assert gbf.device_status()[0] == gbf.EDEVICE
