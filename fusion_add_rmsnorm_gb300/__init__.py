@@ -91,12 +91,13 @@ def _missing(name, why):
 # the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
 try:
     from . import decode_binding as _decode     # noqa: E402
-    if _decode.built_for_torch != torch.__version__:
-        raise ImportError(f"built for torch {_decode.built_for_torch}, this is torch {torch.__version__}")
+    _built_for = getattr(_decode, "built_for_torch", "of an unknown version")
+    if _built_for != torch.__version__:
+        raise ImportError(f"built for torch {_built_for}, this is torch {torch.__version__}")
     _decode.set_error(GbfError)
     paged_slots, paged_attention, sample_tokens = _decode.paged_slots, _decode.paged_attention, _decode.sample_tokens
 except ImportError as _e:
-    paged_slots, paged_attention, sample_tokens = (_missing(_n, _e)
+    paged_slots, paged_attention, sample_tokens = (_missing(_n, str(_e))
                                                    for _n in ("paged_slots", "paged_attention", "sample_tokens"))
 
 

@@ -266,3 +266,10 @@ def test_the_extension_names_its_python_and_torch(gbf, tmp_path):
     path = copy_of_the_package(tmp_path, name)
     other = "import torch; torch.__version__ = '1.0.other'\n" + WITHOUT.format(path=path, why="this is torch 1.0.other")
     run_python(path, other)
+
+
+def test_an_extension_that_names_no_torch_is_not_used(tmp_path):
+    """As builds before the version was noted left it."""
+    path = copy_of_the_package(tmp_path)
+    (tmp_path / "fusion_add_rmsnorm_gb300" / "decode_binding.py").write_text("paged_slots = print\n")
+    run_python(path, WITHOUT.format(path=path, why="unknown version"))
