@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           hit);
       if (by_k) {
         listed = hit[0].at >= 0 && hit[0].upto <= kList;
-        from = fmaxf(s.logit_of(64 * hit[0].at + 128), floor_k);
+        if (hit[0].at < kBins - 1) from = fmaxf(s.logit_of(64 * hit[0].at + 128), floor_k);    // (the last bin has no end)
         p1 = 64 * hit[0].at + 63;
       } else {
         b0 = hit[0].at < 0 ? kBins - 1 : hit[0].at;

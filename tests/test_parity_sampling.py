@@ -330,3 +330,28 @@ def test_short_rows_on_clusters(gbf, batch, f32):
         check(l, u, (tokens[0], lp[0]), **p)
         assert (tokens == tokens[0]).all() and (lp.view(np.int32) == lp[0].view(np.int32)).all()
     assert gbf.device_status()[0] == gbf.OK
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("batch", [1, 20, 44, 120])
+@pytest.mark.parametrize("k,vocab", [(3, 801), (75, 801), (300, 801), (700, 801), (900, 2001), (1500, 2001)])
+def test_top_k_keeps_candidates_of_next_to_no_weight(gbf, k, vocab, batch, f32):
+    """One strong candidate, the others 2^-32 of it and less, beyond the last bin with a lower end: top-k keeps as many
+    of them as it says, and a uniform next to 1 draws one of them.  As many as fit one list, and more."""
+    rng = np.random.default_rng(k + batch)
+    l = -22.2 - 3.0 * rng.random((batch, vocab)) ** 2
+    l[:, 0] = 0.0
+    l = l.astype(np.float32) if f32 else torch.from_numpy(l).to(torch.bfloat16).float().numpy()
+    u, top_k = np.full(batch, np.float32(1 - 2.0 ** -24)), np.full(batch, k, np.int32)
+    u[::3] = 0.5
+    kept = np.minimum(np.exp(np.sort(l.astype(np.float64), axis=1)[:, ::-1]), 1)[:, 1:k].sum(1)
+    tokens, lp = run(gbf, l, u, f32, top_k=top_k)
+    # the kept mass beside the first candidate's: weights to 2^-36 or half a unit of 2^-43, the logarithm to float32
+    first = tokens == 0
+    assert first[::3].all()
+    assert (np.abs(lp + np.log1p(kept))[first] <= 2.0 ** -22 * kept[first] + k * 2.0 ** -44).all()
+    behind = (1 - 2.0 ** -24) * (1 + kept) - 1             # how far u times the kept mass lies behind the first candidate's
+    sure = (np.arange(batch) % 3 != 0) & (np.abs(behind) > 1e-9)
+    assert np.array_equal(first[sure], behind[sure] < 0)
+    rank = (l > np.take_along_axis(l, tokens[:, None], 1)).sum(1)
+    assert (rank < k).all() and (k < 700 or not first[sure].any())
