@@ -3,17 +3,18 @@
 Argument marshalling only.  Every function takes torch tensors that live on
 the current CUDA device, derives the extents from them, passes their data
 pointers and sizes to the C-ABI entry point of the same name (see
-include/gbfuse.h and include/gbfuse_decode.h) on the current torch stream, and raises GbfError on a
-non-zero status.  A raw pointer carries no size, so before the call each
+include/gbfuse.h, include/gbfuse_decode.h and include/gbfuse_block.h) on the current
+torch stream, and raises GbfError on a non-zero status.  A raw pointer carries no size, so before the call each
 wrapper checks what the C library cannot: every operand holds exactly the
 elements the call will read or write (ValueError otherwise), is a contiguous
 torch tensor of the element type the call reads, on the current device.
 There is no CPU path: importing this package fails when the compiled library
 is missing, and every call fails without a CUDA device.  The wrappers of the
-decode-step calls (paged_slots, paged_attention, sample_tokens) are compiled,
-because those calls are about as short as their checks would be in Python;
-where that extension is missing, or was built for another torch, they alone
-raise ImportError when called.
+decode-step calls (paged_slots, paged_attention, sample_tokens) and of the
+block-scaled ones (add_rmsnorm_fp8_block, gated_act_fp8_block,
+quantize_fp8_block, linear_fp8_block) are compiled, because those calls are about
+as short as their checks would be in Python; where that extension is missing, or
+was built for another torch, they alone raise ImportError when called.
 
 Build the library with `python -c "import __graft_entry__ as g; g.build()"`
 (or `python fusion_add_rmsnorm_gb300/build.py`).
@@ -65,14 +66,22 @@ _SIGNATURES_DECODE = {
     "gbfd_paged_attention_workspace": [_i32, _i32, _i32],
     "gbfd_sample_tokens": [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p],
 }
+# the block-scaled 8-bit operators: include/gbfuse_block.h
+_SIGNATURES_BLOCK = {
+    "gbfb_add_rmsnorm_fp8": [_p, _p, _p, _p, _i32, _p, _p, _p, _p, _p, _i64, _i64, _f, _p],
+    "gbfb_gated_act_fp8": [_p, _p, _p, _i64, _i64, _i32, _p],
+    "gbfb_quantize_fp8": [_p, _p, _p, _i64, _i64, _i32, _p],
+    "gbfb_linear_fp8": [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p],
+}
 _RESTYPES = {"gbf_last_error": ctypes.c_char_p, "gbfd_paged_attention_workspace": _i64}
-for _name, _args in {**_SIGNATURES, **_SIGNATURES_DECODE}.items():
+for _name, _args in {**_SIGNATURES, **_SIGNATURES_DECODE, **_SIGNATURES_BLOCK}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _RESTYPES.get(_name, ctypes.c_int)
 
 EXPORTED = tuple(_SIGNATURES)
 EXPORTED_DECODE = tuple(_SIGNATURES_DECODE)
+EXPORTED_BLOCK = tuple(_SIGNATURES_BLOCK)
 
 
 class GbfError(RuntimeError):
@@ -88,17 +97,20 @@ def _missing(name, why):
     return call
 
 
-# the wrappers of the decode-step calls, compiled (binding/decode_binding.cpp): the same checks as below
+# the compiled wrappers (binding/decode_binding.cpp), with the same checks as below
+_COMPILED = ("paged_slots", "paged_attention", "sample_tokens", "add_rmsnorm_fp8_block", "gated_act_fp8_block",
+             "quantize_fp8_block", "linear_fp8_block")
 try:
     from . import decode_binding as _decode     # noqa: E402
     _built_for = getattr(_decode, "built_for_torch", "of an unknown version")
     if _built_for != torch.__version__:
         raise ImportError(f"built for torch {_built_for}, this is torch {torch.__version__}")
     _decode.set_error(GbfError)
-    paged_slots, paged_attention, sample_tokens = _decode.paged_slots, _decode.paged_attention, _decode.sample_tokens
-except ImportError as _e:
-    paged_slots, paged_attention, sample_tokens = (_missing(_n, str(_e))
-                                                   for _n in ("paged_slots", "paged_attention", "sample_tokens"))
+    _calls = [getattr(_decode, _n) for _n in _COMPILED]
+except (ImportError, AttributeError) as _e:      # AttributeError: an extension from before a call was added
+    _calls = [_missing(_n, str(_e)) for _n in _COMPILED]
+(paged_slots, paged_attention, sample_tokens, add_rmsnorm_fp8_block, gated_act_fp8_block, quantize_fp8_block,
+ linear_fp8_block) = _calls
 
 
 def _check(status):

@@ -8,7 +8,7 @@ Objects go to fusion_add_rmsnorm_gb300/_build/ (git-ignored).  A source whose
 object is newer than the source and every header is not recompiled.  The library
 needs neither torch nor Python's headers: it is linked before the binding is
 looked at, and `--no-binding` leaves the binding out.
-binding/decode_binding.cpp (the wrappers of the decode-step calls) becomes
+binding/decode_binding.cpp (the wrappers of the decode-step and block-scaled calls) becomes
 fusion_add_rmsnorm_gb300/decode_binding<tag of this Python>.so against the
 installed torch, whose version it carries; another Python or torch builds it anew.
 """
@@ -44,7 +44,7 @@ def nvcc():
 
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h"))
+        glob.glob(os.path.join(ROOT, "include", "*.h")) + glob.glob(os.path.join(HERE, "binding", "*.h"))
 
 
 def _stale(src, obj, hdr_mtime):

@@ -13,7 +13,9 @@
 #include <mutex>
 
 #include "gbfuse.h"
+#include "gbfuse_block.h"
 #include "gbfuse_decode.h"
+#include "block.h"
 #include "common.cuh"
 #include "decode.h"
 #include "kernels.h"
@@ -580,6 +582,161 @@ GBF_API int gbfd_sample_tokens(const void* logits, int f32, int64_t batch, int64
   a.vocab = static_cast<int>(vocab);
   a.f32 = f32;
   return launch_status(gbf::launch_sample_tokens(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+// ------------------------------------------------ block-scaled 8-bit operators
+
+namespace {
+
+// Checks of an activation's codes [rows, d] and scales that the three writers share.
+int block_codes(const char* fn, int64_t rows, int64_t d) {
+  if (rows < 0 || d <= 0)
+    return fail(GBF_EINVAL, "%s: rows (%lld) must be >= 0 and the width (%lld) > 0", fn, (long long)rows, (long long)d);
+  if (d % 16 != 0) return fail(GBF_EALIGN, "%s: the width (%lld) must be a multiple of 16", fn, (long long)d);
+  // extents and offsets are int64 bytes
+  if (d >= 1LL << 31 || rows > (1LL << 60) / d)
+    return fail(GBF_EUNSUPPORTED, "%s: the width must be below 2^31 and the tensor below 2^60 elements", fn);
+  return GBF_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int quant_entry(const char* fn, const void* x, uint8_t* q_out, float* scales, int64_t rows, int64_t d, int act,
+                int block_rows, void* stream) {
+  const int bad = block_codes(fn, rows, d);
+  if (bad != GBF_OK) return bad;
+  const int64_t scale_rows = (rows + block_rows - 1) / block_rows, across = gbf::block_count(d);
+  if (block_rows > 1 && scale_rows >= (1LL << 31) / across)
+    return fail(GBF_EUNSUPPORTED, "%s: 2^31 blocks of 128 x 128 or more", fn);
+  if (rows == 0) return ok();
+  if (!x || !q_out || !scales) return fail(GBF_EINVAL, "%s: x, q_out and scales are required", fn);
+  if (!aligned16(x) || !aligned16(q_out)) return fail(GBF_EALIGN, "%s: x and q_out must be 16-byte aligned", fn);
+  if (!aligned4(scales)) return fail(GBF_EALIGN, "%s: scales must be 4-byte aligned", fn);
+  const int64_t xb = rows * d * (act == GBF_ACT_NONE ? 2 : 4), sb = scale_rows * across * 4;
+  if (overlap(q_out, rows * d, x, xb) || overlap(scales, sb, x, xb) || overlap(q_out, rows * d, scales, sb))
+    return fail(GBF_EINVAL, "%s: x, q_out and scales may not overlap", fn);
+  gbf::QuantBlockArgs a = {};
+  a.x = x;
+  a.q_out = q_out;
+  a.scales = scales;
+  a.rows = rows;
+  a.d = d;
+  a.act = act;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch_status(block_rows > 1 ? gbf::launch_quant_tiles(a, s) : gbf::launch_quant_rows(a, s), fn);
+}
+
+}  // namespace
+
+GBF_API int gbfb_add_rmsnorm_fp8(const void* x, const void* res_in, void* res_out, const void* gate, int mode,
+                                 const void* weight, const void* ada_scale, const void* ada_shift, uint8_t* q_out,
+                                 float* scales, int64_t rows, int64_t hidden, float eps, void* stream) {
+  const char* fn = "gbfb_add_rmsnorm_fp8";
+  const int bad = block_codes(fn, rows, hidden);
+  if (bad != GBF_OK) return bad;
+  if (mode != GBF_NORM_WEIGHT && mode != GBF_NORM_NOWEIGHT && mode != GBF_NORM_ADA)
+    return fail(GBF_EINVAL, "%s: unknown norm mode %d", fn, mode);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(GBF_EINVAL, "%s: eps must be finite and >= 0", fn);
+  if (hidden > 32768) return fail(GBF_EUNSUPPORTED, "%s: hidden (%lld) > 32768", fn, (long long)hidden);
+  if (rows == 0) return ok();
+  if (!x || !res_in || !res_out || !q_out || !scales)
+    return fail(GBF_EINVAL, "%s: x, res_in, res_out, q_out, scales are required", fn);
+  if (mode == GBF_NORM_WEIGHT && !weight) return fail(GBF_EINVAL, "%s: weight is required in WEIGHT mode", fn);
+  if (mode == GBF_NORM_ADA && (!ada_scale || !ada_shift))
+    return fail(GBF_EINVAL, "%s: ada_scale and ada_shift are required in ADA mode", fn);
+  if (mode != GBF_NORM_WEIGHT) weight = nullptr;
+  if (mode != GBF_NORM_ADA) ada_scale = ada_shift = nullptr;
+  const int64_t nb = rows * hidden * 2, nv = hidden * 2;
+  const void* ins[] = {x, res_in, gate, weight, ada_scale, ada_shift};
+  const int64_t in_len[] = {nb, nb, nv, nv, nv, nv};
+  const void* outs[] = {res_out, q_out, scales};
+  const int64_t out_len[] = {nb, rows * hidden, rows * gbf::block_count(hidden) * 4};
+  for (const void* p : ins)
+    if (p && !aligned16(p)) return fail(GBF_EALIGN, "%s: every tensor but scales must be 16-byte aligned", fn);
+  if (!aligned16(res_out) || !aligned16(q_out) || !aligned4(scales))
+    return fail(GBF_EALIGN, "%s: res_out and q_out must be 16-byte aligned, scales 4-byte", fn);
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 6; ++j) {
+      if (i == 0 && j == 1 && res_out == res_in) continue;              // the residual stream, updated in place
+      if (overlap(outs[i], out_len[i], ins[j], in_len[j]))
+        return fail(GBF_EINVAL, "%s: an output overlaps an input (only res_out may equal res_in)", fn);
+    }
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], out_len[i], outs[j], out_len[j])) return fail(GBF_EINVAL, "%s: outputs overlap", fn);
+  }
+  gbf::AddRmsNormBlockArgs a = {};
+  a.x = x;
+  a.res_in = res_in;
+  a.res_out = res_out;
+  a.gate = gate;
+  a.weight = weight;
+  a.ada_scale = ada_scale;
+  a.ada_shift = ada_shift;
+  a.q_out = q_out;
+  a.scales = scales;
+  a.rows = rows;
+  a.hidden = hidden;
+  a.eps = eps;
+  a.mode = mode;
+  return launch_status(gbf::launch_add_rmsnorm_block(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+GBF_API int gbfb_gated_act_fp8(const void* x, uint8_t* q_out, float* scales, int64_t rows, int64_t d, int act,
+                               void* stream) {
+  const char* fn = "gbfb_gated_act_fp8";
+  if (act != GBF_ACT_GELU_TANH && act != GBF_ACT_GELU_ERF && act != GBF_ACT_SILU)
+    return fail(GBF_EINVAL, "%s: act must be GELU_TANH, GELU_ERF or SILU (got %d)", fn, act);
+  return quant_entry(fn, x, q_out, scales, rows, d, act, 1, stream);
+}
+
+GBF_API int gbfb_quantize_fp8(const void* x, uint8_t* q_out, float* scales, int64_t rows, int64_t d, int block_rows,
+                              void* stream) {
+  const char* fn = "gbfb_quantize_fp8";
+  if (block_rows != 1 && block_rows != gbf::kBlockCols)
+    return fail(GBF_EINVAL, "%s: block_rows must be 1 or 128 (got %d)", fn, block_rows);
+  return quant_entry(fn, x, q_out, scales, rows, d, GBF_ACT_NONE, block_rows, stream);
+}
+
+GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales,
+                            const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int act, void* stream) {
+  const char* fn = "gbfb_linear_fp8";
+  if (M < 0 || N <= 0 || K <= 0) return fail(GBF_EINVAL, "%s: M >= 0, N > 0, K > 0 required", fn);
+  if (act != GBF_ACT_NONE && act != GBF_ACT_GELU_TANH && act != GBF_ACT_GELU_ERF && act != GBF_ACT_SILU)
+    return fail(GBF_EINVAL, "%s: unknown activation %d", fn, act);
+  if (K % 16 != 0 || N % 8 != 0)
+    return fail(GBF_EUNSUPPORTED, "%s: needs K %% 16 == 0 and N %% 8 == 0 (K=%lld, N=%lld)", fn, (long long)K,
+                (long long)N);
+  // the kernels index rows, columns, tiles and TMA coordinates with int32
+  const int64_t lim = 1LL << 31;
+  if (M >= lim || N >= lim || K >= lim) return fail(GBF_EUNSUPPORTED, "%s: M, N and K must be below 2^31", fn);
+  if (gbf::block_count(M) * gbf::block_count(N) >= lim)
+    return fail(GBF_EUNSUPPORTED, "%s: more than 2^31 - 1 output tiles of 128 x 128", fn);
+  if (M == 0) return ok();
+  if (!Xq || !x_scales || !Wq || !w_scales || !Y)
+    return fail(GBF_EINVAL, "%s: Xq, x_scales, Wq, w_scales, Y are required", fn);
+  if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || (bias && !aligned16(bias)))
+    return fail(GBF_EALIGN, "%s: Xq, Wq, Y, bias must be 16-byte aligned", fn);
+  if (!aligned4(x_scales) || !aligned4(w_scales)) return fail(GBF_EALIGN, "%s: scales must be 4-byte aligned", fn);
+  const int64_t kb = gbf::block_count(K), yb = M * N * 2;
+  if (overlap(Y, yb, Xq, M * K) || overlap(Y, yb, Wq, N * K) || overlap(Y, yb, bias, N * 2) ||
+      overlap(Y, yb, x_scales, M * kb * 4) || overlap(Y, yb, w_scales, gbf::block_count(N) * kb * 4))
+    return fail(GBF_EINVAL, "%s: Y overlaps an input", fn);
+  gbf::LinearBlockArgs a = {};
+  a.x = Xq;
+  a.x_scales = x_scales;
+  a.w = Wq;
+  a.w_scales = w_scales;
+  a.bias = bias;
+  a.y = Y;
+  a.err = error_word();
+  a.m = M;
+  a.n = N;
+  a.k = K;
+  a.act = act;
+  const char* why = nullptr;
+  cudaError_t e = gbf::launch_linear_block(a, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why) return fail(GBF_ELAUNCH, "%s: %s (%s)", fn, why, cudaGetErrorString(e));
+  return launch_status(e, fn);
 }
 
 // ------------------------------------------------------------- copy probe

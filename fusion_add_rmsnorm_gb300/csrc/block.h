@@ -1,0 +1,62 @@
+// Internal interface between the C-ABI layer (abi.cu) and the block-scaled
+// 8-bit operators.  Argument structs are passed to kernels by value.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gbf {
+
+constexpr int kBlockCols = 128;           // columns that share a scale (and rows, in a weight)
+constexpr int64_t block_count(int64_t n) { return (n + kBlockCols - 1) / kBlockCols; }
+
+// ------------------------------------- add + RMSNorm + block-scaled FP8
+struct AddRmsNormBlockArgs {
+  const void* x;
+  const void* res_in;
+  void* res_out;
+  const void* gate;       // nullable
+  const void* weight;     // kNormWeight
+  const void* ada_scale;  // kNormAda
+  const void* ada_shift;  // kNormAda
+  uint8_t* q_out;
+  float* scales;          // [rows, block_count(hidden)]
+  int64_t rows;
+  int64_t hidden;
+  float eps;
+  int mode;
+  int tpr;                // threads per row (set by the launcher)
+};
+
+cudaError_t launch_add_rmsnorm_block(AddRmsNormBlockArgs a, cudaStream_t stream);
+
+// --------------------------- (gated activation or copy) + block-scaled FP8
+struct QuantBlockArgs {
+  const void* x;          // bf16 [rows, d], or [rows, 2d] (gate | up) with an activation
+  uint8_t* q_out;         // [rows, d]
+  float* scales;          // [rows, block_count(d)], or one row for every 128 rows
+  int64_t rows, d;
+  int act;                // kActNone: quantise x itself
+  int64_t step_rows;      // one grid stride, in whole rows and blocks (set by the launcher)
+  int step_blocks;
+};
+
+cudaError_t launch_quant_rows(QuantBlockArgs a, cudaStream_t stream);
+cudaError_t launch_quant_tiles(const QuantBlockArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------- Linear on block-scaled codes
+struct LinearBlockArgs {
+  const uint8_t* x;       // [m, k] E4M3 codes
+  const float* x_scales;  // [m, block_count(k)]
+  const uint8_t* w;       // [n, k] E4M3 codes
+  const float* w_scales;  // [block_count(n), block_count(k)]
+  const void* bias;       // bf16 [n], nullable
+  void* y;                // bf16 [m, n]
+  unsigned int* err;
+  int64_t m, n, k;
+  int act;
+};
+
+cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
+
+}  // namespace gbf

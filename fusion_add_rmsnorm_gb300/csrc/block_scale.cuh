@@ -1,0 +1,52 @@
+// Scales found from the data: one float32 for every 128 columns of a row (or
+// 128 x 128 block of a weight), E4M3 codes of the values over it.
+//
+//   scale = max(amax * RN(1 / 448), 2^-100),  code = e4m3_rne_sat(y * RN(1 / scale))
+//
+// in binary32.  448 is E4M3's largest value, so a block's largest element
+// lands there; 2^-100 keeps the reciprocal finite where a block holds only
+// zeros (or values below 448 * 2^-100).  The maximum passes NaN on: a block
+// that holds one gets scale NaN and NaN codes, one that holds an infinity gets
+// scale infinity, NaN codes at the infinities and zeros elsewhere, so that
+// code * scale is never a finite number that stands for neither.
+#pragma once
+
+#include "block.h"
+#include "common.cuh"
+
+namespace gbf {
+
+constexpr int kSegLanes = 8;              // lanes that hold a block of 128 columns, two 8-column vectors each
+constexpr int kSegVecs = 2;               // lane l has vectors l and l + 8: loads of 128 contiguous bytes
+
+// The larger of two values, NaN if either is.
+GBF_DEVICE float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+GBF_DEVICE float amax8(const float (&v)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+  return m;
+}
+
+// Maximum over the aligned eight lanes of a block; every lane of the warp takes part.
+GBF_DEVICE float seg_max(float m) {
+#pragma unroll
+  for (int o = kSegLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+GBF_DEVICE float scale_of(float amax) { return max_nan(amax * (1.0f / 448.0f), 0x1p-100f); }
+
+// Eight codes of v over the scale whose reciprocal is r.
+GBF_DEVICE uint2 codes8(const float (&v)[8], float r) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
+  return f32x8_to_e4m3x8(q);
+}
+
+}  // namespace gbf
