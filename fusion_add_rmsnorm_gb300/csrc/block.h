@@ -58,5 +58,6 @@ struct LinearBlockArgs {
 };
 
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
+cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
 
 }  // namespace gbf

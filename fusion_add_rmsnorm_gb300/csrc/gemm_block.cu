@@ -186,14 +186,14 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = smem_u32(smem_s) + quarter * 2 * NX * 4;
     constexpr int PER = NX < 32 ? 1 : NX / 32;              // scales a lane fetches
-    float next[PER];
+    float next[PER], w_next;                                // multiplied where they are used: no wait here
     auto fetch = [&](int kb) {
-      const float sw = kb < kb1 ? p.w_scales[static_cast<int64_t>(nt) * p.blocks + kb] : 0.0f;
+      w_next = kb < kb1 ? p.w_scales[static_cast<int64_t>(nt) * p.blocks + kb] : 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int row = m0 + lane + i * 32;
         next[i] = (NX >= 32 || lane < NX) && kb < kb1 && row < p.m
-                      ? p.x_scales[static_cast<int64_t>(row) * p.blocks + kb] * sw
+                      ? p.x_scales[static_cast<int64_t>(row) * p.blocks + kb]
                       : 0.0f;
       }
     };
@@ -205,7 +205,7 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       const uint32_t sc = sbuf + (i & 1) * NX * 4;
 #pragma unroll
       for (int j = 0; j < PER; ++j)
-        if (NX >= 32 || lane < NX) sts32f(sc + (lane + j * 32) * 4, next[j]);
+        if (NX >= 32 || lane < NX) sts32f(sc + (lane + j * 32) * 4, next[j] * w_next);
       fetch(kb0 + i + 1);
       __syncwarp();
       if (!mbar_wait_warp<false>(&ctl->acc_full[b], (i / A) & 1, &ctl->abort, p.err)) break;
@@ -329,6 +329,7 @@ cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, c
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (a.m > 128) return launch_linear_block_pair(a, stream, why);
   LinearBlockParams p = {};
   p.x_scales = a.x_scales;
   p.w_scales = a.w_scales;
