@@ -9,7 +9,7 @@
 // own: either has two accumulators of 128 columns in turn, an issuer and half of
 // the epilogue, so that neither waits for the other.
 //   warp 0      TMA producer: the CTA's 128 X rows and 64 W rows of either half,
-//               a K block at a time, into a six-stage ring
+//               a K block at a time, into a four-stage ring
 //   warps 1-2   one a half.  Even CTA: MMA issuers, four M256 N128 K32 MMAs a K
 //               block (the whole warp walks the loop, which keeps the descriptors
 //               in uniform registers: 25 cycles an MMA, 120 from a lane's own).
@@ -46,14 +46,13 @@ constexpr int kBpThreads = 640;
 constexpr int kBpRows = 128;                    // X rows of a CTA
 constexpr int kBpCols = 256;                    // channels of a pair's tile
 constexpr int kBpHalf = kBpCols / 2;
-constexpr int kBpStages = 6;
+constexpr int kBpStages = 4;
 constexpr int kBpStageBytes = (kBpRows + kBpHalf) * BK_BYTES;
 constexpr int kBpEpilogue = 4;                  // first epilogue warp
 constexpr int kBpEpilogueWarps = 16;
 constexpr int kBpWarpCols = 64;                 // channels of an epilogue warp
 constexpr int kBpMaxSplit = 4;                  // pairs of a portable cluster
-constexpr int kBpBoxRows = 8;                   // a store's box: 8 rows x 64 columns of bf16
-constexpr int kBpBoxBytes = kBpBoxRows * kBpWarpCols * 2;
+constexpr int kBpBoxBytes = 32 * kBpWarpCols * 2;  // an epilogue warp's store: 32 rows x 64 columns of bf16
 // Scales of 16 K blocks, one copy in use and one being filled: X's as
 // [K block][row], two words more a row than needed so that both the filling (16
 // K blocks of two rows) and the reading (32 rows of one) meet every bank once.
@@ -84,6 +83,7 @@ constexpr size_t kBpSmem = 1024 /* alignment */ + kBpStages * kBpStageBytes + kB
                            2 * sizeof(BpScales) + sizeof(BpCtl);
 static_assert(kBpSmem <= 232448, "227 KB a CTA");
 static_assert(kBpRows * kBpCols * 4 <= kBpStages * kBpStageBytes, "partial sums fit the ring");
+static_assert(kBpChunk * kBpRows % 32 == 0 && kBpChunk == 16, "a lane's share of the scales");
 
 struct BlockPairParams {
   const float* x_scales;
@@ -136,6 +136,20 @@ GBF_DEVICE void commit_pair(uint64_t* bar, int rank) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(0x3 << rank))
       : "memory");
+}
+
+// A copy of N bytes to shared memory that nobody waits for (zeros where `has` is
+// false, and nothing is read), and an arrival on `bar` when all of this thread's
+// copies before it have landed.
+template <int N>
+GBF_DEVICE void async_copy(void* dst, const void* src, bool has) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(has ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(has ? 4 : 0) : "memory");
+}
+GBF_DEVICE void async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 16 float32 columns of this warp's TMEM lanes, not waited for.
@@ -217,7 +231,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->drain[b], 1);
-      mbar_init(&ctl->scales_full[b], 1);
+      mbar_init(&ctl->scales_full[b], 32);                  // the lanes that fill them
       mbar_init(&ctl->scales_empty[b], kBpEpilogueWarps);
     }
     ctl->peer_issued = 0;
@@ -328,26 +342,23 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           ok = mbar_wait_warp(&ctl->scales_empty[chunk & 1], ((chunk >> 1) & 1) ^ 1u, &ctl->abort, p.err);
           if (!ok) break;
           const bool in = kb + at < kb_end;
+          // rows and channels outside have no scales: zeros, and what they sum is not stored
           const int n = n0 + second * kBlockCols;
-          const float w = in && n < p.n ? p.w_scales[static_cast<int64_t>(n / kBlockCols) * p.blocks + kb + at] : 0.0f;
-          uint4 bias = make_uint4(0, 0, 0, 0);
-          if (kb == kb_begin && p.bias && n0 + lane * 8 < p.n) bias = ld_cached(p.bias + n0 + lane * 8);
-          const int row0 = m0 + second;
-          const float* sx = p.x_scales + static_cast<int64_t>(row0) * p.blocks + kb + at;
-          for (int r = 0; r < kBpRows; r += 64) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)                    // rows behind the last have no scales, and are not stored
-              v[i] = in && row0 + r + 2 * i < p.m ? sx[static_cast<int64_t>(r + 2 * i) * p.blocks] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sc.x[at * kBpChunkRow + second + r + 2 * i] = v[i];
+          const bool has = in && n < p.n;
+          async_copy<4>(&sc.w[second][at], p.w_scales + (has ? static_cast<int64_t>(n / kBlockCols) * p.blocks + kb + at : 0), has);
+          if (kb == kb_begin) {
+            const bool some = p.bias && n0 + lane * 8 < p.n;
+            async_copy<16>(&sc.bias[lane * 8], some ? static_cast<const void*>(p.bias + n0 + lane * 8) : p.y, some);
           }
-          sc.w[second][at] = w;
-          if (kb == kb_begin) *reinterpret_cast<uint4*>(&sc.bias[lane * 8]) = bias;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->scales_full[chunk & 1]);
+#pragma unroll 8
+          for (int r = second; r < kBpRows; r += 32 / kBpChunk) {
+            const bool row = in && m0 + r < p.m;
+            async_copy<4>(&sc.x[at * kBpChunkRow + r], p.x_scales + (row ? static_cast<int64_t>(m0 + r) * p.blocks + kb + at : 0), row);
+          }
+          async_arrive(&ctl->scales_full[chunk & 1]);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -425,23 +436,18 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->scales_empty[(chunk - 1) & 1]);
-#pragma unroll 1
-      for (int h = 0; h < 32 / kBpBoxRows; ++h) {
-        if (lane == 0) bulk_wait_read_all();                // the store before has read the box
-        __syncwarp();
-        if (lane / kBpBoxRows == h) {
+      if (lane == 0) bulk_wait_read_all();                  // the tile before has left the box
+      __syncwarp();
 #pragma unroll
-          for (int c = 0; c < kBpWarpCols / 8; ++c)         // piece c sits at c ^ (row % 8): the TMA 128-byte swizzle
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(box) + lane % kBpBoxRows * 128 + ((c ^ (lane & 7)) << 4)),
-                         "r"(out[c].x), "r"(out[c].y), "r"(out[c].z), "r"(out[c].w)
-                         : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && ok && col0 < p.n && row0 + h * kBpBoxRows < p.m) {
-          tma_store_2d(&map_y, box, col0, row0 + h * kBpBoxRows);
-          bulk_commit();
-        }
+      for (int c = 0; c < kBpWarpCols / 8; ++c)             // piece c sits at c ^ (row % 8): the TMA 128-byte swizzle
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(box) + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                     "r"(out[c].x), "r"(out[c].y), "r"(out[c].z), "r"(out[c].w)
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && ok && col0 < p.n && row0 < p.m) {
+        tma_store_2d(&map_y, box, col0, row0);
+        bulk_commit();
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -538,7 +544,7 @@ cudaError_t resident_clusters(int split, int* clusters) {
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
   CUtensorMap map_x, map_w, map_y;
   if (!make_map(&map_x, a.x, a.m, a.k, kBpRows, true) || !make_map(&map_w, a.w, a.n, a.k, kBpHalf / 2, true) ||
-      !make_map(&map_y, a.y, a.m, a.n, kBpBoxRows, false)) {
+      !make_map(&map_y, a.y, a.m, a.n, 32, false)) {
     *why = "cuTensorMapEncodeTiled is unavailable or rejected the operands";
     return cudaErrorInvalidValue;
   }
