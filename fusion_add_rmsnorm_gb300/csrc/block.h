@@ -59,5 +59,6 @@ struct LinearBlockArgs {
 
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
+int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k);       // about how long that takes
 
 }  // namespace gbf

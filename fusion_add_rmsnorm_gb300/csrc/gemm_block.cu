@@ -13,15 +13,17 @@
 // linear_block_kernel: the 128 rows of a W block are the MMA's rows (TMEM
 // lanes), NX rows of X its columns, so a decode batch of a few rows wastes no
 // MMA rows and all of W's bytes are spread over the CTAs.  A thread holds one
-// output channel and its NX rows' sums.
+// output channel and the sums of some of the NX rows.
 //   warp 0     TMA producer: W's 128 and X's NX rows of a K block into a ring
-//   warp 1     MMA issuer: four MMAs of 32 K into the next accumulator
-//   warp 2     tensor memory
-//   warps 4-7  epilogue: accumulators of 32 channels each; the X scales of a
-//              block, times W's, go through shared memory one block ahead
-// With few output tiles, a cluster of up to eight CTAs cuts K between them and
-// adds its partial sums through distributed shared memory, in the order of K,
-// so that a result has the same bits in every run.
+//   warp 1     MMA issuer: four MMAs of 32 K into the next accumulator (the whole
+//              warp walks the loop, which keeps the descriptors in uniform
+//              registers; one lane issues)
+//   warps 2-3  the X scales of 8 K blocks ahead, times W's; warp 2 tensor memory
+//   warps 4...  epilogue, 32 channels and up to 64 rows of X each
+// With few output tiles, a cluster of up to eight CTAs cuts K between them.  Each
+// owns NX / split of the tile's rows of X, gets the others' sums of them by remote
+// stores and adds them in the order of K, so that a result has the same bits in
+// every run.
 //
 // Every mbarrier wait is bounded, as in gemm_tcgen05.cu: one that gives up
 // sets the device error word and an abort flag, every role leaves its loop,
@@ -36,37 +38,51 @@
 namespace gbf {
 namespace {
 
-constexpr int kLbThreads = 256;
 constexpr int kLbRows = 128;              // W rows of a tile: one scale block
 constexpr int kLbEpilogue = 4;            // first epilogue warp
 constexpr int kLbMaxSplit = 8;            // portable cluster size
 
-// Shared memory of a CTA with NX rows of X: two CTAs an SM up to 64 of them, so
-// that one's start and end hide behind the other's loads.
-template <int NX>
+constexpr int kLbChunk = 8;               // K blocks whose scales are filled at a time
+
+// Shared memory of a CTA with NX rows of X, alone on K or one of a cluster
+// (SPLIT): two CTAs an SM up to 32 rows, so that the next call's comes beside
+// this one's; from 64 on a deeper ring is worth more.  No more accumulators than stages: the epilogue then waits for a
+// stage's MMAs before that stage can be through twice.
+template <int NX, bool SPLIT>
 struct Lb {
-  static constexpr int kPerSm = NX <= 64 ? 2 : 1;
+  static constexpr int kPerSm = NX <= 32 ? 2 : 1;
+  static constexpr int kGroups = NX <= 32 ? 1 : NX / 32;                            // groups of four epilogue warps
+  static constexpr int kCols = NX / kGroups;                                      // rows of X of a group
+  static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kStageBytes = (kLbRows + NX) * BK_BYTES;
-  static constexpr int kStages = NX == 16 ? 6 : NX == 32 ? 5 : NX == 64 ? 4 : 6;
-  static constexpr int kAccs = NX == 16 ? 8 : (kPerSm == 2 ? 256 : 512) / NX;     // accumulators in TMEM
-  static constexpr int kTmemCols = kAccs * NX;
-  static constexpr int kScaleBytes = 4 * 2 * NX * 4;                              // [epilogue warp][2][NX]
+  static constexpr int kPartBytes = SPLIT ? NX * kLbRows * 4 : 0;                 // [part][owned row][channel]
+  static constexpr int kScaleRow = NX + 4;                                        // read as 16-byte vectors
+  static constexpr int kScaleBytes = 2 * kLbChunk * kScaleRow * 4;
+  static constexpr int kRoom = (kPerSm == 2 ? 115712 : 232448) - 2048;            // of a CTA, less alignment and barriers
+  static constexpr int kFit = (kRoom - kPartBytes - kScaleBytes) / kStageBytes;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kAccs = kStages < 512 / kPerSm / NX ? kStages : 512 / kPerSm / NX;
+  static constexpr int kTmemCols = kAccs * NX <= 32 ? 32 : kAccs * NX <= 64 ? 64 : kAccs * NX <= 128 ? 128 : kAccs * NX <= 256 ? 256 : 512;
+  static_assert(kStages >= 3 && kAccs >= 3, "stages and accumulators in flight");
 };
 
-template <int NX>
+template <int S, int A>
 struct __align__(8) LbCtl {
-  uint64_t full[Lb<NX>::kStages];
-  uint64_t empty[Lb<NX>::kStages];
-  uint64_t acc_full[Lb<NX>::kAccs];
-  uint64_t acc_empty[Lb<NX>::kAccs];
+  uint64_t full[S];
+  uint64_t done[S];          // a K block's MMAs: its stage is free, its accumulator full
+  uint64_t acc_empty[A];
+  uint64_t scales_full[2];
+  uint64_t scales_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-template <int NX>
+template <int NX, bool SPLIT>
 constexpr size_t lb_smem() {
-  return 1024 /* alignment */ + Lb<NX>::kStages * Lb<NX>::kStageBytes + Lb<NX>::kScaleBytes + sizeof(LbCtl<NX>);
+  using L = Lb<NX, SPLIT>;
+  return 1024 /* alignment */ + L::kStages * L::kStageBytes + L::kPartBytes + L::kScaleBytes +
+         sizeof(LbCtl<L::kStages, L::kAccs>);
 }
 
 struct LinearBlockParams {
@@ -76,7 +92,8 @@ struct LinearBlockParams {
   __nv_bfloat16* y;
   unsigned int* err;
   int m, n, blocks;          // blocks: of K
-  int m_tiles, n_tiles, split;
+  int m_tiles, n_tiles;
+  int split;                 // CTAs (a cluster) that cut K: a power of two, at most kLbMaxSplit
   int act;
 };
 
@@ -91,30 +108,32 @@ GBF_DEVICE void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-GBF_DEVICE float ld_cluster_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+GBF_DEVICE void st_cluster_f32(uint32_t a, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+
+// One lane of the (converged) warp.
+GBF_DEVICE bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
-GBF_DEVICE void sts32f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-
-template <int NX>
-__global__ void __launch_bounds__(kLbThreads, Lb<NX>::kPerSm)
+template <int NX, bool SPLIT>
+__global__ void __launch_bounds__(Lb<NX, SPLIT>::kThreads, Lb<NX, SPLIT>::kPerSm)
 linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                     const LinearBlockParams p) {
-  using L = Lb<NX>;
-  constexpr int S = L::kStages, A = L::kAccs;
+  using L = Lb<NX, SPLIT>;
+  constexpr int S = L::kStages, A = L::kAccs, COLS = L::kCols;
   constexpr uint32_t kIdesc = idesc(true, kLbRows, NX);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smem_w = smem;                                   // S x 128 rows of 128 bytes
   uint8_t* smem_x = smem + S * kLbRows * BK_BYTES;          // S x NX rows of 128 bytes
-  uint8_t* smem_s = smem + S * L::kStageBytes;
-  LbCtl<NX>* ctl = reinterpret_cast<LbCtl<NX>*>(smem_s + L::kScaleBytes);
+  float* part = reinterpret_cast<float*>(smem + S * L::kStageBytes);
+  float* scales = reinterpret_cast<float*>(smem + S * L::kStageBytes + L::kPartBytes);
+  LbCtl<S, A>* ctl = reinterpret_cast<LbCtl<S, A>*>(smem + S * L::kStageBytes + L::kPartBytes + L::kScaleBytes);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / p.split;
   const int m0 = tile % p.m_tiles * NX, nt = tile / p.m_tiles, n0 = nt * kLbRows;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / p.split);
@@ -123,11 +142,12 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&ctl->full[s], 1);
-      mbar_init(&ctl->empty[s], 1);
+      mbar_init(&ctl->done[s], 1);
     }
-    for (int b = 0; b < A; ++b) {
-      mbar_init(&ctl->acc_full[b], 1);
-      mbar_init(&ctl->acc_empty[b], 4);                     // one arrive per epilogue warp
+    for (int b = 0; b < A; ++b) mbar_init(&ctl->acc_empty[b], 4 * L::kGroups);     // one arrive per epilogue warp
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctl->scales_full[b], 2);                   // the two warps that fill them
+      mbar_init(&ctl->scales_empty[b], 4 * L::kGroups);
     }
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
@@ -140,17 +160,19 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  // every CTA of the cluster runs before its shared memory is written to (waited for below)
+  if (SPLIT) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
 
-  float acc[NX];
+  float acc[COLS];
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       int issued = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++issued) {
         const int s = issued % S;
-        if (!mbar_wait<false, false>(&ctl->empty[s], ((issued / S) & 1) ^ 1u, &ctl->abort, p.err)) break;
+        if (!mbar_wait<false, false>(&ctl->done[s], ((issued / S) & 1) ^ 1u, &ctl->abort, p.err)) break;
         mbar_arrive_expect_tx(&ctl->full[s], L::kStageBytes);
         tma_load_2d(smem_w + s * kLbRows * BK_BYTES, &map_w, &ctl->full[s], kb * BK_BYTES, n0);
         tma_load_2d(smem_x + s * NX * BK_BYTES, &map_x, &ctl->full[s], kb * BK_BYTES, m0);
@@ -162,88 +184,107 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        const int s = i % S, b = i % A;
-        if (!mbar_wait<false, false>(&ctl->acc_empty[b], ((i / A) & 1) ^ 1u, &ctl->abort, p.err)) break;
-        if (!mbar_wait<false, false>(&ctl->full[s], (i / S) & 1, &ctl->abort, p.err)) break;
-        tc_fence_after();
-        const uint32_t w_addr = smem_u32(smem_w + s * kLbRows * BK_BYTES), x_addr = smem_u32(smem_x + s * NX * BK_BYTES);
+    const bool elected = elect_one();
+    bool ok = true;
+    for (int i = 0; i < kb1 - kb0 && ok; ++i) {
+      const int s = i % S, b = i % A;
+      const uint64_t w_desc = smem_desc_sw128(smem_u32(smem_w) + s * kLbRows * BK_BYTES);
+      const uint64_t x_desc = smem_desc_sw128(smem_u32(smem_x) + s * NX * BK_BYTES);
+      ok = mbar_wait<false, false>(&ctl->acc_empty[b], ((i / A) & 1) ^ 1u, &ctl->abort, p.err) &&
+           mbar_wait<false, false>(&ctl->full[s], (i / S) & 1, &ctl->abort, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (ok && elected) {
 #pragma unroll
-        for (int kk = 0; kk < BK_BYTES / UMMA_K_BYTES; ++kk)
-          tc_mma<true, false>(tmem_base + b * NX, smem_desc_sw128(w_addr + kk * UMMA_K_BYTES),
-                              smem_desc_sw128(x_addr + kk * UMMA_K_BYTES), kIdesc, kk != 0);
-        tc_commit<false>(&ctl->empty[s]);
-        tc_commit<false>(&ctl->acc_full[b]);
+        for (int kk = 0; kk < BK_BYTES / UMMA_K_BYTES; ++kk)         // 32 bytes on inside the swizzled row
+          tc_mma<true, false>(tmem_base + b * NX, w_desc + kk * (UMMA_K_BYTES >> 4), x_desc + kk * (UMMA_K_BYTES >> 4),
+                              kIdesc, kk != 0);
+        tc_commit<false>(&ctl->done[s]);
       }
+    }
+    if (elected) {
       tc_commit_self<false>(&ctl->drain);
       int own = 0;
       mbar_wait(&ctl->drain, 0, &own, p.err);
     }
-  } else if (warp >= kLbEpilogue) {
-    // -------------------------------------------------------------- epilogue
-    const int quarter = warp - kLbEpilogue;                 // TMEM lanes 32 * quarter .. + 31
-    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t sbuf = smem_u32(smem_s) + quarter * 2 * NX * 4;
-    constexpr int PER = NX < 32 ? 1 : NX / 32;              // scales a lane fetches
-    float next[PER], w_next;                                // multiplied where they are used: no wait here
-    auto fetch = [&](int kb) {
-      w_next = kb < kb1 ? p.w_scales[static_cast<int64_t>(nt) * p.blocks + kb] : 0.0f;
+  } else if (warp < kLbEpilogue) {
+    // ---------------------------------------------------------------- scales
+    const int at = lane % kLbChunk, first = (warp - 2) * 4 + lane / kLbChunk;     // a lane's K block, every eighth row
+    for (int kb = kb0, chunk = 0; kb < kb1; kb += kLbChunk, ++chunk) {
+      if (!mbar_wait_warp(&ctl->scales_empty[chunk & 1], ((chunk >> 1) & 1) ^ 1u, &ctl->abort, p.err)) break;
+      float* to = scales + (chunk & 1) * kLbChunk * L::kScaleRow + at * L::kScaleRow;
+      const bool in = kb + at < kb1;
+      const float w = in ? p.w_scales[static_cast<int64_t>(nt) * p.blocks + kb + at] : 0.0f;
+      float v[NX / 8];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int row = m0 + lane + i * 32;
-        next[i] = (NX >= 32 || lane < NX) && kb < kb1 && row < p.m
-                      ? p.x_scales[static_cast<int64_t>(row) * p.blocks + kb]
-                      : 0.0f;
+      for (int i = 0; i < NX / 8; ++i) {                    // rows behind the last have no scales, and are not stored
+        const int row = m0 + first + 8 * i;
+        v[i] = in && row < p.m ? p.x_scales[static_cast<int64_t>(row) * p.blocks + kb + at] : 0.0f;
       }
-    };
 #pragma unroll
-    for (int j = 0; j < NX; ++j) acc[j] = 0.0f;
-    fetch(kb0);
-    for (int i = 0; i < kb1 - kb0; ++i) {
-      const int b = i % A;
-      const uint32_t sc = sbuf + (i & 1) * NX * 4;
-#pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (NX >= 32 || lane < NX) sts32f(sc + (lane + j * 32) * 4, next[j] * w_next);
-      fetch(kb0 + i + 1);
+      for (int i = 0; i < NX / 8; ++i) to[first + 8 * i] = v[i] * w;
       __syncwarp();
-      if (!mbar_wait_warp<false>(&ctl->acc_full[b], (i / A) & 1, &ctl->abort, p.err)) break;
-      tc_fence_after();
-      constexpr int STEP = NX < 32 ? 16 : 32;
+      if (lane == 0) mbar_arrive(&ctl->scales_full[chunk & 1]);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3, col0 = (warp - kLbEpilogue) / 4 * COLS;     // TMEM lanes 32 * quarter .. + 31
+    const uint32_t taddr = tmem_base + col0 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < NX; c += STEP) {
-        uint32_t r[STEP];
-        if constexpr (STEP == 16) tmem_ld_16cols(taddr + b * NX + c, r);
-        else tmem_ld_32cols(taddr + b * NX + c, r);
+    for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
+    bool ok = true;
+    int i = 0;
+    for (int kb = kb0, chunk = 0; kb < kb1 && ok; kb += kLbChunk, ++chunk) {
+      uint32_t sc = smem_u32(scales + (chunk & 1) * kLbChunk * L::kScaleRow + col0);
+      ok = mbar_wait_warp<false>(&ctl->scales_full[chunk & 1], (chunk >> 1) & 1, &ctl->abort, p.err);
+      for (const int end = min(kb1 - kb0, i + kLbChunk); i < end && ok; ++i, sc += L::kScaleRow * 4) {
+        const int b = i % A;
+        ok = mbar_wait<false, false>(&ctl->done[i % S], (i / S) & 1, &ctl->abort, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        constexpr int STEP = COLS < 32 ? 16 : 32;
 #pragma unroll
-        for (int j = 0; j < STEP; j += 4) {
-          const float4 f = lds128f(sc + (c + j) * 4);
-          const float2 lo = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                       make_float2(f.x, f.y), make_float2(acc[c + j], acc[c + j + 1]));
-          const float2 hi = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
-                                       make_float2(f.z, f.w), make_float2(acc[c + j + 2], acc[c + j + 3]));
-          acc[c + j] = lo.x;
-          acc[c + j + 1] = lo.y;
-          acc[c + j + 2] = hi.x;
-          acc[c + j + 3] = hi.y;
+        for (int c = 0; c < COLS; c += STEP) {
+          uint32_t r[STEP];
+          if constexpr (STEP == 16) tmem_ld_16cols(taddr + b * NX + c, r);
+          else tmem_ld_32cols(taddr + b * NX + c, r);
+          if (c + STEP == COLS) {                             // all read: the accumulator goes back before the sums
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->acc_empty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < STEP; j += 4) {
+            const float4 f = lds128f(sc + (c + j) * 4);
+            const float2 lo = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                         make_float2(f.x, f.y), make_float2(acc[c + j], acc[c + j + 1]));
+            const float2 hi = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                         make_float2(f.z, f.w), make_float2(acc[c + j + 2], acc[c + j + 3]));
+            acc[c + j] = lo.x;
+            acc[c + j + 1] = lo.y;
+            acc[c + j + 2] = hi.x;
+            acc[c + j + 3] = hi.y;
+          }
         }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->acc_empty[b]);
+      if (lane == 0) mbar_arrive(&ctl->scales_empty[chunk & 1]);
     }
     const int ch = quarter * 32 + lane;                     // this thread's row of the W tile
-    if (p.split > 1) {
-      // the ring is free: the last accumulator came after every copy and MMA
+    if constexpr (SPLIT) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      const int owned = NX / p.split, log = __ffs(owned) - 1;      // a power of two
+      const uint32_t to = smem_u32(part) + (rank * owned * kLbRows + ch) * 4;
 #pragma unroll
-      for (int j = 0; j < NX; ++j) sts32f(smem_u32(smem) + (j * kLbRows + ch) * 4, acc[j]);
+      for (int j = 0; j < COLS; ++j)
+        st_cluster_f32(map_cluster(to + ((col0 + j) & (owned - 1)) * kLbRows * 4, (col0 + j) >> log), acc[j]);
     } else if (n0 + ch < p.n) {
       const float bias = p.bias ? __bfloat162float(p.bias[n0 + ch]) : 0.0f;
 #pragma unroll
-      for (int j = 0; j < NX; ++j)
-        if (m0 + j < p.m)
-          p.y[static_cast<int64_t>(m0 + j) * p.n + n0 + ch] = __float2bfloat16(fast_act(acc[j] + bias, p.act));
+      for (int j = 0; j < COLS; ++j)
+        if (m0 + col0 + j < p.m)
+          p.y[static_cast<int64_t>(m0 + col0 + j) * p.n + n0 + ch] = __float2bfloat16(fast_act(acc[j] + bias, p.act));
     }
   }
 
@@ -253,22 +294,22 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     tc_fence_after();
     tmem_dealloc<false>(tmem_base, L::kTmemCols);
   }
-  if (p.split > 1) {
-    cluster_sync();                                         // every CTA's partial sums are in its shared memory
-    const int per = NX / p.split, ch = threadIdx.x & (kLbRows - 1);
-    for (int j = rank * per + threadIdx.x / kLbRows; j < (rank + 1) * per; j += kLbThreads / kLbRows) {
-      const uint32_t at = smem_u32(smem) + (j * kLbRows + ch) * 4;
-      float part[kLbMaxSplit], sum = 0.0f;
+  if constexpr (SPLIT) {
+    if (warp < kLbEpilogue) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_sync();                                         // every CTA's sums are where they are added
+    const int owned = NX / p.split, ch = threadIdx.x & (kLbRows - 1);
+    const float bias = p.bias && n0 + ch < p.n ? __bfloat162float(p.bias[n0 + ch]) : 0.0f;
+    for (int j = threadIdx.x / kLbRows; j < owned; j += L::kThreads / kLbRows) {
+      const int row = m0 + rank * owned + j;
+      float v[kLbMaxSplit], sum = 0.0f;
 #pragma unroll
-      for (int r = 0; r < kLbMaxSplit; ++r) part[r] = r < p.split ? ld_cluster_f32(map_cluster(at, r)) : 0.0f;
+      for (int r = 0; r < kLbMaxSplit; ++r)
+        v[r] = r < p.split ? part[(r * owned + j) * kLbRows + ch] : 0.0f;
 #pragma unroll
-      for (int r = 0; r < kLbMaxSplit; ++r) sum += part[r];
-      if (m0 + j < p.m && n0 + ch < p.n) {
-        const float bias = p.bias ? __bfloat162float(p.bias[n0 + ch]) : 0.0f;
-        p.y[static_cast<int64_t>(m0 + j) * p.n + n0 + ch] = __float2bfloat16(fast_act(sum + bias, p.act));
-      }
+      for (int r = 0; r < kLbMaxSplit; ++r) sum += v[r];
+      if (row < p.m && n0 + ch < p.n)
+        p.y[static_cast<int64_t>(row) * p.n + n0 + ch] = __float2bfloat16(fast_act(sum + bias, p.act));
     }
-    cluster_sync();                                         // no CTA leaves while another reads its sums
   }
 }
 
@@ -286,30 +327,45 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
-template <int NX>
-cudaError_t launch_lb(const LinearBlockArgs& a, LinearBlockParams p, int sms, cudaStream_t stream, const char** why) {
+// K is cut while every CTA still has an SM to itself (the next call's may then
+// come beside it) and keeps four blocks.
+int split_of(int64_t tiles, int blocks, int sms) {
+  int split = 1;
+  while (split < kLbMaxSplit && tiles * split * 2 <= sms && blocks >= split * 2 * 4) split *= 2;
+  return split;
+}
+
+// About how long this kernel takes with NX = 64 or 128, which with
+// linear_block_pair_ns() decides who takes a call of more than 32 rows.
+// Measured: a K block of a tile 280 or 345 ns, its start and end 2.5 us, joining
+// a cluster's sums 1.5 or 3 us more.  The estimates against the measured times
+// (us; N x K, rows): 4096 x 4096, 128: 7 / 9.0 with 64, 7.8 / 9.1 with 128,
+// 13.1 / 18.4 with pairs; 512: 20.4 / 21.4, 13.5 / 13.4, 16.7 / 19.4; 1024: 38.3 /
+// 46, 24.6 / 31, 22.4 / 23.2; 16384 x 4096, 256: 38 / 44, 24.6 / 27.8, 22.4 / 23.8.
+int64_t thin_ns(int64_t m, int nx, const LinearBlockParams& p, int sms) {
+  const int64_t tiles = (m + nx - 1) / nx * p.n_tiles, waves = (tiles + sms - 1) / sms;
+  const int split = split_of(tiles, p.blocks, sms);
+  return waves * (2500 + (p.blocks + split - 1) / split * (nx == 64 ? 280 : 345)) +
+         (split > 1 ? (nx == 64 ? 1500 : 3000) : 0);
+}
+
+template <int NX, bool SPLIT>
+cudaError_t launch_split(const LinearBlockArgs& a, const LinearBlockParams& p, cudaStream_t stream, const char** why) {
   CUtensorMap map_x, map_w;
   if (!make_map(&map_x, a.x, a.m, a.k, NX, true) || !make_map(&map_w, a.w, a.n, a.k, kLbRows, true)) {
     *why = "cuTensorMapEncodeTiled is unavailable or rejected the operands";
     return cudaErrorInvalidValue;
   }
-  auto kern = linear_block_kernel<NX>;
-  cudaError_t e = allow_smem<linear_block_kernel<NX>>(lb_smem<NX>());
+  auto kern = linear_block_kernel<NX, SPLIT>;
+  cudaError_t e = allow_smem<linear_block_kernel<NX, SPLIT>>(lb_smem<NX, SPLIT>());
   if (e != cudaSuccess) {
     *why = "could not reserve shared memory";
     return e;
   }
-  p.m_tiles = (p.m + NX - 1) / NX;
-  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  // K is cut while the CTAs still fit the GPU at once and each keeps four blocks
-  p.split = 1;
-  while (p.split < kLbMaxSplit && tiles * p.split * 2 <= static_cast<int64_t>(sms) * Lb<NX>::kPerSm &&
-         p.blocks >= p.split * 2 * 4)
-    p.split *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(kLbThreads);
-  cfg.dynamicSmemBytes = lb_smem<NX>();
+  cfg.gridDim = dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split));
+  cfg.blockDim = dim3(Lb<NX, SPLIT>::kThreads);
+  cfg.dynamicSmemBytes = lb_smem<NX, SPLIT>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -323,13 +379,19 @@ cudaError_t launch_lb(const LinearBlockArgs& a, LinearBlockParams p, int sms, cu
   return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p);
 }
 
+template <int NX>
+cudaError_t launch_lb(const LinearBlockArgs& a, LinearBlockParams p, int sms, cudaStream_t stream, const char** why) {
+  p.m_tiles = (p.m + NX - 1) / NX;
+  p.split = split_of(static_cast<int64_t>(p.m_tiles) * p.n_tiles, p.blocks, sms);
+  return p.split > 1 ? launch_split<NX, true>(a, p, stream, why) : launch_split<NX, false>(a, p, stream, why);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (a.m > 128) return launch_linear_block_pair(a, stream, why);
   LinearBlockParams p = {};
   p.x_scales = a.x_scales;
   p.w_scales = a.w_scales;
@@ -341,10 +403,11 @@ cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, c
   p.blocks = static_cast<int>(block_count(a.k));
   p.n_tiles = static_cast<int>(block_count(a.n));
   p.act = a.act;
-  return a.m <= 16   ? launch_lb<16>(a, p, sms, stream, why)
-         : a.m <= 32 ? launch_lb<32>(a, p, sms, stream, why)
-         : a.m <= 64 ? launch_lb<64>(a, p, sms, stream, why)
-                     : launch_lb<128>(a, p, sms, stream, why);
+  if (a.m <= 16) return launch_lb<16>(a, p, sms, stream, why);
+  if (a.m <= 32) return launch_lb<32>(a, p, sms, stream, why);
+  const int64_t t64 = thin_ns(a.m, 64, p, sms), t128 = thin_ns(a.m, 128, p, sms), tp = linear_block_pair_ns(a.m, a.n, a.k);
+  if (tp < t64 && tp < t128) return launch_linear_block_pair(a, stream, why);
+  return t64 <= t128 ? launch_lb<64>(a, p, sms, stream, why) : launch_lb<128>(a, p, sms, stream, why);
 }
 
 }  // namespace gbf

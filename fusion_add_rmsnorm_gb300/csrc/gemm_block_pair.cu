@@ -539,7 +539,27 @@ cudaError_t resident_clusters(int split, int* clusters) {
   return cudaSuccess;
 }
 
+// K is cut while all tiles' clusters fit the GPU at once and each pair keeps six blocks.
+cudaError_t split_of(int64_t tiles, int blocks, int* split, int* fit) {
+  for (*split = kBpMaxSplit; *split >= 1; --*split) {
+    if (*split > 1 && blocks < *split * 6) continue;
+    const cudaError_t e = resident_clusters(*split, fit);
+    if (e != cudaSuccess || *split == 1 || tiles <= *fit) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
+
+// About how long a call takes here (measured: a K block 450 ns, the start and the
+// end of a tile 8 us, joining a cluster's sums 4 us more; see gemm_block.cu).
+int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k) {
+  const int64_t tiles = (m + 2 * kBpRows - 1) / (2 * kBpRows) * ((n + kBpCols - 1) / kBpCols);
+  const int blocks = static_cast<int>(block_count(k));
+  int split = 1, fit = 0;
+  if (split_of(tiles, blocks, &split, &fit) != cudaSuccess || fit < 1) return INT64_MAX;
+  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 450 + 2000) + 6000 + (split > 1 ? 4000 : 0);
+}
 
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
   CUtensorMap map_x, map_w, map_y;
@@ -561,16 +581,11 @@ cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stre
   p.n_tiles = static_cast<int>((a.n + kBpCols - 1) / kBpCols);
   p.act = a.act;
   const int64_t tiles = static_cast<int64_t>(p.m_units) * p.n_tiles;
-  // K is cut while all tiles' clusters fit the GPU at once and each pair keeps six blocks
   int fit = 0;
-  for (p.split = kBpMaxSplit; p.split >= 1; --p.split) {
-    if (p.split > 1 && p.blocks < p.split * 6) continue;
-    const cudaError_t e = resident_clusters(p.split, &fit);
-    if (e != cudaSuccess) {
-      *why = "could not reserve shared memory";
-      return e;
-    }
-    if (p.split == 1 || tiles <= fit) break;
+  const cudaError_t e = split_of(tiles, p.blocks, &p.split, &fit);
+  if (e != cudaSuccess) {
+    *why = "could not reserve shared memory";
+    return e;
   }
   const int clusters = static_cast<int>(tiles < fit ? tiles : fit);
   // as in gemm_tcgen05.cu: the divisor of the clusters at work nearest 16 within 12..24
