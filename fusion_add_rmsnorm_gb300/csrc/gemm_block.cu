@@ -339,9 +339,9 @@ int split_of(int64_t tiles, int blocks, int sms) {
 // linear_block_pair_ns() decides who takes a call of more than 32 rows.
 // Measured: a K block of a tile 280 or 345 ns, its start and end 2.5 us, joining
 // a cluster's sums 1.5 or 3 us more.  The estimates against the measured times
-// (us; N x K, rows): 4096 x 4096, 128: 7 / 9.0 with 64, 7.8 / 9.1 with 128,
-// 13.1 / 18.4 with pairs; 512: 20.4 / 21.4, 13.5 / 13.4, 16.7 / 19.4; 1024: 38.3 /
-// 46, 24.6 / 31, 22.4 / 23.2; 16384 x 4096, 256: 38 / 44, 24.6 / 27.8, 22.4 / 23.8.
+// (us; 64 rows a tile, 128, pairs), N x K = 4096 x 4096: 128 rows 7.2 / 9.0, 8.3 /
+// 9.1, 13.9 / 18; 512 rows 22.9 / 21.4, 13.5 / 13.4, 17.8 / 19; 1024 rows 34 / 46,
+// 27 / 31, 21.8 / 21.7.  16384 x 4096, 256 rows: 45 / 44, 27 / 27.8, 21.8 / 23.7.
 int64_t thin_ns(int64_t m, int nx, const LinearBlockParams& p, int sms) {
   const int64_t tiles = (m + nx - 1) / nx * p.n_tiles, waves = (tiles + sms - 1) / sms;
   const int split = split_of(tiles, p.blocks, sms);

@@ -15,15 +15,20 @@
 //               in uniform registers: 25 cycles an MMA, 120 from a lane's own).
 //               Odd CTA: tell the even one's issuer that an accumulator was read
 //   warp 3      tensor memory; the scales of 16 K blocks ahead, and the bias
-//   warps 4-19  epilogue, 32 rows x 64 channels each: a K block's accumulator is
-//               read back, given back, and added, scaled, to 64 float32 registers;
+//   warps 4-11  epilogue, 32 rows x 128 channels each: a K block's accumulator is
+//               read back, given back, and added, scaled, to 128 float32 registers;
 //               after the last block bias, activation, one bf16 rounding, and bulk
 //               tensor stores
+// The registers that the first four warps do not need go to the epilogue
+// (setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168).
 // What bounds it: an accumulator's way round (MMAs, completion, read back, given
 // back in both CTAs), as 512 TMEM columns hold two K blocks.  So that way is kept
 // short: an SM's epilogue gives back through a hardware barrier, not an mbarrier,
-// scales come from shared memory, and no wait or arrival in the loop has cluster
-// scope (an acquire there empties L1, a release waits for loads in flight).
+// scales come from shared memory, no wait or arrival in the loop has cluster scope
+// (an acquire there empties L1, a release waits for loads in flight), and the next
+// accumulator is asked about while this one's last columns are added.  8192 x 16384
+// x 4096: 453 us with the tanh GELU, 382 without an activation (24 us less for each
+// tile's end with 16 warps of 64 channels, but 90 more in the loop).
 //
 // CTAs are persistent and walk the tiles.  With few of them, up to four pairs of
 // a cluster cut K, and add their partial sums through distributed shared memory,
@@ -42,17 +47,18 @@
 namespace gbf {
 namespace {
 
-constexpr int kBpThreads = 640;
+constexpr int kBpThreads = 384;
 constexpr int kBpRows = 128;                    // X rows of a CTA
 constexpr int kBpCols = 256;                    // channels of a pair's tile
 constexpr int kBpHalf = kBpCols / 2;
 constexpr int kBpStages = 4;
 constexpr int kBpStageBytes = (kBpRows + kBpHalf) * BK_BYTES;
 constexpr int kBpEpilogue = 4;                  // first epilogue warp
-constexpr int kBpEpilogueWarps = 16;
-constexpr int kBpWarpCols = 64;                 // channels of an epilogue warp
+constexpr int kBpEpilogueWarps = 8;
+constexpr int kBpWarpCols = 128;                // channels of an epilogue warp: a half
 constexpr int kBpMaxSplit = 4;                  // pairs of a portable cluster
-constexpr int kBpBoxBytes = 32 * kBpWarpCols * 2;  // an epilogue warp's store: 32 rows x 64 columns of bf16
+constexpr int kBpBoxCols = 64;                  // an epilogue warp's stores: 32 rows x 64 columns of bf16
+constexpr int kBpBoxBytes = 32 * kBpBoxCols * 2;
 // Scales of 16 K blocks, one copy in use and one being filled: X's as
 // [K block][row], two words more a row than needed so that both the filling (16
 // K blocks of two rows) and the reading (32 rows of one) meet every bank once.
@@ -79,7 +85,7 @@ struct __align__(8) BpCtl {
   int abort;
 };
 
-constexpr size_t kBpSmem = 1024 /* alignment */ + kBpStages * kBpStageBytes + kBpEpilogueWarps * kBpBoxBytes +
+constexpr size_t kBpSmem = 1024 /* alignment */ + kBpStages * kBpStageBytes + kBpEpilogueWarps * 2 * kBpBoxBytes +
                            2 * sizeof(BpScales) + sizeof(BpCtl);
 static_assert(kBpSmem <= 232448, "227 KB a CTA");
 static_assert(kBpRows * kBpCols * 4 <= kBpStages * kBpStageBytes, "partial sums fit the ring");
@@ -152,28 +158,39 @@ GBF_DEVICE void async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 16 float32 columns of this warp's TMEM lanes, not waited for.
-GBF_DEVICE void tmem_ld_async(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 float32 columns of this warp's TMEM lanes, not waited for.
+GBF_DEVICE void tmem_ld_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
 
 // Waits for the loads above.  The registers pass through, so that no use of
 // them is moved ahead of the wait.
-GBF_DEVICE void tmem_ld_wait(uint32_t (&r)[16]) {
+GBF_DEVICE void tmem_ld_wait(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               ::"memory");
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-GBF_DEVICE void add_scaled(float (&acc)[kBpWarpCols], int at, const uint32_t (&r)[16], float2 s) {
+// Whether the phase of `bar` with this parity is over, without waiting.
+GBF_DEVICE uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok;
+}
+GBF_DEVICE void add_scaled(float (&acc)[kBpWarpCols], int at, const uint32_t (&r)[32], float2 s) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
+  for (int j = 0; j < 32; j += 2) {
     const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s,
                                 make_float2(acc[at + j], acc[at + j + 1]));
     acc[at + j] = v.x;
@@ -211,7 +228,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
   uint8_t* smem_x = smem;
   uint8_t* smem_w = smem + S * kBpRows * BK_BYTES;
   uint8_t* smem_out = smem + S * kBpStageBytes;
-  BpScales* scales = reinterpret_cast<BpScales*>(smem_out + kBpEpilogueWarps * kBpBoxBytes);
+  BpScales* scales = reinterpret_cast<BpScales*>(smem_out + kBpEpilogueWarps * 2 * kBpBoxBytes);
   BpCtl* ctl = reinterpret_cast<BpCtl*>(scales + 2);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -256,7 +273,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
 
   uint32_t issued = 0;                                      // producer: K blocks whose copies it issued
   if (warp < kBpEpilogue) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       if (lane == 0) {
@@ -362,12 +379,12 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;                           // TMEM lanes 32 * quarter .. + 31
     const int col_at = (warp - kBpEpilogue) / 4 * kBpWarpCols, half = col_at / kBpHalf;
     const uint32_t taddr = tmem_base + col_at + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* box = smem_out + (warp - kBpEpilogue) * kBpBoxBytes;
-    uint32_t it = 0, chunk = 0;
+    uint8_t* box = smem_out + (warp - kBpEpilogue) * 2 * kBpBoxBytes;
+    uint32_t it = 0, chunk = 0, ready = 0;
     bool ok = true;
     for (int tile = first; tile < tiles; tile += stride) {
       const __nv_bfloat16* bias = scales[chunk & 1].bias + col_at;
@@ -380,10 +397,11 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         const float* sw = sc.w[half];
         const int end = min(kBpChunk, kb_end - kb0);
         ok = ok && mbar_wait_warp(&ctl->scales_full[chunk & 1], (chunk >> 1) & 1, &ctl->abort, p.err);
+        float s_next = sx[0] * sw[0];
         for (int kb = 0; kb < end; ++kb, ++it) {
           const uint32_t b = (it & 1) * 2 + half;
-          const float s = sx[kb * kBpChunkRow] * sw[kb];
-          ok = ok && mbar_wait<false, false>(&ctl->acc_full[b], (it >> 1) & 1, &ctl->abort, p.err);
+          const float s = s_next;
+          if (!ready) ok = ok && mbar_wait<false, false>(&ctl->acc_full[b], (it >> 1) & 1, &ctl->abort, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             give_back(b);
@@ -392,21 +410,24 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           tc_fence_after();
           const float2 ss = make_float2(s, s);
           const uint32_t at = taddr + (it & 1) * kBpCols;
-          uint32_t r0[16], r1[16];
+          uint32_t r0[32], r1[32];
           tmem_ld_async(at, r0);
           tmem_ld_wait(r0);
-          tmem_ld_async(at + 16, r1);
+          tmem_ld_async(at + 32, r1);
           add_scaled(acc, 0, r0, ss);
           tmem_ld_wait(r1);
-          tmem_ld_async(at + 32, r0);
-          add_scaled(acc, 16, r1, ss);
+          tmem_ld_async(at + 64, r0);
+          add_scaled(acc, 32, r1, ss);
           tmem_ld_wait(r0);
-          tmem_ld_async(at + 48, r1);
-          add_scaled(acc, 32, r0, ss);
+          tmem_ld_async(at + 96, r1);
+          add_scaled(acc, 64, r0, ss);
           tmem_ld_wait(r1);
           tc_fence_before();
           give_back(b);
-          add_scaled(acc, 48, r1, ss);
+          ready = mbar_test(&ctl->acc_full[b ^ 2], ((it + 1) >> 1) & 1);
+          const int after = min(kb + 1, end - 1);           // the next one's scale, ahead of its wait
+          s_next = sx[after * kBpChunkRow] * sw[after];
+          add_scaled(acc, 96, r1, ss);
         }
         // the last chunk goes back once the tile's bias has been read
         if (kb0 + kBpChunk < kb_end && lane == 0) mbar_arrive(&ctl->scales_empty[chunk & 1]);
@@ -426,29 +447,30 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
       int m0, n0;
       bp_origin(p, odd, tile, m0, n0);
       const int row0 = m0 + quarter * 32, col0 = n0 + col_at;
-      uint4 out[kBpWarpCols / 8];
+      if (lane == 0) bulk_wait_read_all();                  // the tile before has left the boxes
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < kBpWarpCols / 8; ++c) {
         float a[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = acc[c * 8 + e];
-        out[c] = finish8(a, *reinterpret_cast<const uint4*>(bias + c * 8), p.act);
+        const uint4 o = finish8(a, *reinterpret_cast<const uint4*>(bias + c * 8), p.act);
+        // piece c of a row sits at c ^ (row % 8): the TMA 128-byte swizzle
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                     ::"r"(smem_u32(box) + c / 8 * kBpBoxBytes + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)), "r"(o.x), "r"(o.y),
+                     "r"(o.z), "r"(o.w)
+                     : "memory");
+        if (c % 8 == 7) {                                   // a box is whole
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ok && col0 + c / 8 * kBpBoxCols < p.n && row0 < p.m) {
+            tma_store_2d(&map_y, box + c / 8 * kBpBoxBytes, col0 + c / 8 * kBpBoxCols, row0);
+            bulk_commit();
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->scales_empty[(chunk - 1) & 1]);
-      if (lane == 0) bulk_wait_read_all();                  // the tile before has left the box
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < kBpWarpCols / 8; ++c)             // piece c sits at c ^ (row % 8): the TMA 128-byte swizzle
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(box) + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                     "r"(out[c].x), "r"(out[c].y), "r"(out[c].z), "r"(out[c].w)
-                     : "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && ok && col0 < p.n && row0 < p.m) {
-        tma_store_2d(&map_y, box, col0, row0);
-        bulk_commit();
-      }
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -551,14 +573,14 @@ cudaError_t split_of(int64_t tiles, int blocks, int* split, int* fit) {
 
 }  // namespace
 
-// About how long a call takes here (measured: a K block 450 ns, the start and the
-// end of a tile 8 us, joining a cluster's sums 4 us more; see gemm_block.cu).
+// About how long a call takes here (measured: a K block 405 ns, a tile's end 2.8 us,
+// the call's start and end 6 us, joining a cluster's sums 2.5 us more; see gemm_block.cu).
 int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (m + 2 * kBpRows - 1) / (2 * kBpRows) * ((n + kBpCols - 1) / kBpCols);
   const int blocks = static_cast<int>(block_count(k));
   int split = 1, fit = 0;
   if (split_of(tiles, blocks, &split, &fit) != cudaSuccess || fit < 1) return INT64_MAX;
-  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 450 + 2000) + 6000 + (split > 1 ? 4000 : 0);
+  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 405 + 2800) + 6000 + (split > 1 ? 2500 : 0);
 }
 
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
