@@ -13,10 +13,6 @@
 // where a row has several warps) and each block's maximum (three shuffles).
 // CTAs are persistent and hold the next row's x and res in registers while
 // they reduce and write the current one.
-#include <map>
-#include <mutex>
-#include <tuple>
-
 #include "block_scale.cuh"
 #include "kernels.h"
 
@@ -150,25 +146,6 @@ __global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const 
       if (live && t % kSegLanes == 0 && block < blocks) a.scales[row * blocks + block] = s;
     }
   }
-}
-
-// CTAs of `kern` that fit on the GPU at once, by device (a persistent grid's size).
-template <typename K>
-int64_t resident(K kern, int threads) {
-  static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int>, int64_t> known;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  int64_t& n = known[std::make_tuple(reinterpret_cast<const void*>(kern), threads, dev)];
-  if (n == 0) {
-    int sms = 0, per_sm = 0;
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
-    cudaGetLastError();
-    n = static_cast<int64_t>(sms < 1 ? 1 : sms) * per_sm;
-  }
-  return n;
 }
 
 template <int MODE, bool GATED, int NS, bool AHEAD>

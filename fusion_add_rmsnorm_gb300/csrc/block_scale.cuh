@@ -11,6 +11,10 @@
 // code * scale is never a finite number that stands for neither.
 #pragma once
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "block.h"
 #include "common.cuh"
 
@@ -32,6 +36,13 @@ GBF_DEVICE float amax8(const float (&v)[8], float m) {
   return m;
 }
 
+// The same of eight packed bf16, in bf16: exact, and without widening them.
+GBF_DEVICE float amax8(uint4 v, float m) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+  const __nv_bfloat162 a = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+  return max_nan(max_nan(__low2float(a), __high2float(a)), m);
+}
+
 // Maximum over the aligned eight lanes of a block; every lane of the warp takes part.
 GBF_DEVICE float seg_max(float m) {
 #pragma unroll
@@ -47,6 +58,25 @@ GBF_DEVICE uint2 codes8(const float (&v)[8], float r) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
   return f32x8_to_e4m3x8(q);
+}
+
+// CTAs of `kern` that fit on the GPU at once, by device (a persistent grid's size).
+template <typename K>
+int64_t resident(K kern, int threads) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, int64_t> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  int64_t& n = known[std::make_tuple(reinterpret_cast<const void*>(kern), threads, dev)];
+  if (n == 0) {
+    int sms = 0, per_sm = 0;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+    cudaGetLastError();
+    n = static_cast<int64_t>(sms < 1 ? 1 : sms) * per_sm;
+  }
+  return n;
 }
 
 }  // namespace gbf

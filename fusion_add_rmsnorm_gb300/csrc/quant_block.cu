@@ -10,14 +10,15 @@
 // block waits for another.  The blocks of all rows are one list that groups of
 // eight lanes walk with the grid's stride; a group's place in the row moves on
 // by a stride that the host has split into rows and blocks, so nothing is
-// divided in the loop.
+// divided in the loop.  CTAs are persistent, and the next block's vectors are on
+// their way while this one's are reduced and written.
 #include "block_scale.cuh"
 #include "kernels.h"
 
 namespace gbf {
 namespace {
 
-constexpr int kQbThreads = 128;
+constexpr int kQbThreads = 256;
 constexpr int kQbGroups = kQbThreads / kSegLanes;
 
 // act(g) in float32.  SiLU and the tanh GELU (g times the logistic function of
@@ -34,8 +35,22 @@ GBF_DEVICE float gate_of(float g) {
   return g * __fdividef(z >= 0.0f ? 1.0f : e, 1.0f + e);
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(kQbThreads) quant_rows_kernel(const QuantBlockArgs a) {
+// 32 contiguous bytes that stay out of L1: one load where they are aligned to
+// their size (WIDE), else two.
+template <bool WIDE>
+GBF_DEVICE void ld_stream32(const void* p, uint4 (&v)[2]) {
+  if (WIDE) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                 : "l"(p));
+  } else {
+    v[0] = ld_stream(p);
+    v[1] = ld_stream(static_cast<const uint4*>(p) + 1);
+  }
+}
+
+template <int ACT, bool WIDE>
+__global__ void __launch_bounds__(kQbThreads, ACT == kActNone ? 6 : 5) quant_rows_kernel(const QuantBlockArgs a) {
   constexpr bool GATED = ACT != kActNone;
   const int l = threadIdx.x & (kSegLanes - 1);
   const int blocks = static_cast<int>(block_count(a.d));
@@ -45,75 +60,82 @@ __global__ void __launch_bounds__(kQbThreads) quant_rows_kernel(const QuantBlock
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
   pdl_wait();
   pdl_launch_dependents();
-  // a warp's four groups leave together: its first one is the last to run out
   const int64_t total = a.rows * blocks, stride = static_cast<int64_t>(gridDim.x) * kQbGroups;
-  for (int64_t at = first; at - ((threadIdx.x & 31) / kSegLanes) < total; at += stride) {
-    const bool live = at < total;
-    const __nv_bfloat16* g = x + row * a.d * (GATED ? 2 : 1);
-    uint4 v[kSegVecs] = {}, u[kSegVecs] = {};
-    int64_t col[kSegVecs];
-    bool in[kSegVecs];
+  // column of vector k of a block (a width is whole pairs of vectors)
+  auto column = [&](int b, int k) { return static_cast<int64_t>(b) * kBlockCols + (l * kSegVecs + k) * 8; };
+  uint4 v[kSegVecs] = {}, u[kSegVecs] = {};
+  auto load = [&](int64_t at, int64_t r, int b) {
+    const __nv_bfloat16* g = x + r * a.d * (GATED ? 2 : 1);
+    if (at < total && column(b, 0) < a.d) {
+      ld_stream32<WIDE>(g + column(b, 0), v);
+      if (GATED) ld_stream32<WIDE>(g + a.d + column(b, 0), u);
+    } else {                                                  // behind the row's end: zeros
 #pragma unroll
-    for (int k = 0; k < kSegVecs; ++k) {
-      col[k] = static_cast<int64_t>(block) * kBlockCols + (l + k * kSegLanes) * 8;
-      in[k] = live && col[k] < a.d;
-      if (in[k]) {
-        v[k] = ld_stream(g + col[k]);
-        if (GATED) u[k] = ld_stream(g + a.d + col[k]);
-      }
+      for (int k = 0; k < kSegVecs; ++k) v[k] = u[k] = uint4{};
     }
+  };
+  load(first, row, block);
+  // a warp's groups go on together, as long as its first one has a block
+  for (int64_t at = first; at - (threadIdx.x & 31) / kSegLanes < total; at += stride) {
     float y[kSegVecs][8], m = 0.0f;
+    uint4 own[kSegVecs], up[kSegVecs];
 #pragma unroll
     for (int k = 0; k < kSegVecs; ++k) {
-      bf16x8_to_f32(v[k], y[k]);
-      if (GATED) {
-        float up[8];
-        bf16x8_to_f32(u[k], up);
+      own[k] = v[k];
+      up[k] = u[k];
+    }
+    int64_t next_row = row + a.step_rows;
+    int next = block + a.step_blocks;
+    if (next >= blocks) {
+      next -= blocks;
+      ++next_row;
+    }
+    load(at + stride, next_row, next);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[k][i] = gate_of<ACT>(y[k][i]) * up[i];
+    for (int k = 0; k < kSegVecs; ++k) {
+      bf16x8_to_f32(own[k], y[k]);
+      if (GATED) {
+        float w[8];
+        bf16x8_to_f32(up[k], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[k][i] = gate_of<ACT>(y[k][i]) * w[i];
       }
-      m = amax8(y[k], m);                                     // a vector behind the row's end is zeros
+      m = GATED ? amax8(y[k], m) : amax8(own[k], m);
     }
     const float s = scale_of(seg_max(m)), r = __frcp_rn(s);
-#pragma unroll
-    for (int k = 0; k < kSegVecs; ++k)
-      if (in[k]) *reinterpret_cast<uint2*>(a.q_out + row * a.d + col[k]) = codes8(y[k], r);
-    if (live && l == 0) a.scales[row * blocks + block] = s;
-    row += a.step_rows;
-    block += a.step_blocks;
-    if (block >= blocks) {
-      block -= blocks;
-      ++row;
+    if (at < total && column(block, 0) < a.d) {
+      const uint2 c0 = codes8(y[0], r), c1 = codes8(y[1], r);
+      st_16(a.q_out + row * a.d + column(block, 0), make_uint4(c0.x, c0.y, c1.x, c1.y));
     }
+    if (at < total && l == 0) a.scales[row * blocks + block] = s;
+    row = next_row;
+    block = next;
   }
 }
 
-// A weight's 128 x 128 blocks, one a CTA: 256 threads hold the block (eight
-// vectors each, 16 rows apart), so it is read once.
+// A weight's 128 x 128 blocks, one a CTA: 256 threads hold the block (16 columns
+// of four rows each, 32 rows apart), so it is read once.
 constexpr int kQtThreads = 256;
-constexpr int kQtRows = kQtThreads / (kBlockCols / 8);        // rows of one pass
-constexpr int kQtVecs = kBlockCols / kQtRows;
+constexpr int kQtRows = kQtThreads / kSegLanes;               // rows of one pass
+constexpr int kQtPasses = kBlockCols / kQtRows;
 
-__global__ void __launch_bounds__(kQtThreads) quant_tiles_kernel(const QuantBlockArgs a) {
+template <bool WIDE>
+__global__ void __launch_bounds__(kQtThreads, 4) quant_tiles_kernel(const QuantBlockArgs a) {
   __shared__ float part[kQtThreads / 32];
   const int64_t across = block_count(a.d);
   const int64_t up = blockIdx.x / across, over = blockIdx.x - up * across;
-  const int64_t col = over * kBlockCols + (threadIdx.x % (kBlockCols / 8)) * 8;
-  const int64_t row0 = up * kBlockCols + threadIdx.x / (kBlockCols / 8);
+  const int64_t col = over * kBlockCols + threadIdx.x % kSegLanes * 16;
+  const int64_t row0 = up * kBlockCols + threadIdx.x / kSegLanes;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
   pdl_wait();
   pdl_launch_dependents();
-  uint4 v[kQtVecs] = {};
+  uint4 v[kQtPasses][kSegVecs] = {};
 #pragma unroll
-  for (int k = 0; k < kQtVecs; ++k)
-    if (row0 + k * kQtRows < a.rows && col < a.d) v[k] = ld_stream(x + (row0 + k * kQtRows) * a.d + col);
+  for (int k = 0; k < kQtPasses; ++k)
+    if (row0 + k * kQtRows < a.rows && col < a.d) ld_stream32<WIDE>(x + (row0 + k * kQtRows) * a.d + col, v[k]);
   float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kQtVecs; ++k) {
-    float y[8];
-    bf16x8_to_f32(v[k], y);
-    m = amax8(y, m);
-  }
+  for (int k = 0; k < kQtPasses; ++k) m = amax8(v[k][0], amax8(v[k][1], m));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -122,26 +144,29 @@ __global__ void __launch_bounds__(kQtThreads) quant_tiles_kernel(const QuantBloc
   for (int w = 0; w < kQtThreads / 32; ++w) m = max_nan(m, part[w]);
   const float s = scale_of(m), r = __frcp_rn(s);
 #pragma unroll
-  for (int k = 0; k < kQtVecs; ++k)
+  for (int k = 0; k < kQtPasses; ++k)
     if (row0 + k * kQtRows < a.rows && col < a.d) {
-      float y[8];
-      bf16x8_to_f32(v[k], y);
-      *reinterpret_cast<uint2*>(a.q_out + (row0 + k * kQtRows) * a.d + col) = codes8(y, r);
+      float y0[8], y1[8];
+      bf16x8_to_f32(v[k][0], y0);
+      bf16x8_to_f32(v[k][1], y1);
+      const uint2 c0 = codes8(y0, r), c1 = codes8(y1, r);
+      st_16(a.q_out + (row0 + k * kQtRows) * a.d + col, make_uint4(c0.x, c0.y, c1.x, c1.y));
     }
   if (threadIdx.x == 0) a.scales[blockIdx.x] = s;
 }
 
-template <int ACT>
-cudaError_t launch_rows(QuantBlockArgs a, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+template <int ACT, bool WIDE>
+cudaError_t launch_wide(QuantBlockArgs a, cudaStream_t stream) {
   const int64_t blocks = block_count(a.d), need = (a.rows * blocks + kQbGroups - 1) / kQbGroups;
-  // at most 16 CTAs per SM; what fewer registers would allow is not needed to fill HBM
-  const int64_t grid = need < 16LL * sms ? need : 16LL * sms;
+  const int64_t fit = resident(quant_rows_kernel<ACT, WIDE>, kQbThreads), grid = need < fit ? need : fit;
   a.step_rows = grid * kQbGroups / blocks;
   a.step_blocks = static_cast<int>(grid * kQbGroups % blocks);
-  return launch_pdl(quant_rows_kernel<ACT>, dim3(static_cast<unsigned>(grid)), dim3(kQbThreads), 0, stream, a);
+  return launch_pdl(quant_rows_kernel<ACT, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(kQbThreads), 0, stream, a);
+}
+
+template <int ACT>
+cudaError_t launch_rows(const QuantBlockArgs& a, cudaStream_t stream) {
+  return reinterpret_cast<uintptr_t>(a.x) % 32 == 0 ? launch_wide<ACT, true>(a, stream) : launch_wide<ACT, false>(a, stream);
 }
 
 }  // namespace
@@ -158,7 +183,8 @@ cudaError_t launch_quant_rows(QuantBlockArgs a, cudaStream_t stream) {
 
 cudaError_t launch_quant_tiles(const QuantBlockArgs& a, cudaStream_t stream) {
   const int64_t tiles = block_count(a.rows) * block_count(a.d);
-  return launch_pdl(quant_tiles_kernel, dim3(static_cast<unsigned>(tiles)), dim3(kQtThreads), 0, stream, a);
+  auto kern = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 ? quant_tiles_kernel<true> : quant_tiles_kernel<false>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(kQtThreads), 0, stream, a);
 }
 
 }  // namespace gbf
