@@ -39,10 +39,16 @@ GBF_DEVICE uint4 residual(uint4 g, uint4 x, uint4 r) {
   return o;
 }
 
-// NS blocks a lane group; AHEAD: factors in registers and the next row's loads
-// in flight (rows of up to 16,384 columns), else both are loaded where they are used.
-template <int MODE, bool GATED, int NS, bool AHEAD>
-__global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const AddRmsNormBlockArgs a) {
+// NS blocks a lane group.  One or two: the next row's loads are in flight while
+// this one is reduced and written; four: they begin with the row.  The factors
+// are held in registers but for AdaRMSNorm's at two blocks and all at four, which
+// are read from L1 where they are used (16384 x 8192 gated AdaRMSNorm: 149 us, held
+// and spilled 181).  CTAS: an SM's at one block a lane group, three for streaming
+// (32768 x 4096: 143 us, two 150), two for fewer rows (777 x 2736: 3.8 us, three 4.4).
+template <int MODE, bool GATED, int NS, int CTAS>
+__global__ void __launch_bounds__(NS == 1 ? kNbThreads / 2 : kNbThreads, CTAS)
+add_rmsnorm_block_kernel(const AddRmsNormBlockArgs a) {
+  constexpr bool AHEAD = NS <= 2, HELD = NS == 1 || (NS == 2 && MODE != kNormAda);
   constexpr int NV = NS * kSegVecs, NF = factors<MODE, GATED>();
   const int tpr = a.tpr, rows_per_cta = blockDim.x / tpr;
   const int t = threadIdx.x % tpr;
@@ -73,13 +79,13 @@ __global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const 
       }
   };
   if (AHEAD) load_row(row);
-  uint4 held[AHEAD ? NV : 1][NF > 0 ? NF : 1] = {};
-  if (AHEAD)
+  uint4 held[HELD ? NV : 1][NF > 0 ? NF : 1] = {};
+  if (HELD)
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int j = 0; j < NF; ++j)
-        if (column(k) < hidden) held[AHEAD ? k : 0][j] = factor(j, k);
+        if (column(k) < hidden) held[HELD ? k : 0][j] = factor(j, k);
   pdl_launch_dependents();
 
   // Partial sums of a row's warps, two copies by trip parity: a warp that
@@ -96,7 +102,7 @@ __global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const bool in = live && column(k) < hidden;
-      const uint4 g = !GATED ? uint4{} : AHEAD ? held[AHEAD ? k : 0][0] : in ? factor(0, k) : uint4{};
+      const uint4 g = !GATED ? uint4{} : HELD ? held[HELD ? k : 0][0] : in ? factor(0, k) : uint4{};
       h[k] = in ? residual<GATED>(g, xr[k], rr[k]) : uint4{};
       if (in) st_16(res_out + row * hidden + column(k), h[k]);
       float f[8];
@@ -125,8 +131,8 @@ __global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const 
         float f0[8], f1[8];
         if (MODE != kNormNoWeight) {
           const int j1 = MODE == kNormAda ? F + 1 : F;
-          bf16x8_to_f32(AHEAD ? held[AHEAD ? k : 0][F] : in ? factor(F, k) : uint4{}, f0);
-          bf16x8_to_f32(AHEAD ? held[AHEAD ? k : 0][j1] : in ? factor(j1, k) : uint4{}, f1);
+          bf16x8_to_f32(HELD ? held[HELD ? k : 0][F] : in ? factor(F, k) : uint4{}, f0);
+          bf16x8_to_f32(HELD ? held[HELD ? k : 0][j1] : in ? factor(j1, k) : uint4{}, f1);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -148,9 +154,9 @@ __global__ void __launch_bounds__(kNbThreads, 1) add_rmsnorm_block_kernel(const 
   }
 }
 
-template <int MODE, bool GATED, int NS, bool AHEAD>
+template <int MODE, bool GATED, int NS, int CTAS>
 cudaError_t launch(const AddRmsNormBlockArgs& a, int threads, cudaStream_t stream) {
-  auto kern = add_rmsnorm_block_kernel<MODE, GATED, NS, AHEAD>;
+  auto kern = add_rmsnorm_block_kernel<MODE, GATED, NS, CTAS>;
   const int rows_per_cta = threads / a.tpr;
   const int64_t need = (a.rows + rows_per_cta - 1) / rows_per_cta, fit = resident(kern, threads);
   return launch_pdl(kern, dim3(static_cast<unsigned>(need < fit ? need : fit)), dim3(threads), 0, stream, a);
@@ -168,9 +174,13 @@ cudaError_t launch_plan(AddRmsNormBlockArgs a, cudaStream_t stream) {
   if (need > 32) tpr = static_cast<int>((need + 31) / 32 * 32);
   a.tpr = tpr;
   const int threads = tpr > 32 ? tpr : 128;
-  if (ns == 1) return launch<MODE, GATED, 1, true>(a, threads, stream);
-  if (ns == 2) return launch<MODE, GATED, 2, true>(a, threads, stream);
-  return launch<MODE, GATED, 4, false>(a, threads, stream);
+  if (ns == 4) return launch<MODE, GATED, 4, 1>(a, threads, stream);
+  if (ns == 2) return launch<MODE, GATED, 2, 1>(a, threads, stream);
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const bool streaming = a.rows / (threads / tpr) > 8LL * sms;          // over eight CTAs an SM
+  return streaming ? launch<MODE, GATED, 1, 3>(a, threads, stream) : launch<MODE, GATED, 1, 2>(a, threads, stream);
 }
 
 }  // namespace
