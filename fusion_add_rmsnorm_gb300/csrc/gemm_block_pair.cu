@@ -68,9 +68,13 @@ constexpr int kBpChunkRow = kBpRows + 2;
 struct __align__(16) BpScales {
   float x[kBpChunk * kBpChunkRow];
   float w[2][kBpChunk];
-  __nv_bfloat16 bias[kBpCols];                  // of the tile whose first chunk this is
 };
-static_assert(sizeof(float) * kBpChunk * kBpChunkRow % 16 == 0, "bias is read as 16-byte vectors");
+// The biases of this tile's channels and of the next one's, by the tile's parity:
+// they are written with a tile's first scales and read at its end, when its first
+// scales' place may already hold the next tile's.
+struct __align__(16) BpBias {
+  __nv_bfloat16 of[2][kBpCols];
+};
 
 struct __align__(8) BpCtl {
   uint64_t full[kBpStages];
@@ -86,7 +90,7 @@ struct __align__(8) BpCtl {
 };
 
 constexpr size_t kBpSmem = 1024 /* alignment */ + kBpStages * kBpStageBytes + kBpEpilogueWarps * 2 * kBpBoxBytes +
-                           2 * sizeof(BpScales) + sizeof(BpCtl);
+                           2 * sizeof(BpScales) + sizeof(BpBias) + sizeof(BpCtl);
 static_assert(kBpSmem <= 232448, "227 KB a CTA");
 static_assert(kBpRows * kBpCols * 4 <= kBpStages * kBpStageBytes, "partial sums fit the ring");
 static_assert(kBpChunk * kBpRows % 32 == 0 && kBpChunk == 16, "a lane's share of the scales");
@@ -229,7 +233,8 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
   uint8_t* smem_w = smem + S * kBpRows * BK_BYTES;
   uint8_t* smem_out = smem + S * kBpStageBytes;
   BpScales* scales = reinterpret_cast<BpScales*>(smem_out + kBpEpilogueWarps * 2 * kBpBoxBytes);
-  BpCtl* ctl = reinterpret_cast<BpCtl*>(scales + 2);
+  BpBias* biases = reinterpret_cast<BpBias*>(scales + 2);
+  BpCtl* ctl = reinterpret_cast<BpCtl*>(biases + 1);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), odd = rank & 1, part = rank >> 1;
@@ -349,9 +354,9 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     } else {
       // ---------------------------------------------------------------- scales
       const int at = lane % kBpChunk, second = lane / kBpChunk;   // a lane's K block, and which rows
-      uint32_t chunk = 0;
+      uint32_t chunk = 0, turn = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
+      for (int tile = first; tile < tiles && ok; tile += stride, turn ^= 1) {
         int m0, n0;
         bp_origin(p, odd, tile, m0, n0);
         for (int kb = kb_begin; kb < kb_end; kb += kBpChunk, ++chunk) {
@@ -365,7 +370,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           async_copy<4>(&sc.w[second][at], p.w_scales + (has ? static_cast<int64_t>(n / kBlockCols) * p.blocks + kb + at : 0), has);
           if (kb == kb_begin) {
             const bool some = p.bias && n0 + lane * 8 < p.n;
-            async_copy<16>(&sc.bias[lane * 8], some ? static_cast<const void*>(p.bias + n0 + lane * 8) : p.y, some);
+            async_copy<16>(&biases->of[turn][lane * 8], some ? static_cast<const void*>(p.bias + n0 + lane * 8) : p.y, some);
           }
 #pragma unroll 8
           for (int r = second; r < kBpRows; r += 32 / kBpChunk) {
@@ -384,10 +389,10 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     const int col_at = (warp - kBpEpilogue) / 4 * kBpWarpCols, half = col_at / kBpHalf;
     const uint32_t taddr = tmem_base + col_at + (static_cast<uint32_t>(quarter * 32) << 16);
     uint8_t* box = smem_out + (warp - kBpEpilogue) * 2 * kBpBoxBytes;
-    uint32_t it = 0, chunk = 0, ready = 0;
+    uint32_t it = 0, chunk = 0, ready = 0, turn = 0;
     bool ok = true;
-    for (int tile = first; tile < tiles; tile += stride) {
-      const __nv_bfloat16* bias = scales[chunk & 1].bias + col_at;
+    for (int tile = first; tile < tiles; tile += stride, turn ^= 1) {
+      const __nv_bfloat16* bias = biases->of[turn] + col_at;
       float acc[kBpWarpCols];
 #pragma unroll
       for (int j = 0; j < kBpWarpCols; ++j) acc[j] = 0.0f;
@@ -429,7 +434,8 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           s_next = sx[after * kBpChunkRow] * sw[after];
           add_scaled(acc, 96, r1, ss);
         }
-        // the last chunk goes back once the tile's bias has been read
+        // the last chunk goes back once the tile's bias has been read: with one chunk a tile, the
+        // next but one's bias takes this one's place
         if (kb0 + kBpChunk < kb_end && lane == 0) mbar_arrive(&ctl->scales_empty[chunk & 1]);
       }
       if (p.split > 1) {

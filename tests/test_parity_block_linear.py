@@ -81,9 +81,11 @@ def test_activations(gbf, act, m):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (32, 1024, 16384), (7, 256, 32768), (96, 2048, 1536),
-                                   (333, 1000, 2736), (640, 2304, 1024), (1030, 520, 656), (2048, 4104, 256)])
+                                   (333, 1000, 2736), (640, 2304, 1024), (1030, 520, 656), (2048, 4104, 256),
+                                   (1024, 8192, 2304), (1040, 8200, 4224), (768, 12288, 2048)])
 def test_sizes(gbf, m, n, k):
-    """K cut over clusters, long and short K, more tiles than the GPU holds at once."""
+    """K cut over clusters, long and short K, more tiles than the GPU holds at once (with one, two and three
+    fillings of the scales' place to a tile, so that a tile's bias has to outlast them)."""
     c = case(m, n, k, m + n + k)
     check(run(gbf, c), c)
 
