@@ -671,15 +671,19 @@ def strip_comments(text):
 
 def kernel_source_hash(source):
     """First 16 hex digits of the SHA-256 of a kernel source followed by the
-    headers every kernel includes, comments and layout stripped (a change to
+    headers every kernel includes (and the tensor-core one where it is), comments and layout stripped (a change to
     the code of either invalidates its record; a comment edit does not)."""
     csrc = os.path.join(ROOT, "fusion_add_rmsnorm_gb300", "csrc")
     h = hashlib.sha256()
-    for name in (source, "common.cuh", "tma.cuh", "kernels.h"):
+    for name in (source, "common.cuh", "tma.cuh", "kernels.h", "tcgen05.cuh"):
         path = os.path.join(csrc, name)
         if not os.path.exists(path):
             return None
-        h.update(strip_comments(open(path, encoding="utf-8").read()).encode())
+        text = open(path, encoding="utf-8").read()
+        if name == source:
+            tensor = '#include "tcgen05.cuh"' in text       # the tensor-core kernels' header, for those that include it
+        if name != "tcgen05.cuh" or tensor:
+            h.update(strip_comments(text).encode())
     return h.hexdigest()[:16]
 
 

@@ -158,7 +158,7 @@ template <int MODE, bool GATED, int NS, int CTAS>
 cudaError_t launch(const AddRmsNormBlockArgs& a, int threads, cudaStream_t stream) {
   auto kern = add_rmsnorm_block_kernel<MODE, GATED, NS, CTAS>;
   const int rows_per_cta = threads / a.tpr;
-  const int64_t need = (a.rows + rows_per_cta - 1) / rows_per_cta, fit = resident(kern, threads);
+  const int64_t need = (a.rows + rows_per_cta - 1) / rows_per_cta, fit = resident<add_rmsnorm_block_kernel<MODE, GATED, NS, CTAS>>(threads);
   return launch_pdl(kern, dim3(static_cast<unsigned>(need < fit ? need : fit)), dim3(threads), 0, stream, a);
 }
 

@@ -11,9 +11,7 @@
 // code * scale is never a finite number that stands for neither.
 #pragma once
 
-#include <map>
-#include <mutex>
-#include <tuple>
+#include <atomic>
 
 #include "block.h"
 #include "common.cuh"
@@ -60,21 +58,23 @@ GBF_DEVICE uint2 codes8(const float (&v)[8], float r) {
   return f32x8_to_e4m3x8(q);
 }
 
-// CTAs of `kern` that fit on the GPU at once, by device (a persistent grid's size).
-template <typename K>
-int64_t resident(K kern, int threads) {
-  static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int>, int64_t> known;
+// CTAs of KERNEL with `threads` threads (a multiple of 32, at most 1024) that fit
+// on the GPU at once: a persistent grid's size.  Asked for once on each device.
+template <auto KERNEL>
+int64_t resident(int threads) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][33];
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  int64_t& n = known[std::make_tuple(reinterpret_cast<const void*>(kern), threads, dev)];
+  const bool keep = dev >= 0 && dev < kDevices;
+  int n = keep ? known[dev][threads / 32].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
     int sms = 0, per_sm = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
     cudaGetLastError();
-    n = static_cast<int64_t>(sms < 1 ? 1 : sms) * per_sm;
+    n = (sms < 1 ? 1 : sms) * per_sm;
+    if (keep) known[dev][threads / 32].store(n, std::memory_order_relaxed);
   }
   return n;
 }

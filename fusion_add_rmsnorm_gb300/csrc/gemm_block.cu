@@ -46,8 +46,9 @@ constexpr int kLbChunk = 8;               // K blocks whose scales are filled at
 
 // Shared memory of a CTA with NX rows of X, alone on K or one of a cluster
 // (SPLIT): two CTAs an SM up to 32 rows, so that the next call's comes beside
-// this one's; from 64 on a deeper ring is worth more.  No more accumulators than stages: the epilogue then waits for a
-// stage's MMAs before that stage can be through twice.
+// this one's; from 64 on a deeper ring is worth more.  No more accumulators than
+// stages: the epilogue then waits for a stage's MMAs before that stage can be
+// through twice.
 template <int NX, bool SPLIT>
 struct Lb {
   static constexpr int kPerSm = NX <= 32 ? 2 : 1;
@@ -109,13 +110,6 @@ GBF_DEVICE void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
 }
 
 GBF_DEVICE void st_cluster_f32(uint32_t a, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-
-// One lane of the (converged) warp.
-GBF_DEVICE bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 
 template <int NX, bool SPLIT>
 __global__ void __launch_bounds__(Lb<NX, SPLIT>::kThreads, Lb<NX, SPLIT>::kPerSm)
@@ -381,7 +375,7 @@ cudaError_t launch_split(const LinearBlockArgs& a, const LinearBlockParams& p, c
 
 template <int NX>
 cudaError_t launch_lb(const LinearBlockArgs& a, LinearBlockParams p, int sms, cudaStream_t stream, const char** why) {
-  p.m_tiles = (p.m + NX - 1) / NX;
+  p.m_tiles = static_cast<int>((a.m + NX - 1) / NX);
   p.split = split_of(static_cast<int64_t>(p.m_tiles) * p.n_tiles, p.blocks, sms);
   return p.split > 1 ? launch_split<NX, true>(a, p, stream, why) : launch_split<NX, false>(a, p, stream, why);
 }

@@ -118,13 +118,6 @@ GBF_DEVICE void bp_origin(const BlockPairParams& p, int odd, int tile, int& m0, 
   n0 = (g * p.group_n + i % width) * kBpCols;
 }
 
-// One lane of the (converged) warp.
-GBF_DEVICE bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 // The hardware barrier of accumulator b ([parity][half]): the half's epilogue
 // warps arrive once they have read it, the half's issuer (odd CTA: relay) waits
 // for all of them.

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kQtThreads, 4) quant_tiles_kernel(const QuantB
 template <int ACT, bool WIDE>
 cudaError_t launch_wide(QuantBlockArgs a, cudaStream_t stream) {
   const int64_t blocks = block_count(a.d), need = (a.rows * blocks + kQbGroups - 1) / kQbGroups;
-  const int64_t fit = resident(quant_rows_kernel<ACT, WIDE>, kQbThreads), grid = need < fit ? need : fit;
+  const int64_t fit = resident<quant_rows_kernel<ACT, WIDE>>(kQbThreads), grid = need < fit ? need : fit;
   a.step_rows = grid * kQbGroups / blocks;
   a.step_blocks = static_cast<int>(grid * kQbGroups % blocks);
   return launch_pdl(quant_rows_kernel<ACT, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(kQbThreads), 0, stream, a);

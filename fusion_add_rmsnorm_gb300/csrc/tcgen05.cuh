@@ -84,6 +84,13 @@ GBF_DEVICE void cluster_sync() {
 GBF_DEVICE void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 GBF_DEVICE void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of the (converged) warp.
+GBF_DEVICE bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Every tcgen05 instruction of one kernel names the same CTA group: 1 when
 // unpaired, 2 in a pair.
 template <bool PAIR>
