@@ -31,9 +31,7 @@
 // reach its barriers and TMEM is freed.
 #include <atomic>
 
-#include "block.h"
-#include "kernels.h"
-#include "tcgen05.cuh"
+#include "gemm_block.cuh"
 
 namespace gbf {
 namespace {
@@ -275,10 +273,12 @@ linear_block_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         st_cluster_f32(map_cluster(to + ((col0 + j) & (owned - 1)) * kLbRows * 4, (col0 + j) >> log), acc[j]);
     } else if (n0 + ch < p.n) {
       const float bias = p.bias ? __bfloat162float(p.bias[n0 + ch]) : 0.0f;
+      with_act(p.act, [&](auto ACT) {
 #pragma unroll
-      for (int j = 0; j < COLS; ++j)
-        if (m0 + col0 + j < p.m)
-          p.y[static_cast<int64_t>(m0 + col0 + j) * p.n + n0 + ch] = __float2bfloat16(fast_act(acc[j] + bias, p.act));
+        for (int j = 0; j < COLS; ++j)
+          if (m0 + col0 + j < p.m)
+            p.y[static_cast<int64_t>(m0 + col0 + j) * p.n + n0 + ch] = __float2bfloat16(fast_act(acc[j] + bias, ACT.value));
+      });
     }
   }
 
