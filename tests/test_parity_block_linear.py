@@ -153,3 +153,19 @@ def test_leading_dimensions_and_empty_batch(gbf):
     e = torch.empty(0, 256, dtype=torch.uint8, device="cuda")
     gbf.linear_fp8_block(e, torch.empty(0, 2, device="cuda"), t["wq"], t["w_scales"], t["bias"],
                          torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), act=0)
+
+
+@pytest.mark.parametrize("m,n,k", [((1 << 31) // 8192 + 300, 8192, 128), ((1 << 31) // 4096 + 300, 16, 4096)])
+def test_offsets_past_32_bits(gbf, m, n, k):
+    """The last rows of outputs, or inputs, of more than 2^31 elements."""
+    c = case(3, n, k, 5)
+    c["x_scales"][0, -1] = 1
+    t = tensors(c)
+    xq = torch.zeros(m, k, dtype=torch.uint8, device="cuda")
+    xs = torch.zeros(m, block.block_count(k), device="cuda")
+    xq[-3:], xs[-3:] = t["xq"], t["x_scales"]
+    y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    gbf.linear_fp8_block(xq, xs, t["wq"], t["w_scales"], t["bias"], y, act=0)
+    torch.cuda.synchronize()
+    check(bf16_decode(to_bits(y[-3:])), c)
+    assert torch.equal(y[0], t["bias"]) and torch.equal(y[m // 2], t["bias"])

@@ -258,6 +258,54 @@ def test_norm_zero_rows_have_the_least_scale(gbf):
     assert (scales == np.float32(2.0 ** -100)).all() and not codes.any()
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_inputs_on_sixteen_bytes_only(gbf, block_rows):
+    """A tensor that begins 16 bytes into a 32-byte line is read as well."""
+    rng = np.random.default_rng(11)
+    x = bits(rng, 37, 272)
+    for act in (None, *ACTS):
+        d = 272 if act is None else 136 - 8
+        v = x if act is None else np.ascontiguousarray(x[:, :2 * d])
+        raw = torch.empty(v.size + 8, dtype=torch.bfloat16, device="cuda")
+        t = raw[8:].view(*v.shape)
+        t.copy_(from_bits(v))
+        assert t.data_ptr() % 32 == 16
+        br = block_rows if act is None else 1
+        q = torch.empty(37, d, dtype=torch.uint8, device="cuda")
+        s = torch.empty(-(-37 // br), block.block_count(d), device="cuda")
+        if act is None:
+            gbf.quantize_fp8_block(t, q, s, block_rows=br)
+            same_bits((q.cpu().numpy(), s.cpu().numpy()), block.quantize(bf16_decode(v), br))
+        else:
+            gbf.gated_act_fp8_block(t, q, s, act=ACTS[act])
+            check_codes(q.cpu().numpy(), s.cpu().numpy(), *gated_ref(v, d, act))
+
+
+def test_offsets_past_32_bits(gbf):
+    """The last rows of tensors of more than 2^31 elements."""
+    rows, d = (1 << 31) // 8192 + 300, 8192
+    rng = np.random.default_rng(12)
+    last = {k: bits(rng, 3, d) for k in ("x", "res")}
+    x, res = (torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-3:], res[-3:] = from_bits(last["x"]), from_bits(last["res"])
+    q = torch.empty(rows, d, dtype=torch.uint8, device="cuda")
+    s = torch.empty(rows, d // 128, device="cuda")
+    gbf.quantize_fp8_block(x, q, s)
+    same_bits((q[-3:].cpu().numpy(), s[-3:].cpu().numpy()), block.quantize(bf16_decode(last["x"])))
+    tiles = torch.empty(-(-rows // 128), d // 128, device="cuda")
+    gbf.quantize_fp8_block(x, q, tiles, block_rows=128)
+    tail = np.zeros((rows % 128, d), np.uint16)
+    tail[-3:] = last["x"]
+    ref = block.quantize(bf16_decode(tail), 128)
+    same_bits((q[-3:].cpu().numpy(), tiles[-1:].cpu().numpy()), (ref[0][-3:], ref[1]))
+    gbf.add_rmsnorm_fp8_block(x, res, res, q, s, gbf.NORM_NOWEIGHT)
+    check_norm((to_bits(res[-3:]), q[-3:].cpu().numpy(), s[-3:].cpu().numpy()), last)
+    gbf.gated_act_fp8_block(x.view(rows // 2, 2 * d), q[:rows // 2], s[:rows // 2], act=ACTS["silu"])
+    v = np.zeros((1, 2 * d), np.uint16)
+    v[0, :d], v[0, d:] = last["x"][1], last["x"][2]
+    check_codes(q[rows // 2 - 1:rows // 2].cpu().numpy(), s[rows // 2 - 1:rows // 2].cpu().numpy(), *gated_ref(v, d, "silu"))
+
+
 def test_streams_and_graph(gbf):
     """Captured on another stream and replayed on new inputs; two calls at once on two streams."""
     a, b = (norm_case(64, 1040, 0, False, s) for s in (1, 2))
