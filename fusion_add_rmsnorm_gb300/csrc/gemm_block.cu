@@ -331,15 +331,16 @@ int split_of(int64_t tiles, int blocks, int sms) {
 
 // About how long this kernel takes with NX = 64 or 128, which with
 // linear_block_pair_ns() decides who takes a call of more than 32 rows.
-// Measured: a K block of a tile 280 or 345 ns, its start and end 2.5 us, joining
+// Measured: a K block of a tile 270 or 335 ns, its start and end 2.2 us, joining
 // a cluster's sums 1.5 or 3 us more.  The estimates against the measured times
-// (us; 64 rows a tile, 128, pairs), N x K = 4096 x 4096: 128 rows 7.2 / 9.0, 8.3 /
-// 9.1, 13.9 / 18; 512 rows 22.9 / 21.4, 13.5 / 13.4, 17.8 / 19; 1024 rows 34 / 46,
-// 27 / 31, 21.8 / 21.7.  16384 x 4096, 256 rows: 45 / 44, 27 / 27.8, 21.8 / 23.7.
+// (us; 64 rows a tile, 128, pairs), N x K = 4096 x 4096: 128 rows 8.0 / 9.0, 7.9 /
+// 9.1, 14.3 / 16; 512 rows 21.7 / 21.4, 12.9 / 13.3, 17.4 / 18; 1024 rows 43.4 / 46,
+// 25.8 / 26, 19.7 / 19.3.  16384 x 4096, 256 rows: 43.4 / 44, 25.8 / 27.6, 19.7 / 21.9.
+// 4096 x 11008, 333 rows: 50.8 / 47, 31.0 / 29.7, 28.0 / 28.0.
 int64_t thin_ns(int64_t m, int nx, const LinearBlockParams& p, int sms) {
   const int64_t tiles = (m + nx - 1) / nx * p.n_tiles, waves = (tiles + sms - 1) / sms;
   const int split = split_of(tiles, p.blocks, sms);
-  return waves * (2500 + (p.blocks + split - 1) / split * (nx == 64 ? 280 : 345)) +
+  return waves * (2200 + (p.blocks + split - 1) / split * (nx == 64 ? 270 : 335)) +
          (split > 1 ? (nx == 64 ? 1500 : 3000) : 0);
 }
 

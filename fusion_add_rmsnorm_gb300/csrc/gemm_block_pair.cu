@@ -152,6 +152,18 @@ GBF_DEVICE void async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// X's scales of a tile's rows and of kBpChunk K blocks from kb on, by `threads`
+// threads (a multiple of kBpChunk) of which this is `t`.  Rows and K blocks outside
+// have none: zeros, and what they sum is not stored.
+GBF_DEVICE void fill_x(const BlockPairParams& p, BpScales& sc, int m0, int kb, int kb_end, int t, int threads) {
+  const int at = t % kBpChunk;
+#pragma unroll 8
+  for (int r = t / kBpChunk; r < kBpRows; r += threads / kBpChunk) {
+    const bool has = kb + at < kb_end && m0 + r < p.m;
+    async_copy<4>(&sc.x[at * kBpChunkRow + r], p.x_scales + (has ? static_cast<int64_t>(m0 + r) * p.blocks + kb + at : 0), has);
+  }
+}
+
 // 32 float32 columns of this warp's TMEM lanes, not waited for.
 GBF_DEVICE void tmem_ld_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -354,7 +366,6 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           ok = mbar_wait_warp(&ctl->scales_empty[chunk & 1], ((chunk >> 1) & 1) ^ 1u, &ctl->abort, p.err);
           if (!ok) break;
           const bool in = kb + at < kb_end;
-          // rows and channels outside have no scales: zeros, and what they sum is not stored
           const int n = n0 + second * kBlockCols;
           const bool has = in && n < p.n;
           async_copy<4>(&sc.w[second][at], p.w_scales + (has ? static_cast<int64_t>(n / kBlockCols) * p.blocks + kb + at : 0), has);
@@ -362,11 +373,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
             const bool some = p.bias && n0 + lane * 8 < p.n;
             async_copy<16>(&biases->of[turn][lane * 8], some ? static_cast<const void*>(p.bias + n0 + lane * 8) : p.y, some);
           }
-#pragma unroll 8
-          for (int r = second; r < kBpRows; r += 32 / kBpChunk) {
-            const bool row = in && m0 + r < p.m;
-            async_copy<4>(&sc.x[at * kBpChunkRow + r], p.x_scales + (row ? static_cast<int64_t>(m0 + r) * p.blocks + kb + at : 0), row);
-          }
+          if (chunk > 0) fill_x(p, sc, m0, kb, kb_end, lane, 32);   // the first is the epilogue's
           async_arrive(&ctl->scales_full[chunk & 1]);
         }
       }
@@ -381,6 +388,15 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     uint8_t* box = smem_out + (warp - kBpEpilogue) * 2 * kBpBoxBytes;
     uint32_t it = 0, chunk = 0, ready = 0, turn = 0;
     bool ok = true;
+    if (first < tiles) {
+      // The first scales of X are filled here, by eight warps that have nothing to do yet: one warp takes
+      // 2,000 cycles longer, later ones are filled ahead.
+      int m0, n0;
+      bp_origin(p, odd, first, m0, n0);
+      fill_x(p, scales[0], m0, kb_begin, kb_end, threadIdx.x - kBpEpilogue * 32, kBpEpilogueWarps * 32);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(kBpEpilogueWarps * 32) : "memory");
+    }
     for (int tile = first; tile < tiles; tile += stride, turn ^= 1) {
       const __nv_bfloat16* bias = biases->of[turn] + col_at;
       float acc[kBpWarpCols];
@@ -484,16 +500,16 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->scales_empty[(chunk - 1) & 1]);
     }
-    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                           // issue counts and partial sums are in place
-  if (warp == 0 && lane == 0 && !odd) {
-    // Every copy to either CTA has landed before they leave.  After an abort the
-    // producers may stand one K block apart on a stage: the phase that only one
-    // of them filled is completed by hand.
+  if (warp >= kBpEpilogue && lane == 0) bulk_wait_all();    // the stores have left shared memory
+  if (warp == 0 && lane == 0 && !odd && *reinterpret_cast<volatile int*>(&ctl->abort)) {
+    // Every copy to either CTA has landed before they leave: its MMAs are done, or,
+    // after an abort, it is waited for.  The producers may then stand one K block
+    // apart on a stage: the phase that only one of them filled is completed by hand.
     int own = 0;
     for (int s = 0; s < S; ++s) {
       const uint32_t mine = (issued + S - 1 - s) / S, theirs = (ctl->peer_issued + S - 1 - s) / S;   // on this stage
@@ -585,14 +601,14 @@ cudaError_t split_of(int64_t tiles, int blocks, int* split, int* fit) {
 
 }  // namespace
 
-// About how long a call takes here (measured: a K block 405 ns, a tile's end 2.8 us,
-// the call's start and end 6 us, joining a cluster's sums 2.5 us more; see gemm_block.cu).
+// About how long a call takes here (measured: a K block 390 ns, a tile's end 2.2 us,
+// the call's start and end 5 us, joining a cluster's sums 4 us more; see gemm_block.cu).
 int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (m + 2 * kBpRows - 1) / (2 * kBpRows) * ((n + kBpCols - 1) / kBpCols);
   const int blocks = static_cast<int>(block_count(k));
   int split = 1, fit = 0;
   if (split_of(tiles, blocks, &split, &fit) != cudaSuccess || fit < 1) return INT64_MAX;
-  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 405 + 2800) + 6000 + (split > 1 ? 2500 : 0);
+  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 390 + 2200) + 5000 + (split > 1 ? 4000 : 0);
 }
 
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
