@@ -19,7 +19,7 @@
 namespace gbf {
 
 constexpr int kSegLanes = 8;              // lanes that hold a block of 128 columns, two 8-column vectors each
-constexpr int kSegVecs = 2;               // lane l has vectors l and l + 8: loads of 128 contiguous bytes
+constexpr int kSegVecs = 2;               // which two of the block's sixteen, each kernel says
 
 // The larger of two values, NaN if either is.
 GBF_DEVICE float max_nan(float a, float b) {

@@ -19,7 +19,7 @@
 //              warp walks the loop, which keeps the descriptors in uniform
 //              registers; one lane issues)
 //   warps 2-3  the X scales of 8 K blocks ahead, times W's; warp 2 tensor memory
-//   warps 4...  epilogue, 32 channels and up to 64 rows of X each
+//   warps 4...  epilogue, 32 channels and 16 or 32 rows of X each
 // With few output tiles, a cluster of up to eight CTAs cuts K between them.  Each
 // owns NX / split of the tile's rows of X, gets the others' sums of them by remote
 // stores and adds them in the order of K, so that a result has the same bits in

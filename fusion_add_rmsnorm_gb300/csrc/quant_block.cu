@@ -6,8 +6,9 @@
 // Bound: HBM.  An element is 2 bytes read (4 with a gate) and 1 written, a
 // block 4 bytes more.
 //
-// Rows: eight lanes hold a block, so its maximum is three shuffles and no
-// block waits for another.  The blocks of all rows are one list that groups of
+// Rows: eight lanes hold a block, two neighbouring vectors each (one 32-byte load
+// and one 16-byte store), so its maximum is three shuffles and no block waits for
+// another.  The blocks of all rows are one list that groups of
 // eight lanes walk with the grid's stride; a group's place in the row moves on
 // by a stride that the host has split into rows and blocks, so nothing is
 // divided in the loop.  CTAs are persistent.  With an activation the next block's
@@ -30,7 +31,8 @@ constexpr int kQbGroups = kQbThreads / kSegLanes;
 // argument, so that nothing overflows on the way.
 //
 // The erf GELU is g Phi(g), Phi(g) = erfc(-g / sqrt 2) / 2.  With z = |g| / sqrt 2
-// and t = 1 / (1 + z / 2), erfc(z) = t exp(-z^2 + P(t)), where P is a polynomial
+// and t = 1 / (1 + z / 2), erfc(z) = t exp(-z^2 + P(t)) (the form of Press et al.,
+// Numerical Recipes, 6.2; the fit is this library's), where P is a polynomial
 // of degree 8 fitted to log(erfc(z) exp(z^2) / t) at Chebyshev nodes of t for z up
 // to 9.6 (relative error 2.4e-7, 3.8e-7 with the coefficients and Horner's steps
 // in float32; from z = 9.4 on the exponential is below float32's range).
