@@ -63,6 +63,11 @@ struct Lb {
   static constexpr int kAccs = kStages < 512 / kPerSm / NX ? kStages : 512 / kPerSm / NX;
   static constexpr int kTmemCols = kAccs * NX <= 32 ? 32 : kAccs * NX <= 64 ? 64 : kAccs * NX <= 128 ? 128 : kAccs * NX <= 256 ? 256 : 512;
   static_assert(kStages >= 3 && kAccs >= 3, "stages and accumulators in flight");
+  // A CTA that waits for tensor memory while one of its cluster waits for it could wait for ever, where
+  // two clusters each hold what the other asks for.  So an SM's shared memory never admits CTAs whose
+  // columns sum to more than 512: two of these at most, and none beside a Linear on its own SM (180 KB or more).
+  static constexpr int kSmem = kStages * kStageBytes + kPartBytes + kScaleBytes;
+  static_assert(kPerSm * kTmemCols <= 512 && kSmem > (kPerSm == 2 ? 228 * 1024 / 3 : 228 * 1024 / 2), "tensor memory for all CTAs of an SM");
 };
 
 template <int S, int A>

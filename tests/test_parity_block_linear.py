@@ -7,6 +7,8 @@ rounding to nearest, in case the tensor core cuts off).  The activations' slope
 is below 1.13; the hardware tanh is off by 2^-10.9, so the tanh GELU by
 |a| 2^-11.9, and the other forms by 2^-20 of |a|.  Then one bf16 rounding.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -142,6 +144,56 @@ def test_streams_and_graph(gbf, m):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, y)
+    assert gbf.device_status()[0] == 0
+
+
+def test_calls_of_all_widths_at_once(gbf):
+    """Two threads with two streams each, every kernel and cluster size among them and the static
+    Linears between: tensor memory and shared memory are shared, the results are those of calls alone."""
+    sizes = [(8, 512, 4096), (16, 4096, 1024), (30, 1024, 2048), (32, 8192, 512), (60, 1024, 4096), (120, 512, 2048),
+             (300, 1024, 4096), (700, 2048, 1024)]
+    cases = [(tensors(case(m, n, k, 20 + i)), torch.empty(m, n, dtype=torch.bfloat16, device="cuda"))
+             for i, (m, n, k) in enumerate(sizes)]
+
+    def block_call(i, y, stream=None):
+        gbf.linear_fp8_block(**cases[i][0], y=y, act=2, stream=stream)
+
+    def static_call(i, y, stream=None):
+        t = cases[i][0]
+        gbf.linear_fp8_act(t["xq"], 1e-3, t["wq"], ones[:y.shape[1]], t["bias"], y, act=0, stream=stream)
+
+    ones = torch.ones(8192, device="cuda")
+    calls = [(f, i) for i in range(len(sizes)) for f in (block_call, static_call)]
+    alone = [torch.empty_like(cases[i][1]) for _, i in calls]
+    for (f, i), y in zip(calls, alone):
+        f(i, y)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def worker(seed):
+        try:
+            streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+            ys = [[torch.zeros_like(y) for y in alone] for _ in streams]
+            torch.cuda.synchronize()
+            rng = np.random.default_rng(seed)
+            for _ in range(10):
+                for st, out in zip(streams, ys):
+                    for j in rng.permutation(len(calls)):
+                        f, i = calls[j]
+                        f(i, out[j], st)
+            for st in streams:
+                st.synchronize()
+            wrong.extend((seed, calls[j][0].__name__, sizes[calls[j][1]]) for out in ys for j in range(len(calls))
+                         if not torch.equal(out[j], alone[j]))
+        except Exception as e:  # noqa: BLE001 - the main thread reports it
+            wrong.append((seed, repr(e)))
+
+    threads = [threading.Thread(target=worker, args=(s,)) for s in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
     assert gbf.device_status()[0] == 0
 
 
