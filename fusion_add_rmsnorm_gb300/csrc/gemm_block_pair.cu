@@ -34,9 +34,9 @@
 // in the order of K.
 //
 // mbarrier waits are bounded, as in gemm_tcgen05.cu.  After one that gave up, the
-// producers leave; issuers, relays and epilogue walk on without working, so that
-// the hardware barriers' counts still meet, and all CTAs of a cluster leave
-// together.
+// producers leave; issuers, relays and epilogue walk the rest of their K blocks
+// without working, in step (see wait_taken), so that the hardware barriers' phases
+// still are K blocks, and all CTAs of a cluster leave together.
 #include <atomic>
 
 #include "gemm_block.cuh"
@@ -83,6 +83,7 @@ struct __align__(8) BpCtl {
   uint64_t drain[2];
   uint32_t tmem_base;
   uint32_t peer_issued;                         // even CTA: K blocks whose copies the odd CTA issued
+  uint32_t taken[2];                            // K blocks whose accumulators a half's issuer or relay took back
   int abort;
 };
 
@@ -121,6 +122,18 @@ GBF_DEVICE void bp_origin(const BlockPairParams& p, int odd, int tile, int& m0, 
 constexpr int kBpGivers = (kBpEpilogueWarps / 2 + 1) * 32;
 GBF_DEVICE void give_back(int b) { asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(1 + b), "n"(kBpGivers) : "memory"); }
 GBF_DEVICE void take_back(int b) { asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(1 + b), "n"(kBpGivers) : "memory"); }
+GBF_DEVICE void set_taken(uint32_t* taken, uint32_t blocks) { *reinterpret_cast<volatile uint32_t*>(taken) = blocks; }
+
+// The barrier counts arrivals, whoever they are from, so a warp may not arrive for
+// K block i before block i - 2's phase is over: two arrivals in one phase, and a
+// later phase stays short of one for ever.  While the waits succeed, acc_full says
+// so (block i's MMAs go out behind that phase).  A warp whose wait gave up has only
+// the issuer's (relay's) own count to go by.  That count moves on: every warp
+// arrives for a block, and the issuer's other waits are bounded.
+GBF_DEVICE void wait_taken(const uint32_t* taken, uint32_t blocks) {
+  for (uint32_t i = 0; i < 4 * kWaitMaxPolls && *reinterpret_cast<const volatile uint32_t*>(taken) < blocks; ++i) __nanosleep(256);
+  __syncwarp();
+}
 
 // Arrives on another CTA's mbarrier.  Relaxed: the accumulator's loads have been
 // waited for, so there is nothing to release; a release at cluster scope waits
@@ -259,6 +272,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
       mbar_init(&ctl->scales_empty[b], kBpEpilogueWarps);
     }
     ctl->peer_issued = 0;
+    ctl->taken[0] = ctl->taken[1] = 0;
     ctl->abort = 0;
     mbar_fence_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
@@ -322,6 +336,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
             if (it >= 2) {
               __syncwarp();
               take_back(b);
+              set_taken(&ctl->taken[h], it - 1);
               ok = ok && mbar_wait<false, false>(&ctl->peer_gave[b], ((it >> 1) & 1) ^ 1u, &ctl->abort, p.err);
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -337,7 +352,10 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           }
         }
         __syncwarp();
-        for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) take_back((i & 1) * 2 + h);
+        for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) {
+          take_back((i & 1) * 2 + h);
+          set_taken(&ctl->taken[h], i + 1);
+        }
         if (elected) {
           tc_commit_self<true>(&ctl->drain[h]);
           int own = 0;
@@ -350,6 +368,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           for (int kb = kb_begin; kb < kb_end; ++kb, ++it) {
             take_back((it & 1) * 2 + h);
             if (elected) mbar_arrive_relaxed(peer + (it & 1) * 16);
+            set_taken(&ctl->taken[h], it + 1);
             __syncwarp();
           }
       }
@@ -414,10 +433,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           const float s = s_next;
           if (!ready) ok = ok && mbar_wait<false, false>(&ctl->acc_full[b], (it >> 1) & 1, &ctl->abort, p.err);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            give_back(b);
-            continue;
-          }
+          if (!ok) break;
           tc_fence_after();
           const float2 ss = make_float2(s, s);
           const uint32_t at = taddr + (it & 1) * kBpCols;
@@ -440,9 +456,19 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           s_next = sx[after * kBpChunkRow] * sw[after];
           add_scaled(acc, 96, r1, ss);
         }
+        if (!ok) break;
         // the last chunk goes back once the tile's bias has been read: with one chunk a tile, the
         // next but one's bias takes this one's place
         if (kb0 + kBpChunk < kb_end && lane == 0) mbar_arrive(&ctl->scales_empty[chunk & 1]);
+      }
+      if (!ok) {                                            // a wait gave up: the K blocks of all tiles that are left
+        const uint32_t all = ((tiles - 1 - first) / stride + 1u) * (kb_end - kb_begin);
+        for (; it < all; ++it) {
+          if (it >= 2) wait_taken(&ctl->taken[half], it - 1);
+          give_back((it & 1) * 2 + half);
+        }
+        if (p.split > 1) asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(kBpEpilogueWarps * 32) : "memory");
+        break;
       }
       if (p.split > 1) {
         // One tile a cluster.  The ring is free once both halves' last accumulators have come: they came
@@ -490,7 +516,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           if (c % 8 == 8 - 2) {                            // a box is whole
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && ok && col0 + c / 8 * kBpBoxCols < p.n && row0 < p.m) {
+            if (lane == 0 && col0 + c / 8 * kBpBoxCols < p.n && row0 < p.m) {
               tma_store_2d(&map_y, box + c / 8 * kBpBoxBytes, col0 + c / 8 * kBpBoxCols, row0);
               bulk_commit();
             }
