@@ -24,10 +24,11 @@
 // What bounds it: an accumulator's way round (MMAs, completion, read back, given
 // back in both CTAs), as 512 TMEM columns hold two K blocks.  So that way is kept
 // short: an SM's epilogue gives back through a hardware barrier, not an mbarrier,
-// scales come from shared memory, no wait or arrival in the loop has cluster scope
-// (an acquire there empties L1, a release waits for loads in flight), and the next
-// accumulator is asked about while this one's last columns are added.  8192 x 16384
-// x 4096: 422 us with the tanh GELU, 382 without an activation.
+// scales come from shared memory, nothing in the loop acquires or releases at
+// cluster scope (an acquire there empties L1, a release waits for loads in flight;
+// see mbar_arrive_relaxed), and the next accumulator is asked about while this one's
+// last columns are added.  8192 x 16384 x 4096: 418 us with the tanh GELU, about 400
+// without an activation.
 //
 // CTAs are persistent and walk the tiles.  With few of them, up to four pairs of
 // a cluster cut K, and add their partial sums through distributed shared memory,
@@ -135,11 +136,19 @@ GBF_DEVICE void wait_taken(const uint32_t* taken, uint32_t blocks) {
   __syncwarp();
 }
 
-// Arrives on another CTA's mbarrier.  Relaxed: the accumulator's loads have been
-// waited for, so there is nothing to release; a release at cluster scope waits
-// for every load in flight, over a thousand cycles a K block.
+// An accumulator goes from CTA to CTA: the odd one's relay arrives on the even one's
+// mbarrier, and the even one's commit on the odd one's.  What goes over is tensor
+// memory alone, so arrival and wait are relaxed, at the scope that holds both CTAs,
+// and the order is the tcgen05 fences': loads waited for, before_thread_sync, the
+// half's hardware barrier, after_ and before_thread_sync in the relay, this arrival,
+// wait_accumulator, after_thread_sync, the MMAs that write it again.  With a
+// release and an acquire instead 8192 x 16384 x 4096 takes 741 us, not 418.
 GBF_DEVICE void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+GBF_DEVICE bool wait_accumulator(uint64_t* bar, uint32_t parity, int* abort, unsigned int* err) {
+  return mbar_wait<true, false, true>(bar, parity, abort, err);
 }
 
 // Arrives on `bar` of both CTAs of the pair whose even one this is, once the
@@ -201,10 +210,10 @@ GBF_DEVICE void tmem_ld_wait(uint32_t (&r)[32]) {
                  "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// Whether the phase of `bar` with this parity is over, without waiting.
-GBF_DEVICE uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+// Whether an accumulator's phase with this parity is over, without waiting.
+GBF_DEVICE uint32_t test_accumulator(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok;
 }
 GBF_DEVICE void add_scaled(float (&acc)[kBpWarpCols], int at, const uint32_t (&r)[32], float2 s) {
@@ -337,7 +346,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
               __syncwarp();
               take_back(b);
               set_taken(&ctl->taken[h], it - 1);
-              ok = ok && mbar_wait<false, false>(&ctl->peer_gave[b], ((it >> 1) & 1) ^ 1u, &ctl->abort, p.err);
+              ok = ok && wait_accumulator(&ctl->peer_gave[b], ((it >> 1) & 1) ^ 1u, &ctl->abort, p.err);
             }
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
@@ -367,6 +376,8 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         for (int tile = first; tile < tiles; tile += stride)
           for (int kb = kb_begin; kb < kb_end; ++kb, ++it) {
             take_back((it & 1) * 2 + h);
+            tc_fence_after();
+            tc_fence_before();
             if (elected) mbar_arrive_relaxed(peer + (it & 1) * 16);
             set_taken(&ctl->taken[h], it + 1);
             __syncwarp();
@@ -431,7 +442,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         for (int kb = 0; kb < end; ++kb, ++it) {
           const uint32_t b = (it & 1) * 2 + half;
           const float s = s_next;
-          if (!ready) ok = ok && mbar_wait<false, false>(&ctl->acc_full[b], (it >> 1) & 1, &ctl->abort, p.err);
+          if (!ready) ok = ok && wait_accumulator(&ctl->acc_full[b], (it >> 1) & 1, &ctl->abort, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -451,7 +462,7 @@ linear_block_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
           tmem_ld_wait(r1);
           tc_fence_before();
           give_back(b);
-          ready = mbar_test(&ctl->acc_full[b ^ 2], ((it + 1) >> 1) & 1);
+          ready = test_accumulator(&ctl->acc_full[b ^ 2], ((it + 1) >> 1) & 1);
           const int after = min(kb + 1, end - 1);           // the next one's scale, ahead of its wait
           s_next = sx[after * kBpChunkRow] * sw[after];
           add_scaled(acc, 96, r1, ss);

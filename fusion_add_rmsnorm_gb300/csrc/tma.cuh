@@ -54,6 +54,10 @@ GBF_DEVICE void mbar_arrive(uint64_t* bar) {
 
 // CLUSTER: acquire at cluster scope, for a barrier that threads of another
 // CTA of the cluster arrive on (their arrive releases at cluster scope).
+// RELAXED (with CLUSTER): that scope without the acquire, for a barrier whose phase
+// hands over tensor memory alone: tcgen05.fence::before_thread_sync in front of the
+// arrival and ::after_thread_sync behind the wait order the tcgen05 operations, and
+// no other memory is handed over.
 // HINT: the form with an explicit suspend-time hint, whose wake-up after the
 // phase completes is prompter than the form without one (measured: ~5 % on
 // the tcgen05 GEMM when its MMA issuer waits on TMA-filled stages this way).
@@ -65,10 +69,13 @@ constexpr uint32_t kSuspendHintNs = 64;
                : "=r"(ok)                                                   \
                : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendHintNs)       \
                : "memory")
-template <bool CLUSTER = false, bool HINT = false>
+template <bool CLUSTER = false, bool HINT = false, bool RELAXED = false>
 GBF_DEVICE bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+  static_assert(!RELAXED || (CLUSTER && HINT), "the relaxed form is at cluster scope, with the hint");
   uint32_t ok;
-  if (CLUSTER && HINT)
+  if (RELAXED)
+    GBF_TRY_WAIT_ASM(".relaxed.cluster", ", %3");
+  else if (CLUSTER && HINT)
     GBF_TRY_WAIT_ASM(".acquire.cluster", ", %3");
   else if (CLUSTER)
     GBF_TRY_WAIT_ASM(".acquire.cluster", "");
@@ -90,13 +97,13 @@ GBF_DEVICE bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // the critical path (mbarrier.try_wait itself suspends the thread until the
 // phase completes or the hinted time passes, so the loop issues few
 // instructions).
-template <bool CLUSTER = false, bool SLEEP = true>
+template <bool CLUSTER = false, bool SLEEP = true, bool RELAXED = false>
 GBF_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned int* err) {
-  if (mbar_try_wait<CLUSTER, !SLEEP>(bar, parity)) return true;
+  if (mbar_try_wait<CLUSTER, !SLEEP, RELAXED>(bar, parity)) return true;
   const uint64_t t0 = global_timer();
   uint32_t sleep_ns = 32;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait<CLUSTER, !SLEEP>(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER, !SLEEP, RELAXED>(bar, parity)) return true;
     // back off so a waiting thread does not flood the issue slots of the
     // threads doing the work (at most ~0.25 us of extra wake-up latency)
     if (SLEEP && i > 4) {

@@ -82,3 +82,17 @@ def test_the_kernel_keeps_that_order():
     assert "if (!ok) break;" in epilogue[:arrivals[0]]
     taken = re.findall(r"^ +(take_back|set_taken)\(", text, re.M)
     assert taken == ["take_back", "set_taken", "take_back", "set_taken", "take_back", "set_taken"]
+
+
+def test_accumulators_change_hands_at_cluster_scope():
+    """The barriers of an accumulator, which the pair's other CTA arrives on, are waited for at
+    the scope that holds both CTAs, between the fences that order tensor memory."""
+    read = lambda name: open(os.path.join(ROOT, "fusion_add_rmsnorm_gb300", "csrc", name)).read()    # noqa: E731
+    text = read("gemm_block_pair.cu")
+    waits = re.findall(r"(\w+)(?:<[\w, ]*>)?\(&ctl->(acc_full|peer_gave)\[", text)
+    waits = {(f, bar) for f, bar in waits if f not in ("mbar_init", "commit_pair", "smem_u32")}
+    assert waits == {("wait_accumulator", "acc_full"), ("wait_accumulator", "peer_gave"), ("test_accumulator", "acc_full")}
+    assert "mbar_wait<true, false, true>" in text and "mbarrier.test_wait.parity.relaxed.cluster" in text
+    assert '".relaxed.cluster"' in read("tma.cuh") and "mbarrier.arrive.relaxed.cluster" in text
+    relay = text[text.index("-- relay"):text.index("-- scales")]
+    assert re.search(r"take_back\(.*?tc_fence_after\(\);\s+tc_fence_before\(\);\s+if \(elected\) mbar_arrive_relaxed", relay, re.S)
