@@ -709,8 +709,9 @@ GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint
   // the kernels index rows, columns, tiles and TMA coordinates with int32
   const int64_t lim = 1LL << 31;
   if (M >= lim || N >= lim || K >= lim) return fail(GBF_EUNSUPPORTED, "%s: M, N and K must be below 2^31", fn);
-  if (gbf::block_count(M) * gbf::block_count(N) >= lim)
-    return fail(GBF_EUNSUPPORTED, "%s: more than 2^31 - 1 output tiles of 128 x 128", fn);
+  // of the tiles that a call of many rows may be cut into the smallest; K is cut only where they are few
+  if ((M + 63) / 64 * gbf::block_count(N) >= lim)
+    return fail(GBF_EUNSUPPORTED, "%s: more than 2^31 - 1 output tiles of 64 x 128", fn);
   if (M == 0) return ok();
   if (!Xq || !x_scales || !Wq || !w_scales || !Y)
     return fail(GBF_EINVAL, "%s: Xq, x_scales, Wq, w_scales, Y are required", fn);

@@ -5,10 +5,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-namespace gbf {
+#include "block_plan.h"
 
-constexpr int kBlockCols = 128;           // columns that share a scale (and rows, in a weight)
-constexpr int64_t block_count(int64_t n) { return (n + kBlockCols - 1) / kBlockCols; }
+namespace gbf {
 
 // ------------------------------------- add + RMSNorm + block-scaled FP8
 struct AddRmsNormBlockArgs {
@@ -58,7 +57,10 @@ struct LinearBlockArgs {
 };
 
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
-cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
-int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k);       // about how long that takes
+cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, const LinearBlockPlan& plan, int clusters,
+                                     cudaStream_t stream, const char** why);
+// Clusters of 1 to kBpMaxSplit pairs that fit on the current device at once (0 where it
+// does not say); raises the pair kernel's shared memory limit.
+void linear_block_clusters(int (&clusters)[kBpMaxSplit + 1]);
 
 }  // namespace gbf

@@ -38,7 +38,6 @@ namespace {
 
 constexpr int kLbRows = 128;              // W rows of a tile: one scale block
 constexpr int kLbEpilogue = 4;            // first epilogue warp
-constexpr int kLbMaxSplit = 8;            // portable cluster size
 
 constexpr int kLbChunk = 8;               // K blocks whose scales are filled at a time
 
@@ -326,29 +325,6 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
-// K is cut while every CTA still has an SM to itself (the next call's may then
-// come beside it) and keeps four blocks.
-int split_of(int64_t tiles, int blocks, int sms) {
-  int split = 1;
-  while (split < kLbMaxSplit && tiles * split * 2 <= sms && blocks >= split * 2 * 4) split *= 2;
-  return split;
-}
-
-// About how long this kernel takes with NX = 64 or 128, which with
-// linear_block_pair_ns() decides who takes a call of more than 32 rows.
-// Measured: a K block of a tile 270 or 335 ns, its start and end 2.2 us, joining
-// a cluster's sums 1.5 or 3 us more.  The estimates against the measured times
-// (us; 64 rows a tile, 128, pairs), N x K = 4096 x 4096: 128 rows 8.0 / 9.0, 7.9 /
-// 9.1, 14.3 / 16; 512 rows 21.7 / 21.4, 12.9 / 13.3, 17.4 / 18; 1024 rows 43.4 / 46,
-// 25.8 / 26, 19.7 / 19.3.  16384 x 4096, 256 rows: 43.4 / 44, 25.8 / 27.6, 19.7 / 21.9.
-// 4096 x 11008, 333 rows: 50.8 / 47, 31.0 / 29.7, 28.0 / 28.0.
-int64_t thin_ns(int64_t m, int nx, const LinearBlockParams& p, int sms) {
-  const int64_t tiles = (m + nx - 1) / nx * p.n_tiles, waves = (tiles + sms - 1) / sms;
-  const int split = split_of(tiles, p.blocks, sms);
-  return waves * (2200 + (p.blocks + split - 1) / split * (nx == 64 ? 270 : 335)) +
-         (split > 1 ? (nx == 64 ? 1500 : 3000) : 0);
-}
-
 template <int NX, bool SPLIT>
 cudaError_t launch_split(const LinearBlockArgs& a, const LinearBlockParams& p, cudaStream_t stream, const char** why) {
   CUtensorMap map_x, map_w;
@@ -363,7 +339,7 @@ cudaError_t launch_split(const LinearBlockArgs& a, const LinearBlockParams& p, c
     return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.m_tiles) * p.n_tiles * p.split);
   cfg.blockDim = dim3(Lb<NX, SPLIT>::kThreads);
   cfg.dynamicSmemBytes = lb_smem<NX, SPLIT>();
   cfg.stream = stream;
@@ -380,18 +356,20 @@ cudaError_t launch_split(const LinearBlockArgs& a, const LinearBlockParams& p, c
 }
 
 template <int NX>
-cudaError_t launch_lb(const LinearBlockArgs& a, LinearBlockParams p, int sms, cudaStream_t stream, const char** why) {
-  p.m_tiles = static_cast<int>((a.m + NX - 1) / NX);
-  p.split = split_of(static_cast<int64_t>(p.m_tiles) * p.n_tiles, p.blocks, sms);
+cudaError_t launch_lb(const LinearBlockArgs& a, const LinearBlockParams& p, cudaStream_t stream, const char** why) {
   return p.split > 1 ? launch_split<NX, true>(a, p, stream, why) : launch_split<NX, false>(a, p, stream, why);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
-  int dev = 0, sms = 0;
+  LinearBlockRoom room = {};
+  int dev = 0;
   cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaDeviceGetAttribute(&room.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (a.m > 32) linear_block_clusters(room.clusters);
+  const LinearBlockPlan plan = plan_linear_block(a.m, a.n, a.k, room);
+  if (plan.rows == kBpTile) return launch_linear_block_pair(a, plan, room.clusters[plan.split], stream, why);
   LinearBlockParams p = {};
   p.x_scales = a.x_scales;
   p.w_scales = a.w_scales;
@@ -401,13 +379,16 @@ cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, c
   p.m = static_cast<int>(a.m);
   p.n = static_cast<int>(a.n);
   p.blocks = static_cast<int>(block_count(a.k));
+  p.m_tiles = static_cast<int>((a.m + plan.rows - 1) / plan.rows);
   p.n_tiles = static_cast<int>(block_count(a.n));
+  p.split = plan.split;
   p.act = a.act;
-  if (a.m <= 16) return launch_lb<16>(a, p, sms, stream, why);
-  if (a.m <= 32) return launch_lb<32>(a, p, sms, stream, why);
-  const int64_t t64 = thin_ns(a.m, 64, p, sms), t128 = thin_ns(a.m, 128, p, sms), tp = linear_block_pair_ns(a.m, a.n, a.k);
-  if (tp < t64 && tp < t128) return launch_linear_block_pair(a, stream, why);
-  return t64 <= t128 ? launch_lb<64>(a, p, sms, stream, why) : launch_lb<128>(a, p, sms, stream, why);
+  switch (plan.rows) {
+    case 16: return launch_lb<16>(a, p, stream, why);
+    case 32: return launch_lb<32>(a, p, stream, why);
+    case 64: return launch_lb<64>(a, p, stream, why);
+    default: return launch_lb<128>(a, p, stream, why);
+  }
 }
 
 }  // namespace gbf

@@ -46,15 +46,14 @@ namespace gbf {
 namespace {
 
 constexpr int kBpThreads = 384;
-constexpr int kBpRows = 128;                    // X rows of a CTA
-constexpr int kBpCols = 256;                    // channels of a pair's tile
+constexpr int kBpRows = kBpTile / 2;            // X rows of a CTA
+constexpr int kBpCols = kBpTile;                // channels of a pair's tile
 constexpr int kBpHalf = kBpCols / 2;
 constexpr int kBpStages = 4;
 constexpr int kBpStageBytes = (kBpRows + kBpHalf) * BK_BYTES;
 constexpr int kBpEpilogue = 4;                  // first epilogue warp
 constexpr int kBpEpilogueWarps = 8;
 constexpr int kBpWarpCols = 128;                // channels of an epilogue warp: a half
-constexpr int kBpMaxSplit = 4;                  // pairs of a portable cluster
 constexpr int kBpBoxCols = 64;                  // an epilogue warp's stores: 32 rows x 64 columns of bf16
 constexpr int kBpBoxBytes = 32 * kBpBoxCols * 2;
 // Scales of 16 K blocks, one copy in use and one being filled: X's as
@@ -626,29 +625,15 @@ cudaError_t resident_clusters(int split, int* clusters) {
   return cudaSuccess;
 }
 
-// K is cut while all tiles' clusters fit the GPU at once and each pair keeps six blocks.
-cudaError_t split_of(int64_t tiles, int blocks, int* split, int* fit) {
-  for (*split = kBpMaxSplit; *split >= 1; --*split) {
-    if (*split > 1 && blocks < *split * 6) continue;
-    const cudaError_t e = resident_clusters(*split, fit);
-    if (e != cudaSuccess || *split == 1 || tiles <= *fit) return e;
-  }
-  return cudaSuccess;
-}
-
 }  // namespace
 
-// About how long a call takes here (measured: a K block 390 ns, a tile's end 2.2 us,
-// the call's start and end 5 us, joining a cluster's sums 4 us more; see gemm_block.cu).
-int64_t linear_block_pair_ns(int64_t m, int64_t n, int64_t k) {
-  const int64_t tiles = (m + 2 * kBpRows - 1) / (2 * kBpRows) * ((n + kBpCols - 1) / kBpCols);
-  const int blocks = static_cast<int>(block_count(k));
-  int split = 1, fit = 0;
-  if (split_of(tiles, blocks, &split, &fit) != cudaSuccess || fit < 1) return INT64_MAX;
-  return (tiles + fit - 1) / fit * ((blocks + split - 1) / split * 390 + 2200) + 5000 + (split > 1 ? 4000 : 0);
+void linear_block_clusters(int (&clusters)[kBpMaxSplit + 1]) {
+  for (int split = 1; split <= kBpMaxSplit; ++split)
+    if (resident_clusters(split, &clusters[split]) != cudaSuccess) clusters[split] = 0;
 }
 
-cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
+cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, const LinearBlockPlan& plan, int fit, cudaStream_t stream,
+                                     const char** why) {
   CUtensorMap map_x, map_w, map_y;
   if (!make_map(&map_x, a.x, a.m, a.k, kBpRows, true) || !make_map(&map_w, a.w, a.n, a.k, kBpHalf / 2, true) ||
       !make_map(&map_y, a.y, a.m, a.n, 32, false)) {
@@ -666,15 +651,9 @@ cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, cudaStream_t stre
   p.blocks = static_cast<int>(block_count(a.k));
   p.m_units = static_cast<int>((a.m + 2 * kBpRows - 1) / (2 * kBpRows));
   p.n_tiles = static_cast<int>((a.n + kBpCols - 1) / kBpCols);
+  p.split = plan.split;
   p.act = a.act;
-  const int64_t tiles = static_cast<int64_t>(p.m_units) * p.n_tiles;
-  int fit = 0;
-  const cudaError_t e = split_of(tiles, p.blocks, &p.split, &fit);
-  if (e != cudaSuccess) {
-    *why = "could not reserve shared memory";
-    return e;
-  }
-  const int clusters = static_cast<int>(tiles < fit ? tiles : fit);
+  const int clusters = static_cast<int>(plan.tiles < fit ? plan.tiles : fit);
   // as in gemm_tcgen05.cu: the divisor of the clusters at work nearest 16 within 12..24
   p.group_n = 16;
   for (int d = 0; d <= 8; ++d) {

@@ -83,9 +83,9 @@ GBF_API int gbfb_quantize_fp8(const void* x, uint8_t* q_out, float* scales, int6
  * Wq: device uint8 E4M3 codes [N, K] (nn.Linear [out, in] layout); w_scales:
  * device float32 [ceil(N / 128), ceil(K / 128)]; bias: device bf16 [N] or NULL;
  * Y: device bf16 [M, N]; act as gbf_linear_bias_gelu.  Requires K % 16 == 0,
- * N % 8 == 0, 16-byte aligned Xq, Wq, Y, bias (scales: 4-byte) and M, N, K below
- * 2^31; Y may not overlap an input.  M == 0 enqueues nothing.  Waits are bounded
- * as in gbf_linear_bias_gelu.
+ * N % 8 == 0, 16-byte aligned Xq, Wq, Y, bias (scales: 4-byte), M, N, K below 2^31
+ * and fewer than 2^31 tiles of 64 x 128 of Y; Y may not overlap an input.  M == 0
+ * enqueues nothing.  Waits are bounded as in gbf_linear_bias_gelu.
  */
 GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales,
                             const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int act, void* stream);
