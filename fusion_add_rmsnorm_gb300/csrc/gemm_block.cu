@@ -365,8 +365,9 @@ cudaError_t launch_lb(const LinearBlockArgs& a, const LinearBlockParams& p, cuda
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
   LinearBlockRoom room = {};
   int dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&room.sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&room.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   if (a.m > 32) linear_block_clusters(room.clusters);
   const LinearBlockPlan plan = plan_linear_block(a.m, a.n, a.k, room);
   if (plan.rows == kBpTile) return launch_linear_block_pair(a, plan, room.clusters[plan.split], stream, why);
