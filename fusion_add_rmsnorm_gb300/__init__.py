@@ -72,6 +72,7 @@ _SIGNATURES_BLOCK = {
     "gbfb_gated_act_fp8": [_p, _p, _p, _i64, _i64, _i32, _p],
     "gbfb_quantize_fp8": [_p, _p, _p, _i64, _i64, _i32, _p],
     "gbfb_linear_fp8": [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p],
+    "gbfb_linear_fp8_plan": [_i64, _i64, _i64, ctypes.POINTER(_i32), ctypes.POINTER(_i32)],
 }
 _RESTYPES = {"gbf_last_error": ctypes.c_char_p, "gbfd_paged_attention_workspace": _i64}
 for _name, _args in {**_SIGNATURES, **_SIGNATURES_DECODE, **_SIGNATURES_BLOCK}.items():
@@ -317,6 +318,14 @@ def paged_attention_workspace(n_q_heads, n_kv_heads, head_dim):
     if n <= 0:
         raise ValueError(f"heads not supported: {n_q_heads} query, {n_kv_heads} KV, head_dim {head_dim}")
     return n
+
+
+def linear_fp8_block_plan(m, n, k):
+    """gbfb_linear_fp8_plan: (rows of a tile, CTAs or pairs that cut K) of a linear_fp8_block call of these sizes;
+    256 rows are CTA pairs."""
+    tile_rows, split = _i32(), _i32()
+    _check(_lib.gbfb_linear_fp8_plan(m, n, k, ctypes.byref(tile_rows), ctypes.byref(split)))
+    return tile_rows.value, split.value
 
 
 def copy(src, dst, nbytes=None, stream=None):

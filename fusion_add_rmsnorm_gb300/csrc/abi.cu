@@ -697,12 +697,11 @@ GBF_API int gbfb_quantize_fp8(const void* x, uint8_t* q_out, float* scales, int6
   return quant_entry(fn, x, q_out, scales, rows, d, GBF_ACT_NONE, block_rows, stream);
 }
 
-GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales,
-                            const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int act, void* stream) {
-  const char* fn = "gbfb_linear_fp8";
+namespace {
+
+// Sizes of a block-scaled Linear.
+int linear_block_sizes(const char* fn, int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0) return fail(GBF_EINVAL, "%s: M >= 0, N > 0, K > 0 required", fn);
-  if (act != GBF_ACT_NONE && act != GBF_ACT_GELU_TANH && act != GBF_ACT_GELU_ERF && act != GBF_ACT_SILU)
-    return fail(GBF_EINVAL, "%s: unknown activation %d", fn, act);
   if (K % 16 != 0 || N % 8 != 0)
     return fail(GBF_EUNSUPPORTED, "%s: needs K %% 16 == 0 and N %% 8 == 0 (K=%lld, N=%lld)", fn, (long long)K,
                 (long long)N);
@@ -712,6 +711,18 @@ GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint
   // of the tiles that a call of many rows may be cut into the smallest; K is cut only where they are few
   if ((M + 63) / 64 * gbf::block_count(N) >= lim)
     return fail(GBF_EUNSUPPORTED, "%s: more than 2^31 - 1 output tiles of 64 x 128", fn);
+  return GBF_OK;
+}
+
+}  // namespace
+
+GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales,
+                            const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int act, void* stream) {
+  const char* fn = "gbfb_linear_fp8";
+  if (act != GBF_ACT_NONE && act != GBF_ACT_GELU_TANH && act != GBF_ACT_GELU_ERF && act != GBF_ACT_SILU)
+    return fail(GBF_EINVAL, "%s: unknown activation %d", fn, act);
+  const int bad = linear_block_sizes(fn, M, N, K);
+  if (bad != GBF_OK) return bad;
   if (M == 0) return ok();
   if (!Xq || !x_scales || !Wq || !w_scales || !Y)
     return fail(GBF_EINVAL, "%s: Xq, x_scales, Wq, w_scales, Y are required", fn);
@@ -738,6 +749,22 @@ GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint
   cudaError_t e = gbf::launch_linear_block(a, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess && why) return fail(GBF_ELAUNCH, "%s: %s (%s)", fn, why, cudaGetErrorString(e));
   return launch_status(e, fn);
+}
+
+GBF_API int gbfb_linear_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile_rows, int* split) {
+  const char* fn = "gbfb_linear_fp8_plan";
+  const int bad = linear_block_sizes(fn, M, N, K);
+  if (bad != GBF_OK) return bad;
+  if (!tile_rows || !split) return fail(GBF_EINVAL, "%s: tile_rows and split are required", fn);
+  gbf::LinearBlockPlan plan = {};
+  gbf::LinearBlockRoom room;
+  if (M > 0) {
+    const cudaError_t e = gbf::linear_block_plan(M, N, K, &plan, &room);
+    if (e != cudaSuccess) return fail(GBF_ELAUNCH, "%s: %s", fn, cudaGetErrorString(e));
+  }
+  *tile_rows = plan.rows;
+  *split = plan.split;
+  return ok();
 }
 
 // ------------------------------------------------------------- copy probe

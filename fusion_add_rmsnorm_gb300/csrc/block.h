@@ -56,6 +56,8 @@ struct LinearBlockArgs {
   int act;
 };
 
+// What a call of these sizes (m > 0) launches on the current device.
+cudaError_t linear_block_plan(int64_t m, int64_t n, int64_t k, LinearBlockPlan* plan, LinearBlockRoom* room);
 cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why);
 cudaError_t launch_linear_block_pair(const LinearBlockArgs& a, const LinearBlockPlan& plan, int clusters,
                                      cudaStream_t stream, const char** why);

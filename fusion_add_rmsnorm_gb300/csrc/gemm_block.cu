@@ -362,14 +362,22 @@ cudaError_t launch_lb(const LinearBlockArgs& a, const LinearBlockParams& p, cuda
 
 }  // namespace
 
-cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
-  LinearBlockRoom room = {};
+cudaError_t linear_block_plan(int64_t m, int64_t n, int64_t k, LinearBlockPlan* plan, LinearBlockRoom* room) {
   int dev = 0;
+  *room = {};
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&room.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&room->sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (a.m > 32) linear_block_clusters(room.clusters);
-  const LinearBlockPlan plan = plan_linear_block(a.m, a.n, a.k, room);
+  if (m > 32) linear_block_clusters(room->clusters);
+  *plan = plan_linear_block(m, n, k, *room);
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_block(const LinearBlockArgs& a, cudaStream_t stream, const char** why) {
+  LinearBlockPlan plan;
+  LinearBlockRoom room;
+  const cudaError_t e = linear_block_plan(a.m, a.n, a.k, &plan, &room);
+  if (e != cudaSuccess) return e;
   if (plan.rows == kBpTile) return launch_linear_block_pair(a, plan, room.clusters[plan.split], stream, why);
   LinearBlockParams p = {};
   p.x_scales = a.x_scales;

@@ -90,6 +90,14 @@ GBF_API int gbfb_quantize_fp8(const void* x, uint8_t* q_out, float* scales, int6
 GBF_API int gbfb_linear_fp8(const uint8_t* Xq, const float* x_scales, const uint8_t* Wq, const float* w_scales,
                             const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int act, void* stream);
 
+/*
+ * gbfb_linear_fp8_plan -- what a gbfb_linear_fp8 call of these sizes launches on the
+ * current device: *tile_rows 16, 32, 64 or 128 (single CTAs, that many rows of X a
+ * tile) or 256 (CTA pairs), *split CTAs (pairs) of a cluster that cut K; both 0 for
+ * M == 0.  For tests and tuning; enqueues nothing.
+ */
+GBF_API int gbfb_linear_fp8_plan(int64_t M, int64_t N, int64_t K, int* tile_rows, int* split);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,7 @@ int main() {
   }
 }
 """
-GB300 = (152, 76, 36, 22, 16)          # SMs; clusters of one to four pairs
+GB300 = (152, 76, 36, 22, 16)          # SMs; clusters of one to four pairs (the larger ones fit a few fewer on some GPUs)
 
 
 @pytest.fixture(scope="module")
@@ -102,3 +102,12 @@ def test_tiles_past_the_grid_are_refused(gbf):                                  
     names = [("x", A(0)), ("sx", A(1 << 20)), ("w", A(2 << 20)), ("sw", A(3 << 20)), ("bias", None), ("y", A(4 << 20)),
              ("m", (1 << 31) - 1), ("n", 12800), ("k", 16), ("act", 0), ("stream", None)]
     assert call(gbf.raw().gbfb_linear_fp8, names, {}) == gbf.EUNSUPPORTED and "64 x 128" in last(gbf)
+
+
+def test_the_librarys_answer(gbf):                                                    # noqa: F811
+    plan = gbf.linear_fp8_block_plan
+    assert plan(0, 64, 256) == (0, 0)
+    for bad in ((-1, 64, 256), (4, 0, 256), (4, 64, 0), (4, 60, 256), (4, 64, 136), (1 << 31, 64, 256)):
+        with pytest.raises(gbf.GbfError):
+            plan(*bad)
+    assert gbf.raw().gbfb_linear_fp8_plan(4, 64, 256, None, None) == gbf.EINVAL
