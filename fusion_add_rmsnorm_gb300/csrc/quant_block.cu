@@ -24,7 +24,9 @@ namespace {
 constexpr int kQbThreads = 256;
 constexpr int kQbGroups = kQbThreads / kSegLanes;
 
-// act(g) in float32.  The scale is a float32 that the activation's error reaches,
+// act(g) in float32, to (10 + 4 |z|) 2^-23 of itself, z the logistic function's
+// argument, or (10 + g^2) 2^-23 (erf): the exponential's argument is rounded, and its
+// error grows with it.  The scale is a float32 that the activation's error reaches,
 // so neither the 11-bit hardware tanh nor an approximation with an absolute error
 // only is used here.  SiLU and the tanh GELU are g times the logistic function of
 // g, or of 2u with the GELU's inner polynomial u, by the exponential of a negative

@@ -52,7 +52,9 @@ GBF_API int gbfb_add_rmsnorm_fp8(const void* x, const void* res_in, void* res_ou
  * gbfb_gated_act_fp8 -- the codes and scales of y = act(gate) * up, which
  * gbf_gated_act writes as bf16: x is device bf16 [rows, 2d], gate then up; act is
  * GBF_ACT_SILU, GBF_ACT_GELU_TANH or GBF_ACT_GELU_ERF.  y is float32 (an
- * act(gate) below float32's normal range may count as zero) and never reaches
+ * act(gate) below float32's normal range may count as zero), off by at most
+ * (10 + 4 |z|) 2^-23 of itself (z the argument of the logistic function that SiLU
+ * and the tanh GELU multiply by) or (10 + gate^2) 2^-23 (erf GELU), and never reaches
  * memory.  q_out: device uint8 [rows, d]; scales: device float32
  * [rows, ceil(d / 128)].  Requires d % 16 == 0 and 16-byte aligned x, q_out.
  */
@@ -78,6 +80,16 @@ GBF_API int gbfb_quantize_fp8(const void* x, uint8_t* q_out, float* scales, int6
  * The sum over a block of 128 k is the tensor core's, in float32; the product of
  * the two scales, its product with the block's sum and the sum over blocks are
  * float32, in registers; one bf16 rounding.  Scales may be any numbers.
+ *
+ * act is gbf_linear_bias_gelu's, evaluated as there, by forms for an epilogue whose
+ * errors, in front of the rounding, are below
+ *   GELU_TANH  |a| 2^-11.9 (the hardware's tanh, relative error 2^-10.9)
+ *   GELU_ERF   |a| 2^-21   (an erf with an absolute error of 1.5e-7)
+ *   SILU       |act(a)| (8 + 2 |a|) 2^-23
+ * so a GELU's value at a strongly negative a, small beside |a|, is right to these
+ * bounds only and not to a bf16 rounding of itself.  Over all bf16 a, what was seen
+ * beyond one bf16 rounding is below |a| 2^-20 and |a| 2^-26: at a = -3 both are
+ * within a rounding, at a = -5 the tanh GELU gives 0 for -2.3e-7.
  *
  * Xq: device uint8 E4M3 codes [M, K]; x_scales: device float32 [M, ceil(K / 128)];
  * Wq: device uint8 E4M3 codes [N, K] (nn.Linear [out, in] layout); w_scales:

@@ -8,7 +8,6 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import block
 from oracle.formats import bf16_decode, bf16_encode
 from parity import from_bits, to_bits
 from test_parity_block_linear import case, check, run, tensors
