@@ -51,8 +51,9 @@ PyObject* gated_act_fp8_block(PyObject*, PyObject* const* args, Py_ssize_t nargs
     const at::Tensor &x = tensor(v.at[0], names[0]), &q = tensor(v.at[1], names[1]);
     const int d = device_of(x);
     const auto [rows, width] = folded(q);
-    if (x.numel() && x.size(-1) != 2 * width)
-      raise(PyExc_ValueError, "x: rows of %lld values, expected 2 * %lld", static_cast<long long>(x.size(-1)),
+    const int64_t given = folded(x).width;
+    if (x.numel() && given != 2 * width)
+      raise(PyExc_ValueError, "x: rows of %lld values, expected 2 * %lld", static_cast<long long>(given),
             static_cast<long long>(width));
     const void* xp = operand(v.at[0], 2 * rows * width, at::kBFloat16, names[0], d);
     void* qp = operand(v.at[1], rows * width, at::kByte, names[1], d);
