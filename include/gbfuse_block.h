@@ -10,7 +10,8 @@
  * `stream` without synchronising, gbf_status return values with gbf_last_error()
  * for the message.  No call keeps state between calls or needs a workspace;
  * every call may be captured into a CUDA graph, allows programmatic dependent
- * launch, and gives the same bits whenever it is given the same inputs.
+ * launch, and gives the same bits whenever it is given the same inputs (on one GPU:
+ * how the Linear cuts K goes by how many clusters a GPU holds at once).
  *
  * A block's scale and codes, in binary32:
  *   scale = max(RN(amax * RN(1 / 448)), 2^-100)      amax = the block's largest |y|
