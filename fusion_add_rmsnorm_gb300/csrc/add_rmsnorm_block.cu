@@ -45,6 +45,8 @@ GBF_DEVICE uint4 residual(uint4 g, uint4 x, uint4 r) {
 // are read from L1 where they are used (16384 x 8192 gated AdaRMSNorm: 149 us, held
 // and spilled 181).  CTAS: an SM's at one block a lane group, three for streaming
 // (32768 x 4096: 143 us, two 150), two for fewer rows (777 x 2736: 3.8 us, three 4.4).
+// What four cost above 16,384 columns, against a floor of 141: 4096 x 32768 weighted
+// 172 us, gated AdaRMSNorm 222 (8192 x 16384 weighted, two blocks: 143).
 template <int MODE, bool GATED, int NS, int CTAS>
 __global__ void __launch_bounds__(NS == 1 ? kNbThreads / 2 : kNbThreads, CTAS)
 add_rmsnorm_block_kernel(const AddRmsNormBlockArgs a) {

@@ -27,8 +27,8 @@
 // scales come from shared memory, nothing in the loop acquires or releases at
 // cluster scope (an acquire there empties L1, a release waits for loads in flight;
 // see mbar_arrive_relaxed), and the next accumulator is asked about while this one's
-// last columns are added.  8192 x 16384 x 4096: 418 to 426 us with the tanh GELU by
-// box (461 in a run of eager calls), 390 to 410 without an activation.
+// last columns are added.  8192 x 16384 x 4096: 418 to 426 us with the tanh GELU on
+// several GPUs (461 in a run of eager calls), 390 to 410 without an activation.
 //
 // CTAs are persistent and walk the tiles.  With few of them, up to four pairs of
 // a cluster cut K, and add their partial sums through distributed shared memory,
